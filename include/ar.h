@@ -459,6 +459,218 @@ const char* ar_get_last_error_detail(void);
 /* Size in bytes of one element of `dtype`, 0 if unknown. */
 size_t ar_dtype_size(ar_dtype_t dtype);
 
+/* ------------------------------------------------------------------------
+ * Operators of the training step around the gradient reduction
+ *
+ * A data-parallel step reduces its gradients over the ranks with the calls
+ * above.  The calls below are what runs next to that reduction: the global
+ * norm of the reduced gradients (for clipping), the AdamW update of the
+ * parameters, and layer norm, whose weight gradient is a sum over every token
+ * of every rank, over a rank's own tokens in its backward pass and over the
+ * ranks in the AllReduce.
+ *
+ * The rules are those of the collectives: host arrays of device pointers,
+ * read during the call only; buffers owned by the caller, aligned to their
+ * element size (vector loads and stores need no more); validation before
+ * anything is enqueued; work enqueued on `stream`, asynchronously; no device
+ * memory allocated.  Element types are AR_FLOAT32, AR_BFLOAT16 and
+ * AR_FLOAT16; sums, statistics and states are kept in float32 or float64 and
+ * each output is rounded once.  The results are the same bits in every run:
+ * no sum's order depends on which workgroup finishes first.
+ * ------------------------------------------------------------------------ */
+
+/* Most tensors in one call or plan, and most tiles (about 2^11 to 2^13
+ * elements each) that their elements may take. */
+#define AR_MAX_TENSORS 65536
+
+/* Global 2-norm of `ntensors` gradients: *norm (device memory) receives
+ * sqrt(sum over all elements of g^2), summed in float64 and rounded once to
+ * float32.  A NaN or infinity among the elements makes it NaN or infinity.
+ * No tensors, or only empty ones: 0.  grads[t] holds counts[t] elements.
+ * `workspace` is device memory of at least ar_update_workspace_bytes(
+ * AR_UPDATE_GRAD_NORM, counts, ntensors) bytes, 8-byte aligned, owned by the
+ * caller; nothing in it needs to start at zero. */
+ar_result_t ar_grad_norm(const void* const* grads, const size_t* counts, int ntensors, ar_dtype_t dtype,
+                         float* norm, void* workspace, size_t workspace_bytes, hipStream_t stream);
+
+/* One AdamW step's settings.  With g the gradient as stored, N the 2-norm
+ * that *grad_norm holds, t = `step`, and every operation below rounded to
+ * float32 on its own:
+ *   c = grad_scale, or with max_norm > 0
+ *       grad_scale * min(1, max_norm / (N * grad_scale + 1e-6))
+ *   g' = c * g
+ *   m' = beta1 * m + (1 - beta1) * g'
+ *   v' = beta2 * v + (1 - beta2) * (g' * g')
+ *   d  = sqrt(v') * (1 / sqrt(1 - beta2^t)) + eps
+ *   p' = p * (1 - lr * weight_decay) - (m' / d) * (lr / (1 - beta1^t))
+ * with the scalars in parentheses computed in float64 on the host and rounded
+ * once.  (Decoupled weight decay: Loshchilov and Hutter, "Decoupled Weight
+ * Decay Regularization", 2019, algorithm 2.)  grad_scale undoes a loss scale
+ * (its inverse), or averages a sum over ranks.  With skip_nonfinite, a norm
+ * that is NaN or infinite makes the call leave every parameter and state as
+ * it is (its outputs hold its inputs' values).  `seed` is used by the packed
+ * step only; give each step its own. */
+typedef struct {
+    double lr;
+    double beta1;
+    double beta2;
+    double eps;
+    double weight_decay;
+    double max_norm;           /* 0: no clipping */
+    double grad_scale;         /* 1: gradients as they are */
+    unsigned long long step;   /* 1 for the first step */
+    unsigned int seed;
+    int skip_nonfinite;
+} ar_adamw_config_t;
+
+/* The tensors of an AdamW step.  Tensor t has counts[t] elements.  The arrays
+ * ending in _out name where the new values go; NULL, or an entry equal to the
+ * input's, updates in place.  An output may overlap nothing else.  `copies`
+ * (NULL: none), for float32 parameters only, also receives the new parameters
+ * rounded to copy_dtype (AR_BFLOAT16 or AR_FLOAT16).  ar_adamw: exp_avgs and
+ * exp_avg_sqs are float32, and the scale arrays are NULL.  ar_adamw_packed:
+ * they are one byte per element, and exp_avg_scales and exp_avg_sq_scales
+ * hold one byte per AR_STATE_BLOCK consecutive elements of the tensor (the
+ * last block may be short). */
+typedef struct {
+    int ntensors;
+    const size_t* counts;
+    ar_dtype_t param_dtype;
+    ar_dtype_t grad_dtype;
+    ar_dtype_t copy_dtype;
+    const void* const* params;
+    const void* const* grads;
+    const void* const* exp_avgs;
+    const void* const* exp_avg_sqs;
+    const void* const* exp_avg_scales;
+    const void* const* exp_avg_sq_scales;
+    void* const* params_out;
+    void* const* exp_avgs_out;
+    void* const* exp_avg_sqs_out;
+    void* const* exp_avg_scales_out;
+    void* const* exp_avg_sq_scales_out;
+    void* const* copies;
+} ar_adamw_tensors_t;
+
+/* One AdamW step over all the tensors.  grad_norm: one float32 in device
+ * memory, as ar_grad_norm writes it, read when the kernels run; needed by
+ * max_norm > 0 and by skip_nonfinite, else it may be NULL. */
+ar_result_t ar_adamw(const ar_adamw_tensors_t* tensors, const ar_adamw_config_t* config, const float* grad_norm,
+                     hipStream_t stream);
+
+/* The same step with each state in 8 bits: 2 bytes and a little of optimizer
+ * state per parameter instead of 8.  A block of AR_STATE_BLOCK elements has a
+ * scale byte e per state, worth 2^(e-127): the smallest e >= 1 whose
+ * 1.875 * 2^(e-127) reaches the largest magnitude of the block (e = 0, as in
+ * zeroed memory, means 1).  A code's value is 2^(e-127) times
+ *   exp_avg:    sign, 4 exponent bits E, 3 mantissa bits F:
+ *               (1 + F/8) * 2^(E-15), or F/8 * 2^-14 for E = 0;
+ *   exp_avg_sq: 5 exponent bits E, 3 mantissa bits F, no sign:
+ *               (1 + F/8) * 2^(E-31), or F/8 * 2^-30 for E = 0.
+ * So zeroed codes and scales are zero states.  e = 255 makes the whole block
+ * NaN: a block that would hold a NaN, an infinity or a value past float32's
+ * largest code gets it.  The step works on the decoded float32 states as
+ * ar_adamw does, updates the parameters from the new states before they are
+ * rounded, and rounds each new state to one of its two neighbouring codes, up
+ * with the probability of its place between them: a second moment moves by
+ * 1 - beta2 of itself a step, far less than the distance of two codes, and
+ * rounding to the nearest would never move it.  The 32 random bits of element i of
+ * tensor t are h(h(seed + 0x9E3779B9 * (t + 1)) + 0x9E3779B9 * i) in 32-bit
+ * arithmetic, h(x): x ^= x >> 16, x *= 0x7FEB352D, x ^= x >> 15,
+ * x *= 0x846CA68B, x ^= x >> 16 (a 32-bit mixer from C. Wellons' published
+ * search for integer hash functions); the lower 16 serve exp_avg, the upper
+ * 16 exp_avg_sq.  A positive exp_avg_sq is never rounded to 0, which would
+ * leave eps alone in the denominator. */
+#define AR_STATE_BLOCK 256
+ar_result_t ar_adamw_packed(const ar_adamw_tensors_t* tensors, const ar_adamw_config_t* config,
+                            const float* grad_norm, hipStream_t stream);
+
+/* Values of packed states, for checkpoints and inspection: outs[t] receives
+ * the counts[t] values that codes[t] and scales[t] stand for, in `dtype`
+ * (float32 and, but for its subnormals, bfloat16 hold every value exactly;
+ * binary16 rounds). */
+typedef enum {
+    AR_STATE_EXP_AVG = 0,
+    AR_STATE_EXP_AVG_SQ = 1
+} ar_state_t;
+ar_result_t ar_unpack_states(const void* const* codes, const void* const* scales, void* const* outs,
+                             const size_t* counts, int ntensors, ar_state_t state, ar_dtype_t dtype,
+                             hipStream_t stream);
+
+/* Persistent forms, for a training loop that updates the same tensors every
+ * step: *_init validates, checks where the buffers live as the collectives'
+ * *_init calls do, plans, and writes a table of the tensors into `workspace`
+ * (at least ar_update_workspace_bytes bytes of device memory, 8-byte aligned,
+ * the caller's, kept until the plan is freed and the work it enqueued is
+ * done).  The table is copied on `stream`, and *_init returns when it is
+ * there; it cannot run while the stream is being captured
+ * (AR_ERR_UNSUPPORTED).  A start then enqueues one launch over all the
+ * tensors (two for the norm of more than one tile), however many they are,
+ * where the one-shot calls need a launch for every few dozen tensors; it can
+ * be captured into a HIP graph, which replays the config it was captured
+ * with.  Same results as the one-shot calls.  ar_adamw_start takes a plan of
+ * ar_adamw_init or ar_adamw_packed_init; grad_norm must not be one of the
+ * plan's output buffers. */
+typedef struct ar_update_s* ar_update_t;
+typedef enum {
+    AR_UPDATE_GRAD_NORM = 0,
+    AR_UPDATE_ADAMW = 1,
+    AR_UPDATE_ADAMW_PACKED = 2
+} ar_update_kind_t;
+
+/* (size_t)-1 for invalid arguments. */
+size_t ar_update_workspace_bytes(ar_update_kind_t kind, const size_t* counts, int ntensors);
+ar_result_t ar_grad_norm_init(const void* const* grads, const size_t* counts, int ntensors, ar_dtype_t dtype,
+                              float* norm, void* workspace, size_t workspace_bytes, hipStream_t stream,
+                              ar_update_t* update);
+ar_result_t ar_adamw_init(const ar_adamw_tensors_t* tensors, void* workspace, size_t workspace_bytes,
+                          hipStream_t stream, ar_update_t* update);
+ar_result_t ar_adamw_packed_init(const ar_adamw_tensors_t* tensors, void* workspace, size_t workspace_bytes,
+                                 hipStream_t stream, ar_update_t* update);
+ar_result_t ar_grad_norm_start(ar_update_t update, hipStream_t stream);
+ar_result_t ar_adamw_start(ar_update_t update, const ar_adamw_config_t* config, const float* grad_norm,
+                           hipStream_t stream);
+/* Kernel launches one start enqueues, or -1 for NULL. */
+int ar_update_num_launches(ar_update_t update);
+ar_result_t ar_update_free(ar_update_t update);
+
+/* Layer norm over the last axis, of every rank's activations at once.  Rank r
+ * owns x[r] (`rows` rows of `cols` elements, row i at x[r] + i * x_stride
+ * elements; a stride of at least cols), its replicas gamma[r] and beta[r]
+ * (cols elements of weight_dtype; a NULL array: 1 and 0), and receives
+ *   mean = sum(x) / cols, rstd = 1 / sqrt(sum((x - mean)^2) / cols + eps),
+ *   y = (x - mean) * rstd * gamma + beta
+ * per row: y[r] in x's type with rows y_stride apart, mean[r] and rstd[r]
+ * (rows float32 each; both arrays NULL when no backward pass follows).
+ * weight_dtype is dtype or AR_FLOAT32.  y[r] may be x[r] with the same
+ * stride (two buffers interleaved in one, their strides equal and their rows
+ * apart, are also fine); outputs overlap nothing else.  rows == 0 or
+ * cols == 0 is a successful no-op. */
+ar_result_t ar_layer_norm(const void* const* x, const void* const* gamma, const void* const* beta, void* const* y,
+                          float* const* mean, float* const* rstd, size_t rows, size_t cols, size_t x_stride,
+                          size_t y_stride, ar_dtype_t dtype, ar_dtype_t weight_dtype, double eps, int nranks,
+                          hipStream_t stream);
+
+/* Its backward pass, from the forward pass's x, gamma, mean and rstd: with
+ * h = (x - mean) * rstd and w = dy * gamma, per row
+ *   dx = rstd * (w - sum(w) / cols - h * sum(w * h) / cols)
+ * and per column, over the rank's rows,
+ *   dgamma = sum(dy * h), dbeta = sum(dy)
+ * in weight_dtype: the rank's part of the weight gradients, which the
+ * AllReduce sums over the ranks.  gamma NULL: 1.  The arrays dgamma and dbeta
+ * may each be NULL; with rows == 0 they receive zeros.  dx[r] may be dy[r]
+ * with the same stride; outputs overlap nothing else.  `workspace`: at least
+ * ar_layer_norm_workspace_bytes(...) bytes of device memory, 4-byte aligned
+ * (the partial sums of dgamma and dbeta), needed unless both are NULL. */
+ar_result_t ar_layer_norm_backward(const void* const* dy, const void* const* x, const void* const* gamma,
+                                   const float* const* mean, const float* const* rstd, void* const* dx,
+                                   void* const* dgamma, void* const* dbeta, size_t rows, size_t cols,
+                                   size_t dy_stride, size_t x_stride, size_t dx_stride, ar_dtype_t dtype,
+                                   ar_dtype_t weight_dtype, int nranks, void* workspace, size_t workspace_bytes,
+                                   hipStream_t stream);
+/* (size_t)-1 for invalid arguments. */
+size_t ar_layer_norm_workspace_bytes(size_t rows, size_t cols, int nranks);
+
 #ifdef __cplusplus
 }
 #endif

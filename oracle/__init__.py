@@ -31,7 +31,10 @@ What it holds, each piece written from the pages on ring AllReduce:
                 send/receive events, and every bracketing of an N-term sum;
 * ``staged``    AllReduce as a reduce onto a root followed by a broadcast
                 (bitfern.com "AllReduce Explained", section "Reduce Followed
-                by Broadcast"), the root folding in the ring's order.
+                by Broadcast"), the root folding in the ring's order;
+* ``step``      the training step's operators around the reduction: global
+                gradient norm, AdamW with float32 and packed states, layer
+                norm and its gradient.
 
 Pins (what each part is checked against) are in ``tests/test_oracle_*.py``.
 Every function has a pin; none is "parity unpinned".

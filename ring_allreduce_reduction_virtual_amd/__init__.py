@@ -30,6 +30,25 @@ from .binding import (  # noqa: F401
     ar_reduce_scatter_noalloc,
     ar_workspace_bytes,
 )
+from .step import (  # noqa: F401
+    PackedState,
+    Update,
+    ar_adamw,
+    ar_adamw_init,
+    ar_adamw_packed,
+    ar_adamw_packed_init,
+    ar_adamw_start,
+    ar_grad_norm,
+    ar_grad_norm_init,
+    ar_grad_norm_start,
+    ar_layer_norm,
+    ar_layer_norm_backward,
+    ar_layer_norm_workspace_bytes,
+    ar_unpack_states,
+    ar_update_free,
+    ar_update_num_launches,
+    ar_update_workspace_bytes,
+)
 
 __all__ = [
     "ArError", "lib", "Plan",
@@ -38,4 +57,8 @@ __all__ = [
     "ar_get_error_string", "ar_get_last_error_detail", "ar_dtype_size",
     "ar_allreduce_init", "ar_reduce_scatter_init", "ar_all_gather_init", "ar_plan_start", "ar_plan_free",
     "ar_plan_limit_blocks", "ar_plan_num_launches", "ar_reduce_scatter_noalloc", "ar_plan_algo",
+    "PackedState", "Update", "ar_grad_norm", "ar_grad_norm_init", "ar_grad_norm_start",
+    "ar_adamw", "ar_adamw_init", "ar_adamw_packed", "ar_adamw_packed_init", "ar_adamw_start", "ar_unpack_states",
+    "ar_update_workspace_bytes", "ar_update_num_launches", "ar_update_free",
+    "ar_layer_norm", "ar_layer_norm_backward", "ar_layer_norm_workspace_bytes",
 ]

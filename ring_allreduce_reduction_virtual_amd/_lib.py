@@ -35,7 +35,15 @@ EXPORTS = (
     "ar_allreduce_init", "ar_reduce_scatter_init", "ar_all_gather_init",
     "ar_plan_start", "ar_plan_num_launches", "ar_plan_free", "ar_plan_limit_blocks",
     "ar_reduce_scatter_noalloc", "ar_plan_algo",
+    "ar_grad_norm", "ar_grad_norm_init", "ar_grad_norm_start",
+    "ar_adamw", "ar_adamw_init", "ar_adamw_packed", "ar_adamw_packed_init", "ar_adamw_start",
+    "ar_unpack_states", "ar_update_workspace_bytes", "ar_update_num_launches", "ar_update_free",
+    "ar_layer_norm", "ar_layer_norm_backward", "ar_layer_norm_workspace_bytes",
 )
+# the training-step operators' enums and constants
+STATES = {"exp_avg": 0, "exp_avg_sq": 1}
+UPDATES = {"grad_norm": 0, "adamw": 1, "adamw_packed": 2}
+STATE_BLOCK = 256
 # bytes of the fixed device array behind ar_reduce_scatter_noalloc
 NOALLOC_SCRATCH_BYTES = 64 << 20
 
@@ -45,6 +53,30 @@ _vp = ctypes.c_void_p
 _vpp = ctypes.POINTER(ctypes.c_void_p)
 _sz = ctypes.c_size_t
 _int = ctypes.c_int
+_szp = ctypes.POINTER(ctypes.c_size_t)
+
+
+class AdamwConfig(ctypes.Structure):
+    """ar_adamw_config_t"""
+
+    _fields_ = [("lr", ctypes.c_double), ("beta1", ctypes.c_double), ("beta2", ctypes.c_double),
+                ("eps", ctypes.c_double), ("weight_decay", ctypes.c_double), ("max_norm", ctypes.c_double),
+                ("grad_scale", ctypes.c_double), ("step", ctypes.c_ulonglong), ("seed", ctypes.c_uint),
+                ("skip_nonfinite", _int)]
+
+
+class AdamwTensors(ctypes.Structure):
+    """ar_adamw_tensors_t"""
+
+    _fields_ = [("ntensors", _int), ("counts", _szp), ("param_dtype", _int), ("grad_dtype", _int),
+                ("copy_dtype", _int)] + [(name, _vpp) for name in (
+                    "params", "grads", "exp_avgs", "exp_avg_sqs", "exp_avg_scales", "exp_avg_sq_scales",
+                    "params_out", "exp_avgs_out", "exp_avg_sqs_out", "exp_avg_scales_out", "exp_avg_sq_scales_out",
+                    "copies")]
+
+
+_tensors = ctypes.POINTER(AdamwTensors)
+_config = ctypes.POINTER(AdamwConfig)
 
 
 def _declare(lib):
@@ -69,6 +101,22 @@ def _declare(lib):
         "ar_plan_free": (_int, [_vp]),
         "ar_plan_limit_blocks": (_int, [_vp, ctypes.c_uint]),
         "ar_reduce_scatter_noalloc": (_int, [_vpp, _vpp, _sz, _int, _int, _int, _int, _vp]),
+        "ar_grad_norm": (_int, [_vpp, _szp, _int, _int, _vp, _vp, _sz, _vp]),
+        "ar_grad_norm_init": (_int, [_vpp, _szp, _int, _int, _vp, _vp, _sz, _vp, _vpp]),
+        "ar_grad_norm_start": (_int, [_vp, _vp]),
+        "ar_adamw": (_int, [_tensors, _config, _vp, _vp]),
+        "ar_adamw_packed": (_int, [_tensors, _config, _vp, _vp]),
+        "ar_adamw_init": (_int, [_tensors, _vp, _sz, _vp, _vpp]),
+        "ar_adamw_packed_init": (_int, [_tensors, _vp, _sz, _vp, _vpp]),
+        "ar_adamw_start": (_int, [_vp, _config, _vp, _vp]),
+        "ar_unpack_states": (_int, [_vpp, _vpp, _vpp, _szp, _int, _int, _int, _vp]),
+        "ar_update_workspace_bytes": (_sz, [_int, _szp, _int]),
+        "ar_update_num_launches": (_int, [_vp]),
+        "ar_update_free": (_int, [_vp]),
+        "ar_layer_norm": (_int, [_vpp, _vpp, _vpp, _vpp, _vpp, _vpp, _sz, _sz, _sz, _sz, _int, _int,
+                                 ctypes.c_double, _int, _vp]),
+        "ar_layer_norm_backward": (_int, [_vpp] * 8 + [_sz] * 5 + [_int, _int, _int, _vp, _sz, _vp]),
+        "ar_layer_norm_workspace_bytes": (_sz, [_sz, _sz, _int]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)

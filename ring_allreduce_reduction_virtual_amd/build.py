@@ -21,7 +21,8 @@ INCLUDE = os.path.join(ROOT, "include")
 LIB_PATH = os.path.join(PKG_DIR, "libar.so")
 
 SOURCES = ("ar_api.hip", "ar_kernels.hip", "ar_tree_kernels.hip", "ar_persistent_kernels.hip", "ar_dbt_kernels.hip",
-           "ar_noalloc.hip")
+           "ar_noalloc.hip", "ar_step_api.hip", "ar_step_kernels.hip", "ar_layer_norm_api.hip",
+           "ar_layer_norm_kernels.hip", "ar_layer_norm_backward_kernels.hip")
 
 # -ffp-contract=off: no fused multiply-add, every add/mul rounds on its own.
 # -fno-fast-math: IEEE semantics (NaN, signed zero, no reassociation).

@@ -1,0 +1,425 @@
+// HIP kernels of the training step around the gradient reduction: the global
+// gradient norm, the AdamW step over many tensors (states in float32, or in 8
+// bits), and the packed states' values.  include/ar.h states the formulas.
+//
+// All of them stream their tensors once: HBM's rate on the bytes that the
+// formulas name bounds them, the packed step's arithmetic aside.  One launch
+// covers many tensors: a tile is a stretch of one tensor, and a workgroup
+// finds the tensor of its tile in a table (in the arguments, or in device
+// memory for a plan).
+
+#include "ar_step.h"
+#include "ar_step_device.h"
+
+namespace arimpl {
+namespace {
+
+template <class Entry>
+__device__ __forceinline__ const Entry& find(const InlineTable<Entry>& t, uint32_t tile) {
+    int lo = 0, hi = t.n;
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (t.e[mid].first_tile <= tile) {
+            lo = mid;
+        } else {
+            hi = mid;
+        }
+    }
+    return t.e[lo];
+}
+template <class Entry>
+__device__ __forceinline__ const Entry& find(const DeviceTable<Entry>& t, uint32_t tile) {
+    return t.e[__builtin_amdgcn_readfirstlane(t.tile_entry[tile])];
+}
+
+// ---------------------------------------------------------------------------
+// gradient norm
+// ---------------------------------------------------------------------------
+
+// The sum of a value over the block, valid in thread 0.
+__device__ __forceinline__ double block_sum(double x) {
+    __shared__ double part[kStepThreads / 64];
+#pragma unroll
+    for (int d = 32; d > 0; d >>= 1) x += __shfl_down(x, d, 64);
+    if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = x;
+    __syncthreads();
+    double s = 0;
+    if (threadIdx.x == 0) {
+        for (int w = 0; w < kStepThreads / 64; ++w) s += part[w];
+    }
+    return s;
+}
+
+// Sum of squares in float64: the square of a float32 is exact there and can
+// neither overflow nor vanish.  Workgroup b takes tiles b, b + gridDim.x, ...
+// and leaves one partial sum, or the norm itself when it is the only one.
+template <int DT, class Table>
+__global__ void __launch_bounds__(kStepThreads) k_grad_norm(Table t, uint32_t tiles, double* partials, float* norm) {
+    constexpr int V = 16 / elem_size<DT>();
+    constexpr int U = kNormTile / (kStepThreads * V);
+    double acc[4] = {0, 0, 0, 0};
+    for (uint32_t tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
+        const auto& e = find(t, tile);
+        const char* const g = e.g;
+        const uint64_t n = e.n;
+        const uint64_t at = static_cast<uint64_t>(tile - e.first_tile) * kNormTile + threadIdx.x * V;
+        Raw<DT, V> r[U];
+        if (at - threadIdx.x * V + kNormTile <= n) {
+#pragma unroll
+            for (int u = 0; u < U; ++u) load_at<true, true>(r[u], g, at + u * kStepThreads * V, n);
+        } else {
+#pragma unroll
+            for (int u = 0; u < U; ++u) load_at<false, false>(r[u], g, at + u * kStepThreads * V, n);
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+#pragma unroll
+            for (int j = 0; j < V; ++j) {
+                const double x = r[u].get(j);
+                acc[j % 4] = __builtin_fma(x, x, acc[j % 4]);
+            }
+        }
+    }
+    const double s = block_sum((acc[0] + acc[1]) + (acc[2] + acc[3]));
+    if (threadIdx.x == 0) {
+        if (norm != nullptr) {
+            *norm = static_cast<float>(sqrt(s));
+        } else {
+            partials[blockIdx.x] = s;
+        }
+    }
+}
+
+__global__ void __launch_bounds__(kStepThreads) k_grad_norm_final(const double* partials, uint32_t n, float* norm) {
+    double acc = 0;
+    for (uint32_t i = threadIdx.x; i < n; i += kStepThreads) acc += partials[i];
+    const double s = block_sum(acc);
+    if (threadIdx.x == 0) *norm = static_cast<float>(sqrt(s));
+}
+
+// ---------------------------------------------------------------------------
+// AdamW
+// ---------------------------------------------------------------------------
+
+// The gradient's factor, and whether the step is skipped.
+struct Gate {
+    float factor;
+    bool skip;
+};
+__device__ __forceinline__ Gate gate(const AdamwScalars& s) {
+    Gate r{s.grad_scale, false};
+    if (s.grad_norm != nullptr) {
+        const float norm = *s.grad_norm;
+        r.skip = s.skip_nonfinite != 0 && (as_u(norm) & 0x7f800000u) == 0x7f800000u;
+        if (s.max_norm > 0.0f) {
+            // a NaN norm makes the factor NaN, as min() in the formula does not
+            const float f = s.max_norm / (norm * s.grad_scale + 1e-6f);
+            r.factor = s.grad_scale * (f > 1.0f ? 1.0f : f);
+        }
+    }
+    return r;
+}
+
+// One element: the new states and parameter from the old ones.
+__device__ __forceinline__ void adamw_update(const AdamwScalars& s, float factor, float g, float& p, float& m,
+                                             float& v) {
+    const float gs = factor * g;
+    m = m * s.beta1 + gs * s.one_minus_beta1;
+    v = v * s.beta2 + (gs * gs) * s.one_minus_beta2;
+    const float d = sqrtf(v) * s.rsqrt_correction2 + s.eps;
+    p = p * s.decay - (m / d) * s.step_size;
+}
+
+template <int PD, int GD, bool FULL>
+__device__ __forceinline__ void adamw_tile(const AdamwEntry& e, const AdamwScalars& s, uint64_t at, uint64_t n) {
+    constexpr int V = 4;
+    constexpr int U = kAdamwTile / (kStepThreads * V);
+    constexpr int kStep = kStepThreads * V;
+    Raw<PD, V> p[U];
+    Raw<GD, V> g[U];
+    Raw<AR_FLOAT32, V> m[U], v[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+        load_at<FULL, true>(g[u], e.g, at + u * kStep, n);
+        load_at<FULL, true>(p[u], e.p, at + u * kStep, n);
+        load_at<FULL, true>(m[u], e.m, at + u * kStep, n);
+        load_at<FULL, true>(v[u], e.v, at + u * kStep, n);
+    }
+    const Gate gt = gate(s);
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+        float pn[V], mn[V], vn[V];
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+            pn[j] = p[u].get(j);
+            mn[j] = m[u].get(j);
+            vn[j] = v[u].get(j);
+            if (!gt.skip) adamw_update(s, gt.factor, g[u].get(j), pn[j], mn[j], vn[j]);
+        }
+        p[u].set_all(pn);
+        m[u].set_all(mn);
+        v[u].set_all(vn);
+        store_at<FULL, true>(p[u], e.p_out, at + u * kStep, n);
+        store_at<FULL, true>(m[u], e.m_out, at + u * kStep, n);
+        store_at<FULL, true>(v[u], e.v_out, at + u * kStep, n);
+        if (PD == AR_FLOAT32 && e.copy != nullptr) {
+            if (s.copy_f16) {
+                Raw<AR_FLOAT16, V> c;
+                c.set_all(pn);
+                store_at<FULL, true>(c, e.copy, at + u * kStep, n);
+            } else {
+                Raw<AR_BFLOAT16, V> c;
+                c.set_all(pn);
+                store_at<FULL, true>(c, e.copy, at + u * kStep, n);
+            }
+        }
+    }
+}
+
+template <int PD, int GD, class Table>
+__global__ void __launch_bounds__(kStepThreads) k_adamw(Table t, AdamwScalars s) {
+    const AdamwEntry e = find(t, blockIdx.x);
+    const uint64_t tile = static_cast<uint64_t>(blockIdx.x - e.first_tile) * kAdamwTile;
+    if (tile + kAdamwTile <= e.n) {
+        adamw_tile<PD, GD, true>(e, s, tile + threadIdx.x * 4, e.n);
+    } else {
+        adamw_tile<PD, GD, false>(e, s, tile + threadIdx.x * 4, e.n);
+    }
+}
+
+// ---------------------------------------------------------------------------
+// AdamW, states in 8 bits
+// ---------------------------------------------------------------------------
+
+// 8 codes at p, whole or up to the tensor's end.
+template <bool FULL>
+__device__ __forceinline__ u32x2 load_codes(const uint8_t* base, uint64_t i, uint64_t n) {
+    if (FULL || i + 8 <= n) return load_as<true, u32x2_a1>(reinterpret_cast<const char*>(base + i));
+    u32x2 r = {0, 0};
+    for (int j = 0; j < 8; ++j) {
+        if (i + j < n) r[j / 4] |= static_cast<uint32_t>(base[i + j]) << (8 * (j % 4));
+    }
+    return r;
+}
+template <bool FULL>
+__device__ __forceinline__ void store_codes(uint8_t* base, uint64_t i, uint64_t n, u32x2 c) {
+    if (FULL || i + 8 <= n) {
+        store_as<true, u32x2_a1>(reinterpret_cast<char*>(base + i), c);
+        return;
+    }
+    for (int j = 0; j < 8; ++j) {
+        if (i + j < n) base[i + j] = static_cast<uint8_t>(c[j / 4] >> (8 * (j % 4)));
+    }
+}
+
+// A thread has 8 neighbouring elements, half a wavefront a state block of 256:
+// the block's largest magnitude is a maximum over 32 lanes, with no LDS.
+template <int PD, int GD, bool FULL>
+__device__ __forceinline__ void packed_tile(const PackedEntry& e, const AdamwScalars& s, uint64_t at, uint64_t n) {
+    constexpr int V = 8;
+    const uint64_t block = at / AR_STATE_BLOCK;
+    const bool live = FULL || block * AR_STATE_BLOCK < n;
+    Raw<PD, V> p;
+    Raw<GD, V> g;
+    load_at<FULL, true>(g, e.g, at, n);
+    load_at<FULL, true>(p, e.p, at, n);
+    const u32x2 mc = load_codes<FULL>(e.m, at, n), vc = load_codes<FULL>(e.v, at, n);
+    const uint32_t me = live ? e.ms[block] : 0, ve = live ? e.vs[block] : 0;
+    const Gate gt = gate(s);
+    const float mscale = scale_value(me), vscale = scale_value(ve);
+    float pn[V], mn[V], vn[V];
+    uint32_t mtop = 0, vtop = 0;
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+        pn[j] = p.get(j);
+        mn[j] = decode<true>((mc[j / 4] >> (8 * (j % 4))) & 0xffu, mscale);
+        vn[j] = decode<false>((vc[j / 4] >> (8 * (j % 4))) & 0xffu, vscale);
+        if (!gt.skip) adamw_update(s, gt.factor, g.get(j), pn[j], mn[j], vn[j]);
+        // beyond the end there is nothing
+        if (!FULL && at + j >= n) mn[j] = vn[j] = 0.0f;
+        const uint32_t mb = as_u(mn[j]) & 0x7fffffffu, vb = as_u(vn[j]) & 0x7fffffffu;
+        mtop = mb > mtop ? mb : mtop;
+        vtop = vb > vtop ? vb : vtop;
+    }
+    const uint32_t me_new = scale_for(max_over_lanes<32>(mtop)), ve_new = scale_for(max_over_lanes<32>(vtop));
+    const float minv = scale_inverse(me_new), vinv = scale_inverse(ve_new);
+    const uint32_t key = mix32(s.seed + 0x9e3779b9u * (e.index + 1));
+    u32x2 mo = {0, 0}, vo = {0, 0};
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+        const uint32_t r = mix32(key + 0x9e3779b9u * static_cast<uint32_t>(at + j));
+        mo[j / 4] |= encode<true>(mn[j], minv, (r & 0xffffu) * 16 + 8) << (8 * (j % 4));
+        vo[j / 4] |= encode<false>(vn[j], vinv, (r >> 16) * 16 + 8) << (8 * (j % 4));
+    }
+    if (me_new == 255) mo = u32x2{0, 0};
+    if (ve_new == 255) vo = u32x2{0, 0};
+    p.set_all(pn);
+    store_at<FULL, true>(p, e.p_out, at, n);
+    store_codes<FULL>(e.m_out, at, n, gt.skip ? mc : mo);
+    store_codes<FULL>(e.v_out, at, n, gt.skip ? vc : vo);
+    if (live && threadIdx.x % 32 == 0) {
+        e.ms_out[block] = static_cast<uint8_t>(gt.skip ? me : me_new);
+        e.vs_out[block] = static_cast<uint8_t>(gt.skip ? ve : ve_new);
+    }
+    if (PD == AR_FLOAT32 && e.copy != nullptr) {
+        if (s.copy_f16) {
+            Raw<AR_FLOAT16, V> c;
+            c.set_all(pn);
+            store_at<FULL, true>(c, e.copy, at, n);
+        } else {
+            Raw<AR_BFLOAT16, V> c;
+            c.set_all(pn);
+            store_at<FULL, true>(c, e.copy, at, n);
+        }
+    }
+}
+
+template <int PD, int GD, class Table>
+__global__ void __launch_bounds__(kStepThreads) k_adamw_packed(Table t, AdamwScalars s) {
+    static_assert(kPackedTile == kStepThreads * 8, "one vector per thread");
+    const PackedEntry e = find(t, blockIdx.x);
+    const uint64_t tile = static_cast<uint64_t>(blockIdx.x - e.first_tile) * kPackedTile;
+    if (tile + kPackedTile <= e.n) {
+        packed_tile<PD, GD, true>(e, s, tile + threadIdx.x * 8, e.n);
+    } else {
+        packed_tile<PD, GD, false>(e, s, tile + threadIdx.x * 8, e.n);
+    }
+}
+
+template <int DT, bool SIGNED>
+__global__ void __launch_bounds__(kStepThreads) k_unpack(InlineTable<UnpackEntry> t) {
+    static_assert(kUnpackTile == kStepThreads * 8, "one vector per thread");
+    const UnpackEntry& e = find(t, blockIdx.x);
+    const uint64_t at = static_cast<uint64_t>(blockIdx.x - e.first_tile) * kUnpackTile + threadIdx.x * 8;
+    if (at >= e.n) return;
+    const u32x2 c = load_codes<false>(e.codes, at, e.n);
+    const float scale = scale_value(e.scales[at / AR_STATE_BLOCK]);
+    float x[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) x[j] = decode<SIGNED>((c[j / 4] >> (8 * (j % 4))) & 0xffu, scale);
+    Raw<DT, 8> r;
+    r.set_all(x);
+    store_at<false, true>(r, e.out, at, e.n);
+}
+
+}  // namespace
+
+// ---------------------------------------------------------------------------
+// launches
+// ---------------------------------------------------------------------------
+
+template <class Table>
+hipError_t launch_norm(const Table& t, uint32_t tiles, uint32_t blocks, ar_dtype_t dtype, double* partials,
+                       float* norm, hipStream_t stream) {
+    const dim3 grid(blocks), block(kStepThreads);
+    switch (dtype) {
+        case AR_FLOAT32:
+            hipLaunchKernelGGL((k_grad_norm<AR_FLOAT32, Table>), grid, block, 0, stream, t, tiles, partials, norm);
+            break;
+        case AR_BFLOAT16:
+            hipLaunchKernelGGL((k_grad_norm<AR_BFLOAT16, Table>), grid, block, 0, stream, t, tiles, partials, norm);
+            break;
+        case AR_FLOAT16:
+            hipLaunchKernelGGL((k_grad_norm<AR_FLOAT16, Table>), grid, block, 0, stream, t, tiles, partials, norm);
+            break;
+        default: return hipErrorInvalidValue;
+    }
+    return hipGetLastError();
+}
+
+hipError_t launch_norm_final(const double* partials, uint32_t n, float* norm, hipStream_t stream) {
+    hipLaunchKernelGGL(k_grad_norm_final, dim3(1), dim3(kStepThreads), 0, stream, partials, n, norm);
+    return hipGetLastError();
+}
+
+namespace {
+
+template <int PD, class Table>
+hipError_t adamw_by_grad(const Table& t, uint32_t tiles, const AdamwScalars& s, ar_dtype_t grad, hipStream_t stream) {
+    const dim3 grid(tiles), block(kStepThreads);
+    switch (grad) {
+        case AR_FLOAT32: hipLaunchKernelGGL((k_adamw<PD, AR_FLOAT32, Table>), grid, block, 0, stream, t, s); break;
+        case AR_BFLOAT16: hipLaunchKernelGGL((k_adamw<PD, AR_BFLOAT16, Table>), grid, block, 0, stream, t, s); break;
+        case AR_FLOAT16: hipLaunchKernelGGL((k_adamw<PD, AR_FLOAT16, Table>), grid, block, 0, stream, t, s); break;
+        default: return hipErrorInvalidValue;
+    }
+    return hipGetLastError();
+}
+
+template <int PD, class Table>
+hipError_t packed_by_grad(const Table& t, uint32_t tiles, const AdamwScalars& s, ar_dtype_t grad, hipStream_t stream) {
+    const dim3 grid(tiles), block(kStepThreads);
+    switch (grad) {
+        case AR_FLOAT32:
+            hipLaunchKernelGGL((k_adamw_packed<PD, AR_FLOAT32, Table>), grid, block, 0, stream, t, s);
+            break;
+        case AR_BFLOAT16:
+            hipLaunchKernelGGL((k_adamw_packed<PD, AR_BFLOAT16, Table>), grid, block, 0, stream, t, s);
+            break;
+        case AR_FLOAT16:
+            hipLaunchKernelGGL((k_adamw_packed<PD, AR_FLOAT16, Table>), grid, block, 0, stream, t, s);
+            break;
+        default: return hipErrorInvalidValue;
+    }
+    return hipGetLastError();
+}
+
+template <int DT>
+hipError_t unpack_by_state(const InlineTable<UnpackEntry>& t, uint32_t tiles, ar_state_t state, hipStream_t stream) {
+    const dim3 grid(tiles), block(kStepThreads);
+    if (state == AR_STATE_EXP_AVG) {
+        hipLaunchKernelGGL((k_unpack<DT, true>), grid, block, 0, stream, t);
+    } else {
+        hipLaunchKernelGGL((k_unpack<DT, false>), grid, block, 0, stream, t);
+    }
+    return hipGetLastError();
+}
+
+}  // namespace
+
+template <class Table>
+hipError_t launch_adamw(const Table& t, uint32_t tiles, const AdamwScalars& s, ar_dtype_t param, ar_dtype_t grad,
+                        hipStream_t stream) {
+    switch (param) {
+        case AR_FLOAT32: return adamw_by_grad<AR_FLOAT32>(t, tiles, s, grad, stream);
+        case AR_BFLOAT16: return adamw_by_grad<AR_BFLOAT16>(t, tiles, s, grad, stream);
+        case AR_FLOAT16: return adamw_by_grad<AR_FLOAT16>(t, tiles, s, grad, stream);
+        default: return hipErrorInvalidValue;
+    }
+}
+
+template <class Table>
+hipError_t launch_packed(const Table& t, uint32_t tiles, const AdamwScalars& s, ar_dtype_t param, ar_dtype_t grad,
+                         hipStream_t stream) {
+    switch (param) {
+        case AR_FLOAT32: return packed_by_grad<AR_FLOAT32>(t, tiles, s, grad, stream);
+        case AR_BFLOAT16: return packed_by_grad<AR_BFLOAT16>(t, tiles, s, grad, stream);
+        case AR_FLOAT16: return packed_by_grad<AR_FLOAT16>(t, tiles, s, grad, stream);
+        default: return hipErrorInvalidValue;
+    }
+}
+
+hipError_t launch_unpack(const InlineTable<UnpackEntry>& t, uint32_t tiles, ar_state_t state, ar_dtype_t dtype,
+                         hipStream_t stream) {
+    switch (dtype) {
+        case AR_FLOAT32: return unpack_by_state<AR_FLOAT32>(t, tiles, state, stream);
+        case AR_BFLOAT16: return unpack_by_state<AR_BFLOAT16>(t, tiles, state, stream);
+        case AR_FLOAT16: return unpack_by_state<AR_FLOAT16>(t, tiles, state, stream);
+        default: return hipErrorInvalidValue;
+    }
+}
+
+template hipError_t launch_norm(const InlineTable<NormEntry>&, uint32_t, uint32_t, ar_dtype_t, double*, float*,
+                                hipStream_t);
+template hipError_t launch_norm(const DeviceTable<NormEntry>&, uint32_t, uint32_t, ar_dtype_t, double*, float*,
+                                hipStream_t);
+template hipError_t launch_adamw(const InlineTable<AdamwEntry>&, uint32_t, const AdamwScalars&, ar_dtype_t, ar_dtype_t,
+                                 hipStream_t);
+template hipError_t launch_adamw(const DeviceTable<AdamwEntry>&, uint32_t, const AdamwScalars&, ar_dtype_t, ar_dtype_t,
+                                 hipStream_t);
+template hipError_t launch_packed(const InlineTable<PackedEntry>&, uint32_t, const AdamwScalars&, ar_dtype_t,
+                                  ar_dtype_t, hipStream_t);
+template hipError_t launch_packed(const DeviceTable<PackedEntry>&, uint32_t, const AdamwScalars&, ar_dtype_t,
+                                  ar_dtype_t, hipStream_t);
+
+}  // namespace arimpl
