@@ -220,22 +220,12 @@ __device__ __forceinline__ float sum_over_lanes(float x) {
 
 // A code's exponent and mantissa bits, put at bits 20 and up of a float32,
 // read as 2^(E-127) (1 + F/8) or, for E = 0, the subnormal F/8 2^-126: one
-// multiplication by a power of two (exact, subnormals included) gives the
-// code's value, for every E alike; the same in reverse rounds.  SIGNED is
-// exp_avg's form (4 exponent bits), else exp_avg_sq's (5).
+// exact shift of the exponent (v_ldexp_f32, which keeps subnormals) gives the
+// code's value times its scale for every E alike; the same in reverse rounds.
+// SIGNED is exp_avg's form (4 exponent bits), else exp_avg_sq's (5).
 template <bool SIGNED>
-constexpr float kCodeUp = SIGNED ? 0x1p112f : 0x1p96f;
-template <bool SIGNED>
-constexpr float kCodeDown = SIGNED ? 0x1p-112f : 0x1p-96f;
+constexpr int kCodeShift = SIGNED ? 15 : 31;
 
-__device__ __forceinline__ float scale_value(uint32_t e) {
-    const uint32_t bits = (e > 0 ? e : 1) << 23;
-    return as_f(e == 255 ? 0x7fc00000u : bits);
-}
-// 1 / scale_value(e) for e in 1..254
-__device__ __forceinline__ float scale_inverse(uint32_t e) {
-    return as_f(e == 254 ? 0x00400000u : (254 - e) << 23);
-}
 // The scale byte of a block whose largest magnitude has these bits: adding just
 // under an eighth of the exponent's step carries when the mantissa is above
 // 1.875.
@@ -244,25 +234,36 @@ __device__ __forceinline__ uint32_t scale_for(uint32_t top_bits) {
     return e == 0 ? 1 : (e > 255 ? 255 : e);
 }
 
+// Code j of four in a word, with scale byte `e`.  A block whose scale is 255
+// (NaN) is its caller's to mark.
 template <bool SIGNED>
-__device__ __forceinline__ float decode(uint32_t code, float scale) {
-    const uint32_t body = SIGNED ? code & 0x7fu : code;
-    const float x = as_f(body << 20) * kCodeUp<SIGNED> * scale;
-    return SIGNED ? as_f(as_u(x) ^ ((code & 0x80u) << 24)) : x;
+__device__ __forceinline__ float decode(uint32_t word, int j, uint32_t e) {
+    const int shift = static_cast<int>(e > 0 ? e : 1) - kCodeShift<SIGNED>;
+    if constexpr (SIGNED) {
+        // to the top byte, then back by four with the sign's copies cut off
+        const int top = static_cast<int>(word << (24 - 8 * j)) >> 4;
+        return __builtin_amdgcn_ldexpf(as_f(static_cast<uint32_t>(top) & 0x87f00000u), shift);
+    } else {
+        const uint32_t body = j < 3 ? word << (20 - 8 * j) : word >> 4;
+        return __builtin_amdgcn_ldexpf(as_f(body & 0x0ff00000u), shift);
+    }
 }
 
-// x (at most 1.875 scales) to one of its two neighbours: `noise`, 20 bits, is
-// added below the code's last bit and the rest cut off.
+// x (at most 1.875 scales) to one of its two neighbours, the code in the
+// result's top byte: `noise`, a multiple of 16 below 2^20, plus 8 is added
+// below the code's last bit; the bits under the top byte are not the code's.
 template <bool SIGNED>
-__device__ __forceinline__ uint32_t encode(float x, float inverse, uint32_t noise) {
-    const uint32_t y = as_u(as_f(as_u(x) & 0x7fffffffu) * inverse * kCodeDown<SIGNED>);
-    uint32_t code = (y + noise) >> 20;
-    if constexpr (SIGNED) {
-        code |= (as_u(x) >> 24) & 0x80u;
-    } else {
-        code = (code == 0 && x > 0.0f) ? 1 : code;
-    }
-    return code;
+__device__ __forceinline__ uint32_t encode(float x, uint32_t e, uint32_t noise) {
+    const int shift = kCodeShift<SIGNED> - static_cast<int>(e);
+    const uint32_t y = as_u(__builtin_amdgcn_ldexpf(__builtin_fabsf(x), shift)) + noise + 8;
+    if constexpr (SIGNED) return (as_u(x) & 0x80000000u) | ((y << 4) & 0x7fffffffu);
+    return y << 4;
+}
+
+// The top bytes of four words as one.
+__device__ __forceinline__ uint32_t top_bytes(uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+    const uint32_t lo = __builtin_amdgcn_perm(b, a, 0x0c0c0703u), hi = __builtin_amdgcn_perm(d, c, 0x0c0c0703u);
+    return __builtin_amdgcn_perm(hi, lo, 0x05040100u);
 }
 
 __device__ __forceinline__ uint32_t mix32(uint32_t x) {

@@ -130,6 +130,21 @@ __device__ __forceinline__ void adamw_update(const AdamwScalars& s, float factor
     p = p * s.decay - (m / d) * s.step_size;
 }
 
+// V new parameters rounded to the copies' type.
+template <bool FULL, int V>
+__device__ __forceinline__ void store_copy(char* copy, const AdamwScalars& s, uint64_t at, uint64_t n,
+                                           const float (&p)[V]) {
+    if (s.copy_f16) {
+        Raw<AR_FLOAT16, V> c;
+        c.set_all(p);
+        store_at<FULL, true>(c, copy, at, n);
+    } else {
+        Raw<AR_BFLOAT16, V> c;
+        c.set_all(p);
+        store_at<FULL, true>(c, copy, at, n);
+    }
+}
+
 template <int PD, int GD, bool FULL>
 __device__ __forceinline__ void adamw_tile(const AdamwEntry& e, const AdamwScalars& s, uint64_t at, uint64_t n) {
     constexpr int V = 4;
@@ -154,7 +169,10 @@ __device__ __forceinline__ void adamw_tile(const AdamwEntry& e, const AdamwScala
             pn[j] = p[u].get(j);
             mn[j] = m[u].get(j);
             vn[j] = v[u].get(j);
-            if (!gt.skip) adamw_update(s, gt.factor, g[u].get(j), pn[j], mn[j], vn[j]);
+        }
+        if (!gt.skip) {
+#pragma unroll
+            for (int j = 0; j < V; ++j) adamw_update(s, gt.factor, g[u].get(j), pn[j], mn[j], vn[j]);
         }
         p[u].set_all(pn);
         m[u].set_all(mn);
@@ -162,17 +180,7 @@ __device__ __forceinline__ void adamw_tile(const AdamwEntry& e, const AdamwScala
         store_at<FULL, true>(p[u], e.p_out, at + u * kStep, n);
         store_at<FULL, true>(m[u], e.m_out, at + u * kStep, n);
         store_at<FULL, true>(v[u], e.v_out, at + u * kStep, n);
-        if (PD == AR_FLOAT32 && e.copy != nullptr) {
-            if (s.copy_f16) {
-                Raw<AR_FLOAT16, V> c;
-                c.set_all(pn);
-                store_at<FULL, true>(c, e.copy, at + u * kStep, n);
-            } else {
-                Raw<AR_BFLOAT16, V> c;
-                c.set_all(pn);
-                store_at<FULL, true>(c, e.copy, at + u * kStep, n);
-            }
-        }
+        if (PD == AR_FLOAT32 && e.copy != nullptr) store_copy<FULL>(e.copy, s, at + u * kStep, n, pn);
     }
 }
 
@@ -212,9 +220,41 @@ __device__ __forceinline__ void store_codes(uint8_t* base, uint64_t i, uint64_t 
     }
 }
 
+// A thread's 8 parameters and codes, and a block's scale bytes.
+template <bool FULL, int PD>
+__device__ __forceinline__ void store_packed(const PackedEntry& e, uint64_t at, uint64_t n, const Raw<PD, 8>& p,
+                                             u32x2 m, u32x2 v, uint32_t mscale, uint32_t vscale) {
+    store_at<FULL, true>(p, e.p_out, at, n);
+    store_codes<FULL>(e.m_out, at, n, m);
+    store_codes<FULL>(e.v_out, at, n, v);
+    if (threadIdx.x % 32 == 0 && (FULL || at < n)) {
+        e.ms_out[at / AR_STATE_BLOCK] = static_cast<uint8_t>(mscale);
+        e.vs_out[at / AR_STATE_BLOCK] = static_cast<uint8_t>(vscale);
+    }
+}
+
+// One element of the packed step.  The states that are kept are the formula's
+// bit for bit; the parameter's quotient takes the hardware's root and
+// reciprocal (within 1.6 half-ulps each, measured), unless EXACT: the root
+// takes a subnormal for 0, which only a tiny eps leaves visible.
+template <bool EXACT>
+__device__ __forceinline__ void packed_update(const AdamwScalars& s, float correction2, float factor, float g, float& p,
+                                              float& m, float& v) {
+    const float gs = factor * g;
+    m = m * s.beta1 + gs * s.one_minus_beta1;
+    v = v * s.beta2 + (gs * gs) * s.one_minus_beta2;
+    if constexpr (EXACT) {
+        const float d = sqrtf(v) * correction2 + s.eps;
+        p = p * s.decay - (m / d) * s.step_size;
+    } else {
+        const float d = __builtin_amdgcn_sqrtf(v) * correction2 + s.eps;
+        p = p * s.decay - (m * __builtin_amdgcn_rcpf(d)) * s.step_size;
+    }
+}
+
 // A thread has 8 neighbouring elements, half a wavefront a state block of 256:
 // the block's largest magnitude is a maximum over 32 lanes, with no LDS.
-template <int PD, int GD, bool FULL>
+template <int PD, int GD, bool FULL, bool EXACT>
 __device__ __forceinline__ void packed_tile(const PackedEntry& e, const AdamwScalars& s, uint64_t at, uint64_t n) {
     constexpr int V = 8;
     const uint64_t block = at / AR_STATE_BLOCK;
@@ -226,63 +266,73 @@ __device__ __forceinline__ void packed_tile(const PackedEntry& e, const AdamwSca
     const u32x2 mc = load_codes<FULL>(e.m, at, n), vc = load_codes<FULL>(e.v, at, n);
     const uint32_t me = live ? e.ms[block] : 0, ve = live ? e.vs[block] : 0;
     const Gate gt = gate(s);
-    const float mscale = scale_value(me), vscale = scale_value(ve);
+    if (gt.skip) {
+        if (PD == AR_FLOAT32 && e.copy != nullptr) {
+            float same[V];
+#pragma unroll
+            for (int j = 0; j < V; ++j) same[j] = p.get(j);
+            store_copy<FULL>(e.copy, s, at, n, same);
+        }
+        store_packed<FULL>(e, at, n, p, mc, vc, me, ve);
+        return;
+    }
+    // a block of NaN stays one, and takes its parameters along
+    const bool mbad = me == 255, vbad = ve == 255;
+    const float correction2 = mbad || vbad ? as_f(0x7fc00000u) : s.rsqrt_correction2;
     float pn[V], mn[V], vn[V];
-    uint32_t mtop = 0, vtop = 0;
+    float mtop = 0;
+    uint32_t vtop = 0;
 #pragma unroll
     for (int j = 0; j < V; ++j) {
         pn[j] = p.get(j);
-        mn[j] = decode<true>((mc[j / 4] >> (8 * (j % 4))) & 0xffu, mscale);
-        vn[j] = decode<false>((vc[j / 4] >> (8 * (j % 4))) & 0xffu, vscale);
-        if (!gt.skip) adamw_update(s, gt.factor, g.get(j), pn[j], mn[j], vn[j]);
+        mn[j] = decode<true>(mc[j / 4], j % 4, me);
+        vn[j] = decode<false>(vc[j / 4], j % 4, ve);
+        packed_update<EXACT>(s, correction2, gt.factor, g.get(j), pn[j], mn[j], vn[j]);
         // beyond the end there is nothing
         if (!FULL && at + j >= n) mn[j] = vn[j] = 0.0f;
-        const uint32_t mb = as_u(mn[j]) & 0x7fffffffu, vb = as_u(vn[j]) & 0x7fffffffu;
-        mtop = mb > mtop ? mb : mtop;
-        vtop = vb > vtop ? vb : vtop;
+        mtop = __builtin_fmaxf(mtop, __builtin_fabsf(mn[j]));
+        vtop = as_u(vn[j]) > vtop ? as_u(vn[j]) : vtop;   // v is never negative
     }
-    const uint32_t me_new = scale_for(max_over_lanes<32>(mtop)), ve_new = scale_for(max_over_lanes<32>(vtop));
-    const float minv = scale_inverse(me_new), vinv = scale_inverse(ve_new);
-    const uint32_t key = mix32(s.seed + 0x9e3779b9u * (e.index + 1));
-    u32x2 mo = {0, 0}, vo = {0, 0};
+    // The maximum of m passes over NaN.  One comes only with the gradient's, and
+    // that makes v, whose bits compare as integers, a NaN too.
+    vtop = max_over_lanes<32>(vtop);
+    const bool nan = vtop > 0x7f800000u;
+    const uint32_t me_new = mbad || nan ? 255 : scale_for(max_over_lanes<32>(as_u(mtop)));
+    const uint32_t ve_new = vbad ? 255 : scale_for(vtop);
+    const uint32_t key = mix32(s.seed + 0x9e3779b9u * (e.index + 1)) + 0x9e3779b9u * static_cast<uint32_t>(at);
+    uint32_t mo[V], vo[V], least = 0xffffffffu;
 #pragma unroll
     for (int j = 0; j < V; ++j) {
-        const uint32_t r = mix32(key + 0x9e3779b9u * static_cast<uint32_t>(at + j));
-        mo[j / 4] |= encode<true>(mn[j], minv, (r & 0xffffu) * 16 + 8) << (8 * (j % 4));
-        vo[j / 4] |= encode<false>(vn[j], vinv, (r >> 16) * 16 + 8) << (8 * (j % 4));
+        const uint32_t r = mix32(key + 0x9e3779b9u * j);
+        mo[j] = encode<true>(mn[j], me_new, (r << 4) & 0xffff0u);
+        vo[j] = encode<false>(vn[j], ve_new, (r >> 12) & 0xffff0u);
+        least = vo[j] < least ? vo[j] : least;
     }
-    if (me_new == 255) mo = u32x2{0, 0};
-    if (ve_new == 255) vo = u32x2{0, 0};
-    p.set_all(pn);
-    store_at<FULL, true>(p, e.p_out, at, n);
-    store_codes<FULL>(e.m_out, at, n, gt.skip ? mc : mo);
-    store_codes<FULL>(e.v_out, at, n, gt.skip ? vc : vo);
-    if (live && threadIdx.x % 32 == 0) {
-        e.ms_out[block] = static_cast<uint8_t>(gt.skip ? me : me_new);
-        e.vs_out[block] = static_cast<uint8_t>(gt.skip ? ve : ve_new);
-    }
-    if (PD == AR_FLOAT32 && e.copy != nullptr) {
-        if (s.copy_f16) {
-            Raw<AR_FLOAT16, V> c;
-            c.set_all(pn);
-            store_at<FULL, true>(c, e.copy, at, n);
-        } else {
-            Raw<AR_BFLOAT16, V> c;
-            c.set_all(pn);
-            store_at<FULL, true>(c, e.copy, at, n);
+    // a positive second moment is never rounded to 0: rare, so looked for first
+    if (__builtin_expect(__ballot(least < (1u << 24)) != 0, 0)) {
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+            if (vo[j] < (1u << 24) && vn[j] > 0.0f) vo[j] = 1u << 24;
         }
     }
+    u32x2 mw = {top_bytes(mo[0], mo[1], mo[2], mo[3]), top_bytes(mo[4], mo[5], mo[6], mo[7])};
+    u32x2 vw = {top_bytes(vo[0], vo[1], vo[2], vo[3]), top_bytes(vo[4], vo[5], vo[6], vo[7])};
+    if (me_new == 255) mw = u32x2{0, 0};
+    if (ve_new == 255) vw = u32x2{0, 0};
+    p.set_all(pn);
+    if (PD == AR_FLOAT32 && e.copy != nullptr) store_copy<FULL>(e.copy, s, at, n, pn);
+    store_packed<FULL>(e, at, n, p, mw, vw, me_new, ve_new);
 }
 
-template <int PD, int GD, class Table>
+template <int PD, int GD, bool EXACT, class Table>
 __global__ void __launch_bounds__(kStepThreads) k_adamw_packed(Table t, AdamwScalars s) {
     static_assert(kPackedTile == kStepThreads * 8, "one vector per thread");
     const PackedEntry e = find(t, blockIdx.x);
     const uint64_t tile = static_cast<uint64_t>(blockIdx.x - e.first_tile) * kPackedTile;
     if (tile + kPackedTile <= e.n) {
-        packed_tile<PD, GD, true>(e, s, tile + threadIdx.x * 8, e.n);
+        packed_tile<PD, GD, true, EXACT>(e, s, tile + threadIdx.x * 8, e.n);
     } else {
-        packed_tile<PD, GD, false>(e, s, tile + threadIdx.x * 8, e.n);
+        packed_tile<PD, GD, false, EXACT>(e, s, tile + threadIdx.x * 8, e.n);
     }
 }
 
@@ -293,10 +343,13 @@ __global__ void __launch_bounds__(kStepThreads) k_unpack(InlineTable<UnpackEntry
     const uint64_t at = static_cast<uint64_t>(blockIdx.x - e.first_tile) * kUnpackTile + threadIdx.x * 8;
     if (at >= e.n) return;
     const u32x2 c = load_codes<false>(e.codes, at, e.n);
-    const float scale = scale_value(e.scales[at / AR_STATE_BLOCK]);
+    const uint32_t scale = e.scales[at / AR_STATE_BLOCK];
     float x[8];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) x[j] = decode<SIGNED>((c[j / 4] >> (8 * (j % 4))) & 0xffu, scale);
+    for (int j = 0; j < 8; ++j) {
+        x[j] = decode<SIGNED>(c[j / 4], j % 4, scale);
+        if (scale == 255) x[j] = as_f(0x7fc00000u);
+    }
     Raw<DT, 8> r;
     r.set_all(x);
     store_at<false, true>(r, e.out, at, e.n);
@@ -346,19 +399,25 @@ hipError_t adamw_by_grad(const Table& t, uint32_t tiles, const AdamwScalars& s, 
     return hipGetLastError();
 }
 
+template <int PD, int GD, class Table>
+void packed_by_root(const Table& t, uint32_t tiles, const AdamwScalars& s, hipStream_t stream) {
+    // The hardware's root takes v below 2^-126 for 0, which moves the denominator
+    // by up to 2^-63 times the correction: at most half an ulp of this eps.
+    const bool exact = !(s.eps >= 0x1p-38f * s.rsqrt_correction2);
+    const dim3 grid(tiles), block(kStepThreads);
+    if (exact) {
+        hipLaunchKernelGGL((k_adamw_packed<PD, GD, true, Table>), grid, block, 0, stream, t, s);
+    } else {
+        hipLaunchKernelGGL((k_adamw_packed<PD, GD, false, Table>), grid, block, 0, stream, t, s);
+    }
+}
+
 template <int PD, class Table>
 hipError_t packed_by_grad(const Table& t, uint32_t tiles, const AdamwScalars& s, ar_dtype_t grad, hipStream_t stream) {
-    const dim3 grid(tiles), block(kStepThreads);
     switch (grad) {
-        case AR_FLOAT32:
-            hipLaunchKernelGGL((k_adamw_packed<PD, AR_FLOAT32, Table>), grid, block, 0, stream, t, s);
-            break;
-        case AR_BFLOAT16:
-            hipLaunchKernelGGL((k_adamw_packed<PD, AR_BFLOAT16, Table>), grid, block, 0, stream, t, s);
-            break;
-        case AR_FLOAT16:
-            hipLaunchKernelGGL((k_adamw_packed<PD, AR_FLOAT16, Table>), grid, block, 0, stream, t, s);
-            break;
+        case AR_FLOAT32: packed_by_root<PD, AR_FLOAT32>(t, tiles, s, stream); break;
+        case AR_BFLOAT16: packed_by_root<PD, AR_BFLOAT16>(t, tiles, s, stream); break;
+        case AR_FLOAT16: packed_by_root<PD, AR_FLOAT16>(t, tiles, s, stream); break;
         default: return hipErrorInvalidValue;
     }
     return hipGetLastError();
