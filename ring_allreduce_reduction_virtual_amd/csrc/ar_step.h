@@ -14,12 +14,38 @@ namespace arimpl {
 
 constexpr int kStepThreads = 256;   // threads per block: four 64-wide wavefronts
 
-// Elements per tile (one workgroup's share of one tensor).
+// Elements per tile (one workgroup's share of one tensor).  The AdamW steps'
+// threads take vectors of 4 (packed: 8) elements, one in the small form, two
+// or four in the large one.
 constexpr uint32_t kNormTile = 8192;
-constexpr uint32_t kAdamwTile = 4096;
-constexpr uint32_t kPackedTile = 2048;
+constexpr uint32_t kAdamwTile = kStepThreads * 4;
+constexpr uint32_t kPackedTile = kStepThreads * 8;
 constexpr uint32_t kUnpackTile = 2048;
 static_assert(kPackedTile % AR_STATE_BLOCK == 0 && kUnpackTile % AR_STATE_BLOCK == 0, "whole state blocks per tile");
+
+// The AdamW steps' two forms.  The small one reads with cache-allocating loads
+// and a vector per thread: more workgroups, and what the reduction, the norm
+// or the last step left in the 256 MB last-level cache is found there.  The
+// large one streams past the cache (nontemporal loads), with more vectors per
+// thread in flight.
+//
+// Float32 states: large above kAdamwLargeBytes read and written; two vectors,
+// or four when parameters and gradients are both float32.  Measured on MI355X,
+// us, small / two / four vectors: float32 29 MB 6.7 / 6.6 / 6.7, 117 MB 19.0 /
+// 21.5 / 21.3, 235 MB 43.2 / 41.5 / 41.3, 1.9 GB 346 / 313 / 314, 8 tensors of
+// 470 MB 681 / 655 / 631; float32 with bf16 gradients and copies 117 MB 20.7 /
+// 25.2 / 26.5, 235 MB 44.3 / 46.8 / 49.1, 1.9 GB 357 / 342 / 358; bf16 92 MB
+// 17.1 / 18.6 / 20.6, 184 MB 32.6 / 33.4 / 35.9, 1.5 GB 250 / 234 / 243.
+//
+// Packed states: two vectors from kPackedLargeElements when parameters and
+// gradients both have 16 bits; 32-bit ones fill a thread's loads with one.  us,
+// small / two vectors: bf16 2^22 elements 12.7 / 15.4, 2^23 18.9 / 19.5, 2^24
+// 37.2 / 35.5, 2^27 247 / 227; 2^26 float32 186 / 206, float32 with bf16
+// gradients and copies 187 / 206.
+constexpr uint64_t kAdamwLargeBytes = 128ull << 20;
+constexpr uint64_t kPackedLargeElements = 1ull << 24;
+constexpr int adamw_vectors(bool large, bool all_f32) { return large ? (all_f32 ? 4 : 2) : 1; }
+constexpr int packed_vectors(bool large) { return large ? 2 : 1; }
 
 // Most partial sums one launch of the gradient norm leaves (its workgroups).
 constexpr uint32_t kNormBlocks = 1024;
@@ -113,12 +139,15 @@ struct AdamwScalars {
 template <class Table>
 hipError_t launch_norm(const Table& t, uint32_t tiles, uint32_t blocks, ar_dtype_t dtype, double* partials,
                        float* norm, hipStream_t stream);
+// What the steps' kernels are chosen by.
+struct StepForm {
+    ar_dtype_t param, grad;
+    bool large;
+};
 template <class Table>
-hipError_t launch_adamw(const Table& t, uint32_t tiles, const AdamwScalars& s, ar_dtype_t param, ar_dtype_t grad,
-                        hipStream_t stream);
+hipError_t launch_adamw(const Table& t, uint32_t tiles, const AdamwScalars& s, const StepForm& f, hipStream_t stream);
 template <class Table>
-hipError_t launch_packed(const Table& t, uint32_t tiles, const AdamwScalars& s, ar_dtype_t param, ar_dtype_t grad,
-                         hipStream_t stream);
+hipError_t launch_packed(const Table& t, uint32_t tiles, const AdamwScalars& s, const StepForm& f, hipStream_t stream);
 hipError_t launch_unpack(const InlineTable<UnpackEntry>& t, uint32_t tiles, ar_state_t state, ar_dtype_t dtype,
                          hipStream_t stream);
 // *norm = sqrt(sum of `n` partial sums), in a fixed order.

@@ -231,8 +231,19 @@ using EntryOf = typename std::conditional<PACKED, PackedEntry, AdamwEntry>::type
 template <bool PACKED>
 constexpr uint32_t kTileOf = PACKED ? kPackedTile : kAdamwTile;
 
+// Which form the call's kernels take (the measurements stand at the bounds).
 template <bool PACKED>
-ar_result_t adamw_lines(const ar_adamw_tensors_t* a, Lines<EntryOf<PACKED>>& lines, std::vector<Range>& ranges) {
+bool large_step(const ar_adamw_tensors_t* a) {
+    uint64_t n = 0;
+    for (int t = 0; t < a->ntensors; ++t) n += a->counts[t];
+    if (PACKED) return a->param_dtype != AR_FLOAT32 && a->grad_dtype != AR_FLOAT32 && n >= kPackedLargeElements;
+    const uint64_t per = 2 * esize(a->param_dtype) + esize(a->grad_dtype) + (a->copies != nullptr ? 2 : 0) + 16;
+    return n * per > kAdamwLargeBytes;
+}
+
+template <bool PACKED>
+ar_result_t adamw_lines(const ar_adamw_tensors_t* a, Lines<EntryOf<PACKED>>& lines, std::vector<Range>& ranges,
+                        StepForm& form) {
     if (a == nullptr) return fail_with(AR_ERR_INVALID_ARGUMENT, "null tensors");
     if (!float_type(a->param_dtype) || !float_type(a->grad_dtype))
         return fail_with(AR_ERR_INVALID_ARGUMENT, "unsupported param dtype %d or grad dtype %d",
@@ -254,7 +265,9 @@ ar_result_t adamw_lines(const ar_adamw_tensors_t* a, Lines<EntryOf<PACKED>>& lin
     if (!PACKED && (a->exp_avg_scales != nullptr || a->exp_avg_sq_scales != nullptr ||
                     a->exp_avg_scales_out != nullptr || a->exp_avg_sq_scales_out != nullptr))
         return fail_with(AR_ERR_INVALID_ARGUMENT, "float32 states have no scales");
-    lines.tile = kTileOf<PACKED>;
+    form = {a->param_dtype, a->grad_dtype, large_step<PACKED>(a)};
+    const bool all_f32 = form.param == AR_FLOAT32 && form.grad == AR_FLOAT32;
+    lines.tile = kTileOf<PACKED> * static_cast<uint32_t>(PACKED ? packed_vectors(form.large) : adamw_vectors(form.large, all_f32));
     const size_t ps = esize(a->param_dtype), gs = esize(a->grad_dtype), ss = PACKED ? 1 : 4;
     for (int t = 0; t < a->ntensors; ++t) {
         const uint64_t n = a->counts[t];
@@ -297,12 +310,11 @@ ar_result_t adamw_lines(const ar_adamw_tensors_t* a, Lines<EntryOf<PACKED>>& lin
 }
 
 template <bool PACKED, class Table>
-hipError_t launch_step(const Table& t, uint32_t tiles, const AdamwScalars& s, ar_dtype_t param, ar_dtype_t grad,
-                       hipStream_t stream) {
+hipError_t launch_step(const Table& t, uint32_t tiles, const AdamwScalars& s, const StepForm& f, hipStream_t stream) {
     if constexpr (PACKED) {
-        return launch_packed(t, tiles, s, param, grad, stream);
+        return launch_packed(t, tiles, s, f, stream);
     } else {
-        return launch_adamw(t, tiles, s, param, grad, stream);
+        return launch_adamw(t, tiles, s, f, stream);
     }
 }
 
@@ -312,7 +324,8 @@ ar_result_t adamw_now(const ar_adamw_tensors_t* a, const ar_adamw_config_t* conf
     Lines<EntryOf<PACKED>> lines;
     std::vector<Range> ranges;
     AdamwScalars s;
-    ar_result_t rc = adamw_lines<PACKED>(a, lines, ranges);
+    StepForm form;
+    ar_result_t rc = adamw_lines<PACKED>(a, lines, ranges, form);
     if (rc != AR_SUCCESS || (rc = scalars(config, grad_norm, a->copy_dtype, &s)) != AR_SUCCESS) return rc;
     if (grad_norm != nullptr &&
         (rc = add_range(ranges, grad_norm, sizeof(float), alignof(float), false, "grad_norm", 0)) != AR_SUCCESS)
@@ -320,10 +333,11 @@ ar_result_t adamw_now(const ar_adamw_tensors_t* a, const ar_adamw_config_t* conf
     if ((rc = check_ranges(ranges)) != AR_SUCCESS) return rc;
     return in_launches(lines, PACKED ? "adamw_packed launch" : "adamw launch",
                        [&](const InlineTable<EntryOf<PACKED>>& t, uint32_t tiles, uint32_t) {
-                           return launch_step<PACKED>(t, tiles, s, a->param_dtype, a->grad_dtype, stream);
+                           return launch_step<PACKED>(t, tiles, s, form, stream);
                        });
 }
 
+// Room for a plan's table in either form: the small one has more tiles.
 template <bool PACKED>
 uint64_t adamw_workspace(const size_t* counts, int n) {
     uint64_t lines = 0, tiles = 0;
@@ -340,7 +354,8 @@ uint64_t adamw_workspace(const size_t* counts, int n) {
 struct ar_update_s {
     ar_update_kind_t kind;
     uint32_t tiles = 0;
-    ar_dtype_t param = AR_FLOAT32, grad = AR_FLOAT32, copy = AR_BFLOAT16;
+    StepForm form{AR_FLOAT32, AR_FLOAT32, false};   // a norm: the gradients' type only
+    ar_dtype_t copy = AR_BFLOAT16;
     float* norm = nullptr;
     double* partials = nullptr;
     DeviceTable<NormEntry> norm_table{};
@@ -356,7 +371,7 @@ ar_result_t start_norm(const ar_update_s& u, hipStream_t stream) {
     const uint32_t blocks = norm_blocks(u.tiles);
     ar_result_t rc = AR_SUCCESS;
     if (blocks > 0)
-        rc = hip_result(launch_norm(u.norm_table, u.tiles, blocks, u.grad, u.partials, blocks == 1 ? u.norm : nullptr,
+        rc = hip_result(launch_norm(u.norm_table, u.tiles, blocks, u.form.grad, u.partials, blocks == 1 ? u.norm : nullptr,
                                     stream),
                         "grad_norm launch");
     if (rc != AR_SUCCESS || blocks == 1) return rc;
@@ -380,13 +395,11 @@ template <bool PACKED>
 ar_result_t init_adamw(const ar_adamw_tensors_t* a, void* ws, size_t ws_bytes, hipStream_t stream, ar_update_s& u) {
     Lines<EntryOf<PACKED>> lines;
     std::vector<Range> ranges;
-    ar_result_t rc = adamw_lines<PACKED>(a, lines, ranges);
+    ar_result_t rc = adamw_lines<PACKED>(a, lines, ranges, u.form);
     if (rc != AR_SUCCESS ||
         (rc = add_workspace(ranges, ws, ws_bytes, adamw_workspace<PACKED>(a->counts, a->ntensors))) != AR_SUCCESS ||
         (rc = check_ranges(ranges)) != AR_SUCCESS)
         return rc;
-    u.param = a->param_dtype;
-    u.grad = a->grad_dtype;
     u.copy = a->copy_dtype;
     if (lines.e.empty()) return AR_SUCCESS;   // nothing to place: no device is asked
     if ((rc = refuse_capture(stream)) != AR_SUCCESS || (rc = check_device_memory(ranges)) != AR_SUCCESS) return rc;
@@ -490,7 +503,7 @@ ar_result_t ar_grad_norm_init(const void* const* grads, const size_t* counts, in
             if (rc != AR_SUCCESS || (rc = refuse_capture(stream)) != AR_SUCCESS ||
                 (rc = check_device_memory(ranges)) != AR_SUCCESS)
                 return rc;
-            u.grad = dtype;
+            u.form.grad = dtype;
             u.norm = norm;
             u.partials = static_cast<double*>(workspace);
             return upload(lines, static_cast<char*>(workspace) + kNormBlocks * sizeof(double), stream, &u.norm_table,
@@ -537,8 +550,8 @@ ar_result_t ar_adamw_start(ar_update_t update, const ar_adamw_config_t* config, 
         if (rc != AR_SUCCESS || update->tiles == 0) return rc;
         const ar_update_s& u = *update;
         return hip_result(u.kind == AR_UPDATE_ADAMW_PACKED
-                              ? launch_packed(u.packed_table, u.tiles, s, u.param, u.grad, stream)
-                              : launch_adamw(u.adamw_table, u.tiles, s, u.param, u.grad, stream),
+                              ? launch_packed(u.packed_table, u.tiles, s, u.form, stream)
+                              : launch_adamw(u.adamw_table, u.tiles, s, u.form, stream),
                           "adamw launch");
     });
 }

@@ -145,20 +145,20 @@ __device__ __forceinline__ void store_copy(char* copy, const AdamwScalars& s, ui
     }
 }
 
-template <int PD, int GD, bool FULL>
+template <int PD, int GD, bool LARGE, bool FULL>
 __device__ __forceinline__ void adamw_tile(const AdamwEntry& e, const AdamwScalars& s, uint64_t at, uint64_t n) {
     constexpr int V = 4;
-    constexpr int U = kAdamwTile / (kStepThreads * V);
+    constexpr int U = adamw_vectors(LARGE, PD == AR_FLOAT32 && GD == AR_FLOAT32);
     constexpr int kStep = kStepThreads * V;
     Raw<PD, V> p[U];
     Raw<GD, V> g[U];
     Raw<AR_FLOAT32, V> m[U], v[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-        load_at<FULL, true>(g[u], e.g, at + u * kStep, n);
-        load_at<FULL, true>(p[u], e.p, at + u * kStep, n);
-        load_at<FULL, true>(m[u], e.m, at + u * kStep, n);
-        load_at<FULL, true>(v[u], e.v, at + u * kStep, n);
+        load_at<FULL, LARGE>(g[u], e.g, at + u * kStep, n);
+        load_at<FULL, LARGE>(p[u], e.p, at + u * kStep, n);
+        load_at<FULL, LARGE>(m[u], e.m, at + u * kStep, n);
+        load_at<FULL, LARGE>(v[u], e.v, at + u * kStep, n);
     }
     const Gate gt = gate(s);
 #pragma unroll
@@ -184,14 +184,15 @@ __device__ __forceinline__ void adamw_tile(const AdamwEntry& e, const AdamwScala
     }
 }
 
-template <int PD, int GD, class Table>
+template <int PD, int GD, bool LARGE, class Table>
 __global__ void __launch_bounds__(kStepThreads) k_adamw(Table t, AdamwScalars s) {
+    constexpr uint32_t kTile = kAdamwTile * adamw_vectors(LARGE, PD == AR_FLOAT32 && GD == AR_FLOAT32);
     const AdamwEntry e = find(t, blockIdx.x);
-    const uint64_t tile = static_cast<uint64_t>(blockIdx.x - e.first_tile) * kAdamwTile;
-    if (tile + kAdamwTile <= e.n) {
-        adamw_tile<PD, GD, true>(e, s, tile + threadIdx.x * 4, e.n);
+    const uint64_t tile = static_cast<uint64_t>(blockIdx.x - e.first_tile) * kTile;
+    if (tile + kTile <= e.n) {
+        adamw_tile<PD, GD, LARGE, true>(e, s, tile + threadIdx.x * 4, e.n);
     } else {
-        adamw_tile<PD, GD, false>(e, s, tile + threadIdx.x * 4, e.n);
+        adamw_tile<PD, GD, LARGE, false>(e, s, tile + threadIdx.x * 4, e.n);
     }
 }
 
@@ -200,9 +201,9 @@ __global__ void __launch_bounds__(kStepThreads) k_adamw(Table t, AdamwScalars s)
 // ---------------------------------------------------------------------------
 
 // 8 codes at p, whole or up to the tensor's end.
-template <bool FULL>
+template <bool FULL, bool NT>
 __device__ __forceinline__ u32x2 load_codes(const uint8_t* base, uint64_t i, uint64_t n) {
-    if (FULL || i + 8 <= n) return load_as<true, u32x2_a1>(reinterpret_cast<const char*>(base + i));
+    if (FULL || i + 8 <= n) return load_as<NT, u32x2_a1>(reinterpret_cast<const char*>(base + i));
     u32x2 r = {0, 0};
     for (int j = 0; j < 8; ++j) {
         if (i + j < n) r[j / 4] |= static_cast<uint32_t>(base[i + j]) << (8 * (j % 4));
@@ -254,16 +255,16 @@ __device__ __forceinline__ void packed_update(const AdamwScalars& s, float corre
 
 // A thread has 8 neighbouring elements, half a wavefront a state block of 256:
 // the block's largest magnitude is a maximum over 32 lanes, with no LDS.
-template <int PD, int GD, bool FULL, bool EXACT>
+template <int PD, int GD, bool LARGE, bool EXACT, bool FULL>
 __device__ __forceinline__ void packed_tile(const PackedEntry& e, const AdamwScalars& s, uint64_t at, uint64_t n) {
     constexpr int V = 8;
     const uint64_t block = at / AR_STATE_BLOCK;
     const bool live = FULL || block * AR_STATE_BLOCK < n;
     Raw<PD, V> p;
     Raw<GD, V> g;
-    load_at<FULL, true>(g, e.g, at, n);
-    load_at<FULL, true>(p, e.p, at, n);
-    const u32x2 mc = load_codes<FULL>(e.m, at, n), vc = load_codes<FULL>(e.v, at, n);
+    load_at<FULL, LARGE>(g, e.g, at, n);
+    load_at<FULL, LARGE>(p, e.p, at, n);
+    const u32x2 mc = load_codes<FULL, LARGE>(e.m, at, n), vc = load_codes<FULL, LARGE>(e.v, at, n);
     const uint32_t me = live ? e.ms[block] : 0, ve = live ? e.vs[block] : 0;
     const Gate gt = gate(s);
     if (gt.skip) {
@@ -324,15 +325,19 @@ __device__ __forceinline__ void packed_tile(const PackedEntry& e, const AdamwSca
     store_packed<FULL>(e, at, n, p, mw, vw, me_new, ve_new);
 }
 
-template <int PD, int GD, bool EXACT, class Table>
+template <int PD, int GD, bool LARGE, bool EXACT, class Table>
 __global__ void __launch_bounds__(kStepThreads) k_adamw_packed(Table t, AdamwScalars s) {
-    static_assert(kPackedTile == kStepThreads * 8, "one vector per thread");
+    constexpr uint32_t kTile = kPackedTile * packed_vectors(LARGE);
     const PackedEntry e = find(t, blockIdx.x);
-    const uint64_t tile = static_cast<uint64_t>(blockIdx.x - e.first_tile) * kPackedTile;
-    if (tile + kPackedTile <= e.n) {
-        packed_tile<PD, GD, true, EXACT>(e, s, tile + threadIdx.x * 8, e.n);
-    } else {
-        packed_tile<PD, GD, false, EXACT>(e, s, tile + threadIdx.x * 8, e.n);
+    const uint64_t tile = static_cast<uint64_t>(blockIdx.x - e.first_tile) * kTile;
+    const bool full = tile + kTile <= e.n;
+#pragma unroll
+    for (uint32_t u = 0; u < kTile; u += kPackedTile) {
+        if (full) {
+            packed_tile<PD, GD, LARGE, EXACT, true>(e, s, tile + u + threadIdx.x * 8, e.n);
+        } else {
+            packed_tile<PD, GD, LARGE, EXACT, false>(e, s, tile + u + threadIdx.x * 8, e.n);
+        }
     }
 }
 
@@ -342,7 +347,7 @@ __global__ void __launch_bounds__(kStepThreads) k_unpack(InlineTable<UnpackEntry
     const UnpackEntry& e = find(t, blockIdx.x);
     const uint64_t at = static_cast<uint64_t>(blockIdx.x - e.first_tile) * kUnpackTile + threadIdx.x * 8;
     if (at >= e.n) return;
-    const u32x2 c = load_codes<false>(e.codes, at, e.n);
+    const u32x2 c = load_codes<false, true>(e.codes, at, e.n);
     const uint32_t scale = e.scales[at / AR_STATE_BLOCK];
     float x[8];
 #pragma unroll
@@ -387,37 +392,58 @@ hipError_t launch_norm_final(const double* partials, uint32_t n, float* norm, hi
 
 namespace {
 
-template <int PD, class Table>
-hipError_t adamw_by_grad(const Table& t, uint32_t tiles, const AdamwScalars& s, ar_dtype_t grad, hipStream_t stream) {
+template <int PD, int GD, class Table>
+void adamw_by_form(const Table& t, uint32_t tiles, const AdamwScalars& s, bool large, hipStream_t stream) {
     const dim3 grid(tiles), block(kStepThreads);
-    switch (grad) {
-        case AR_FLOAT32: hipLaunchKernelGGL((k_adamw<PD, AR_FLOAT32, Table>), grid, block, 0, stream, t, s); break;
-        case AR_BFLOAT16: hipLaunchKernelGGL((k_adamw<PD, AR_BFLOAT16, Table>), grid, block, 0, stream, t, s); break;
-        case AR_FLOAT16: hipLaunchKernelGGL((k_adamw<PD, AR_FLOAT16, Table>), grid, block, 0, stream, t, s); break;
+    if (large) {
+        hipLaunchKernelGGL((k_adamw<PD, GD, true, Table>), grid, block, 0, stream, t, s);
+    } else {
+        hipLaunchKernelGGL((k_adamw<PD, GD, false, Table>), grid, block, 0, stream, t, s);
+    }
+}
+
+template <int PD, class Table>
+hipError_t adamw_by_grad(const Table& t, uint32_t tiles, const AdamwScalars& s, const StepForm& f, hipStream_t stream) {
+    switch (f.grad) {
+        case AR_FLOAT32: adamw_by_form<PD, AR_FLOAT32>(t, tiles, s, f.large, stream); break;
+        case AR_BFLOAT16: adamw_by_form<PD, AR_BFLOAT16>(t, tiles, s, f.large, stream); break;
+        case AR_FLOAT16: adamw_by_form<PD, AR_FLOAT16>(t, tiles, s, f.large, stream); break;
         default: return hipErrorInvalidValue;
     }
     return hipGetLastError();
 }
 
-template <int PD, int GD, class Table>
+template <int PD, int GD, bool LARGE, class Table>
 void packed_by_root(const Table& t, uint32_t tiles, const AdamwScalars& s, hipStream_t stream) {
     // The hardware's root takes v below 2^-126 for 0, which moves the denominator
     // by up to 2^-63 times the correction: at most half an ulp of this eps.
     const bool exact = !(s.eps >= 0x1p-38f * s.rsqrt_correction2);
     const dim3 grid(tiles), block(kStepThreads);
     if (exact) {
-        hipLaunchKernelGGL((k_adamw_packed<PD, GD, true, Table>), grid, block, 0, stream, t, s);
+        hipLaunchKernelGGL((k_adamw_packed<PD, GD, LARGE, true, Table>), grid, block, 0, stream, t, s);
     } else {
-        hipLaunchKernelGGL((k_adamw_packed<PD, GD, false, Table>), grid, block, 0, stream, t, s);
+        hipLaunchKernelGGL((k_adamw_packed<PD, GD, LARGE, false, Table>), grid, block, 0, stream, t, s);
     }
 }
 
+template <int PD, int GD, class Table>
+void packed_by_form(const Table& t, uint32_t tiles, const AdamwScalars& s, bool large, hipStream_t stream) {
+    if constexpr (elem_size<PD>() == 2 && elem_size<GD>() == 2) {
+        if (large) {
+            packed_by_root<PD, GD, true>(t, tiles, s, stream);
+            return;
+        }
+    }
+    packed_by_root<PD, GD, false>(t, tiles, s, stream);
+}
+
 template <int PD, class Table>
-hipError_t packed_by_grad(const Table& t, uint32_t tiles, const AdamwScalars& s, ar_dtype_t grad, hipStream_t stream) {
-    switch (grad) {
-        case AR_FLOAT32: packed_by_root<PD, AR_FLOAT32>(t, tiles, s, stream); break;
-        case AR_BFLOAT16: packed_by_root<PD, AR_BFLOAT16>(t, tiles, s, stream); break;
-        case AR_FLOAT16: packed_by_root<PD, AR_FLOAT16>(t, tiles, s, stream); break;
+hipError_t packed_by_grad(const Table& t, uint32_t tiles, const AdamwScalars& s, const StepForm& f,
+                          hipStream_t stream) {
+    switch (f.grad) {
+        case AR_FLOAT32: packed_by_form<PD, AR_FLOAT32>(t, tiles, s, f.large, stream); break;
+        case AR_BFLOAT16: packed_by_form<PD, AR_BFLOAT16>(t, tiles, s, f.large, stream); break;
+        case AR_FLOAT16: packed_by_form<PD, AR_FLOAT16>(t, tiles, s, f.large, stream); break;
         default: return hipErrorInvalidValue;
     }
     return hipGetLastError();
@@ -437,23 +463,21 @@ hipError_t unpack_by_state(const InlineTable<UnpackEntry>& t, uint32_t tiles, ar
 }  // namespace
 
 template <class Table>
-hipError_t launch_adamw(const Table& t, uint32_t tiles, const AdamwScalars& s, ar_dtype_t param, ar_dtype_t grad,
-                        hipStream_t stream) {
-    switch (param) {
-        case AR_FLOAT32: return adamw_by_grad<AR_FLOAT32>(t, tiles, s, grad, stream);
-        case AR_BFLOAT16: return adamw_by_grad<AR_BFLOAT16>(t, tiles, s, grad, stream);
-        case AR_FLOAT16: return adamw_by_grad<AR_FLOAT16>(t, tiles, s, grad, stream);
+hipError_t launch_adamw(const Table& t, uint32_t tiles, const AdamwScalars& s, const StepForm& f, hipStream_t stream) {
+    switch (f.param) {
+        case AR_FLOAT32: return adamw_by_grad<AR_FLOAT32>(t, tiles, s, f, stream);
+        case AR_BFLOAT16: return adamw_by_grad<AR_BFLOAT16>(t, tiles, s, f, stream);
+        case AR_FLOAT16: return adamw_by_grad<AR_FLOAT16>(t, tiles, s, f, stream);
         default: return hipErrorInvalidValue;
     }
 }
 
 template <class Table>
-hipError_t launch_packed(const Table& t, uint32_t tiles, const AdamwScalars& s, ar_dtype_t param, ar_dtype_t grad,
-                         hipStream_t stream) {
-    switch (param) {
-        case AR_FLOAT32: return packed_by_grad<AR_FLOAT32>(t, tiles, s, grad, stream);
-        case AR_BFLOAT16: return packed_by_grad<AR_BFLOAT16>(t, tiles, s, grad, stream);
-        case AR_FLOAT16: return packed_by_grad<AR_FLOAT16>(t, tiles, s, grad, stream);
+hipError_t launch_packed(const Table& t, uint32_t tiles, const AdamwScalars& s, const StepForm& f, hipStream_t stream) {
+    switch (f.param) {
+        case AR_FLOAT32: return packed_by_grad<AR_FLOAT32>(t, tiles, s, f, stream);
+        case AR_BFLOAT16: return packed_by_grad<AR_BFLOAT16>(t, tiles, s, f, stream);
+        case AR_FLOAT16: return packed_by_grad<AR_FLOAT16>(t, tiles, s, f, stream);
         default: return hipErrorInvalidValue;
     }
 }
@@ -472,13 +496,13 @@ template hipError_t launch_norm(const InlineTable<NormEntry>&, uint32_t, uint32_
                                 hipStream_t);
 template hipError_t launch_norm(const DeviceTable<NormEntry>&, uint32_t, uint32_t, ar_dtype_t, double*, float*,
                                 hipStream_t);
-template hipError_t launch_adamw(const InlineTable<AdamwEntry>&, uint32_t, const AdamwScalars&, ar_dtype_t, ar_dtype_t,
+template hipError_t launch_adamw(const InlineTable<AdamwEntry>&, uint32_t, const AdamwScalars&, const StepForm&,
                                  hipStream_t);
-template hipError_t launch_adamw(const DeviceTable<AdamwEntry>&, uint32_t, const AdamwScalars&, ar_dtype_t, ar_dtype_t,
+template hipError_t launch_adamw(const DeviceTable<AdamwEntry>&, uint32_t, const AdamwScalars&, const StepForm&,
                                  hipStream_t);
-template hipError_t launch_packed(const InlineTable<PackedEntry>&, uint32_t, const AdamwScalars&, ar_dtype_t,
-                                  ar_dtype_t, hipStream_t);
-template hipError_t launch_packed(const DeviceTable<PackedEntry>&, uint32_t, const AdamwScalars&, ar_dtype_t,
-                                  ar_dtype_t, hipStream_t);
+template hipError_t launch_packed(const InlineTable<PackedEntry>&, uint32_t, const AdamwScalars&, const StepForm&,
+                                  hipStream_t);
+template hipError_t launch_packed(const DeviceTable<PackedEntry>&, uint32_t, const AdamwScalars&, const StepForm&,
+                                  hipStream_t);
 
 }  // namespace arimpl
