@@ -65,6 +65,7 @@ ar_result_t ar_layer_norm(const void* const* x, const void* const* gamma, const 
         if (rows == 0 || cols == 0) return AR_SUCCESS;
         const size_t es = esize(dtype), ws = esize(weight_dtype);
         std::vector<Range> v;
+        v.reserve(6 * static_cast<size_t>(nranks));
         for (int r = 0; r < nranks; ++r) {
             const bool in_place = x[r] == y[r] && x_stride == y_stride;
             if ((!in_place && (rc = add_rows(v, x[r], rows, cols, x_stride, es, false, "x", r)) != AR_SUCCESS) ||
@@ -125,6 +126,7 @@ ar_result_t ar_layer_norm_backward(const void* const* dy, const void* const* x, 
         const bool weights = dgamma != nullptr || dbeta != nullptr;
         const size_t es = esize(dtype), ws = esize(weight_dtype);
         std::vector<Range> v;
+        v.reserve(8 * static_cast<size_t>(nranks) + 1);
         for (int r = 0; r < nranks; ++r) {
             const bool in_place = dy[r] == dx[r] && dy_stride == dx_stride;
             if ((!in_place && (rc = add_rows(v, dy[r], rows, cols, dy_stride, es, false, "dy", r)) != AR_SUCCESS) ||

@@ -51,23 +51,34 @@ def _dtype_of(t, what):
     return name
 
 
+_PLAIN = (torch.Tensor, torch.nn.Parameter)
+
+
 def _pointers(tensors, dev, index, dtype, counts, what):
     """Addresses of contiguous tensors on `dev` of one dtype and the given element counts (None: any)."""
     n = len(tensors)
     if counts is not None and len(counts) != n:
         raise ValueError(f"need one of {what} per tensor")
-    arr = (ctypes.c_void_p * max(n, 1))()
-    for i, t in enumerate(tensors):
-        if not isinstance(t, torch.Tensor) or t.get_device() != index or not t.is_cuda:
-            raise ValueError(f"{what} must be tensors on {dev}")
-        if t.dtype is not dtype:
-            raise TypeError(f"{what} must have one dtype, {dtype}")
-        if not t.is_contiguous():
-            raise ValueError(f"{what} must be contiguous")
-        if counts is not None and t.numel() != counts[i]:
-            raise ValueError(f"{what}[{i}] must hold {counts[i]} elements")
-        arr[i] = t.data_ptr()
-    return arr
+    # one cheap test per tensor; what is wrong is found out below
+    at = [t.data_ptr() for t in tensors
+          if type(t) in _PLAIN and t.dtype is dtype and t.get_device() == index and t.is_contiguous()]
+    if len(at) != n or (counts is not None and [t.numel() for t in tensors] != counts):
+        for i, t in enumerate(tensors):
+            _refuse(t, dev, index, dtype, None if counts is None else counts[i], what, i)
+        at = [t.data_ptr() for t in tensors]
+    return (ctypes.c_void_p * max(n, 1))(*at)
+
+
+def _refuse(t, dev, index, dtype, count, what, i):
+    """Raise what is wrong with a tensor, if anything is (a subclass of torch.Tensor may be as good)."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda or t.get_device() != index:
+        raise ValueError(f"{what} must be tensors on {dev}")
+    if t.dtype is not dtype:
+        raise TypeError(f"{what} must have one dtype, {dtype}")
+    if not t.is_contiguous():
+        raise ValueError(f"{what} must be contiguous")
+    if count is not None and t.numel() != count:
+        raise ValueError(f"{what}[{i}] must hold {count} elements")
 
 
 def _counts(sizes):
@@ -155,9 +166,10 @@ def _config(step, lr, betas, eps, weight_decay, max_norm, grad_scale, skip_nonfi
 def _states(states, packed, what):
     """The tensors of a state list: (values, None), or (codes, scales) when packed."""
     if not packed:
-        return list(states), None
-    if not all(isinstance(s, (tuple, list)) and len(s) == 2 for s in states):
-        raise ValueError(f"{what} must be PackedState pairs of codes and scales")
+        return states, None
+    for s in states:
+        if type(s) is not PackedState and not (isinstance(s, (tuple, list)) and len(s) == 2):
+            raise ValueError(f"{what} must be PackedState pairs of codes and scales")
     return [s[0] for s in states], [s[1] for s in states]
 
 
@@ -387,30 +399,48 @@ def ar_update_free(update: Update):
 # layer norm
 # --------------------------------------------------------------------------
 
-def _row_pointers(tensors, n, dev, index, dtype, shape, what):
+def _row_pointers(tensors, n, dev, index, dtype, rows, cols, what):
     """Addresses and common row stride of one [rows, cols] tensor per rank, rows contiguous."""
     if len(tensors) != n:
         raise ValueError(f"need one of {what} per rank")
-    arr = (ctypes.c_void_p * n)()
-    rows, cols = shape
-    stride = None
-    for i, t in enumerate(tensors):
-        if not isinstance(t, torch.Tensor) or not t.is_cuda or t.get_device() != index:
-            raise ValueError(f"{what} must be tensors on {dev}")
-        if t.dtype is not dtype:
-            raise TypeError(f"{what} must have one dtype, {dtype}")
-        if t.shape != shape:
-            raise ValueError(f"{what} must be [{rows}, {cols}] tensors, one per rank")
-        s = t.stride()
-        if (cols > 1 and s[1] != 1) or (rows > 1 and s[0] < cols):
-            raise ValueError(f"{what} must have contiguous rows that do not overlap")
-        if rows > 1:
-            if stride is None:
-                stride = s[0]
-            elif s[0] != stride:
-                raise ValueError(f"{what} must have one row stride")
-        arr[i] = t.data_ptr()
-    return arr, cols if stride is None else stride
+    shape = (rows, cols)
+    # one cheap test per tensor; what is wrong is found out below
+    at = [t.data_ptr() for t in tensors
+          if type(t) is torch.Tensor and t.dtype is dtype and t.get_device() == index and t.shape == shape]
+    if len(at) != n:
+        for t in tensors:
+            if not isinstance(t, torch.Tensor) or not t.is_cuda or t.get_device() != index:
+                raise ValueError(f"{what} must be tensors on {dev}")
+            if t.dtype is not dtype:
+                raise TypeError(f"{what} must have one dtype, {dtype}")
+            if t.shape != shape:
+                raise ValueError(f"{what} must be [{rows}, {cols}] tensors, one per rank")
+        at = [t.data_ptr() for t in tensors]
+    strides = {t.stride() for t in tensors}
+    if any((cols > 1 and s[1] != 1) or (rows > 1 and s[0] < cols) for s in strides):
+        raise ValueError(f"{what} must have contiguous rows that do not overlap")
+    stride = cols
+    if rows > 1:
+        stride = next(iter(strides))[0]
+        if any(s[0] != stride for s in strides):
+            raise ValueError(f"{what} must have one row stride")
+    return (ctypes.c_void_p * n)(*at), stride
+
+
+def _rank_rows(n, rows, cols, dtype, dev, stream):
+    """A new [rows, cols] tensor per rank, and their addresses."""
+    whole = _empty((n, rows, cols), dtype, dev, stream)
+    at, step = whole.data_ptr(), rows * cols * whole.element_size()
+    return list(whole.unbind(0)), (ctypes.c_void_p * n)(*range(at, at + n * step, step) if step else [at] * n)
+
+
+def _rank_vectors(n, length, dtype, dev, stream):
+    """Two new vectors per rank, and the addresses of both sets."""
+    whole = _empty((2 * n, length), dtype, dev, stream)
+    at, step = whole.data_ptr(), length * whole.element_size()
+    ptrs = list(range(at, at + 2 * n * step, step)) if step else [at] * (2 * n)
+    parts = whole.unbind(0)
+    return list(parts[:n]), list(parts[n:]), (ctypes.c_void_p * n)(*ptrs[:n]), (ctypes.c_void_p * n)(*ptrs[n:])
 
 
 def _rank_list(tensors, what):
@@ -428,8 +458,14 @@ def _weights(tensors, n, dev, index, dtype, cols, what):
     return _pointers(tensors, dev, index, dtype, [cols] * n, what)
 
 
-def _split(t):
-    return list(t.unbind(0))
+def _weight_dtype(dtype, *lists):
+    """The weights' type: that of the first list given, else the activations'."""
+    for w in lists:
+        if w is not None and len(w):
+            if w[0].dtype is not dtype and w[0].dtype is not torch.float32:
+                raise TypeError("the weights have the activations' type or float32")
+            return w[0].dtype
+    return dtype
 
 
 def ar_layer_norm(xs, gammas=None, betas=None, ys=None, eps: float = 1e-5, stats: bool = True, stream=None):
@@ -445,23 +481,17 @@ def ar_layer_norm(xs, gammas=None, betas=None, ys=None, eps: float = 1e-5, stats
     n, dev, index, dt = len(xs), x0.device, x0.get_device(), x0.dtype
     name = _dtype_of(x0, "xs")
     rows, cols = x0.shape
-    xp, x_stride = _row_pointers(xs, n, dev, index, dt, x0.shape, "xs")
-    wdt = gammas[0].dtype if gammas is not None and len(gammas) else \
-        betas[0].dtype if betas is not None and len(betas) else dt
-    if wdt is not dt and wdt is not torch.float32:
-        raise TypeError("the weights have the activations' type or float32")
+    xp, x_stride = _row_pointers(xs, n, dev, index, dt, rows, cols, "xs")
+    wdt = _weight_dtype(dt, gammas, betas)
     gp = None if gammas is None else _weights(gammas, n, dev, index, wdt, cols, "gammas")
     bp = None if betas is None else _weights(betas, n, dev, index, wdt, cols, "betas")
     if ys is None:
-        ys = _split(_empty((n, rows, cols), dt, dev, stream))
-    yp, y_stride = _row_pointers(ys, n, dev, index, dt, x0.shape, "ys")
+        (ys, yp), y_stride = _rank_rows(n, rows, cols, dt, dev, stream), cols
+    else:
+        yp, y_stride = _row_pointers(ys, n, dev, index, dt, rows, cols, "ys")
     means = rstds = mp = rp = None
     if stats:
-        both = _empty((2, n, rows), torch.float32, dev, stream)
-        at = both.data_ptr()
-        mp = (ctypes.c_void_p * n)(*[at + 4 * rows * r for r in range(n)])
-        rp = (ctypes.c_void_p * n)(*[at + 4 * rows * (n + r) for r in range(n)])
-        means, rstds = _split(both[0]), _split(both[1])
+        means, rstds, mp, rp = _rank_vectors(n, rows, torch.float32, dev, stream)
     with _on_device(dev):
         rc = _lib.lib().ar_layer_norm(xp, gp, bp, yp, mp, rp, rows, cols, x_stride, y_stride, _lib.DTYPES[name],
                                       _lib.DTYPES[_FLOATS[wdt]], eps, n, _stream_handle(stream, dev.index))
@@ -489,26 +519,26 @@ def ar_layer_norm_backward(dys, xs, gammas, means, rstds, dxs=None, weight_grads
     n, dev, index, dt = len(xs), x0.device, x0.get_device(), x0.dtype
     name = _dtype_of(x0, "xs")
     rows, cols = x0.shape
-    xp, x_stride = _row_pointers(xs, n, dev, index, dt, x0.shape, "xs")
-    dyp, dy_stride = _row_pointers(dys, n, dev, index, dt, x0.shape, "dys")
-    given = next((w for w in (gammas, dgammas, dbetas) if w is not None and len(w)), None)
-    wdt = dt if given is None else given[0].dtype
-    if wdt is not dt and wdt is not torch.float32:
-        raise TypeError("the weights have the activations' type or float32")
+    xp, x_stride = _row_pointers(xs, n, dev, index, dt, rows, cols, "xs")
+    dyp, dy_stride = _row_pointers(dys, n, dev, index, dt, rows, cols, "dys")
+    wdt = _weight_dtype(dt, gammas, dgammas, dbetas)
     gp = None if gammas is None else _weights(gammas, n, dev, index, wdt, cols, "gammas")
     if len(means) != n or len(rstds) != n:
         raise ValueError("need one of means and rstds per rank")
     mp = _pointers(means, dev, index, torch.float32, [rows] * n, "means")
     rp = _pointers(rstds, dev, index, torch.float32, [rows] * n, "rstds")
     if dxs is None:
-        dxs = _split(_empty((n, rows, cols), dt, dev, stream))
-    dxp, dx_stride = _row_pointers(dxs, n, dev, index, dt, x0.shape, "dxs")
-    if weight_grads and (dgammas is None or dbetas is None):
-        both = _empty((2, n, cols), wdt, dev, stream)
-        dgammas = _split(both[0]) if dgammas is None else dgammas
-        dbetas = _split(both[1]) if dbetas is None else dbetas
-    gout = None if dgammas is None else _weights(dgammas, n, dev, index, wdt, cols, "dgammas")
-    bout = None if dbetas is None else _weights(dbetas, n, dev, index, wdt, cols, "dbetas")
+        (dxs, dxp), dx_stride = _rank_rows(n, rows, cols, dt, dev, stream), cols
+    else:
+        dxp, dx_stride = _row_pointers(dxs, n, dev, index, dt, rows, cols, "dxs")
+    if weight_grads and dgammas is None and dbetas is None:
+        dgammas, dbetas, gout, bout = _rank_vectors(n, cols, wdt, dev, stream)
+    else:
+        if weight_grads:
+            made = list(_empty((n, cols), wdt, dev, stream).unbind(0))
+            dgammas, dbetas = made if dgammas is None else dgammas, made if dbetas is None else dbetas
+        gout = None if dgammas is None else _weights(dgammas, n, dev, index, wdt, cols, "dgammas")
+        bout = None if dbetas is None else _weights(dbetas, n, dev, index, wdt, cols, "dbetas")
     with _on_device(dev):
         if gout is not None or bout is not None:
             workspace = _scratch(ar_layer_norm_workspace_bytes(rows, cols, n), workspace, dev, stream)
