@@ -43,34 +43,72 @@ struct NormBackwardArgs {
     uint32_t blocks;                 // partial sums per rank
 };
 
-// How a row lies over threads: `threads` threads a row, each holding `each` of
-// its elements in registers; each == 0: the row does not fit and is read again
-// for every pass (the wide form).  The narrowest form that holds the row: lanes
-// without elements would idle, and more elements per thread mean fewer lanes
-// to combine.
+// How a row lies over threads: `threads` threads a row, each holding `vectors`
+// 16-byte vectors of it in registers; vectors == 0: the row does not fit and is
+// read again for every pass (the wide form).
 struct RowShape {
-    int threads, each;
+    int threads, vectors;
 };
-constexpr uint64_t kWidestRow = 16384;   // elements held in registers at most
-inline RowShape row_shape(uint64_t cols) {
-    if (cols <= 128) return {16, 8};
-    if (cols <= 512) return {64, 8};
-    if (cols <= 1024) return {64, 16};
-    if (cols <= 2048) return {64, 32};
-    if (cols <= 4096) return {256, 16};
-    if (cols <= 8192) return {256, 32};
-    if (cols <= kWidestRow) return {1024, 16};
+
+// Threads of a workgroup, and the rows that it works on at a time: four
+// wavefronts of short rows, or one long row.
+constexpr int block_threads(int threads_per_row) { return threads_per_row <= 64 ? 256 : threads_per_row; }
+constexpr int rows_at_once(int threads_per_row) { return block_threads(threads_per_row) / threads_per_row; }
+
+// The forward pass: as few threads as hold the row, so that short rows leave no
+// lanes idle and rows of up to a wavefront's registers need no barrier.
+// Measured on MI355X, 2^26 bf16 elements on 8 ranks (45.5 us at 5.9 TB/s), us:
+// 64 columns 8x1 51, 16x1 90; 256 32x1 52, 64x1 75; 1,024 64x2 51.6, 128x1
+// 50.2, 256x1 72; 2,048 64x4 48.0, 256x1 48.9, 512x1 72; 4,096 128x4 47.4,
+// 256x2 49.8, 1024x1 80; 8,192 256x4 48.5, 512x2 49.6, wide 77; 16,384 1024x2
+// 53.9, 512x4 59.
+// float32, 2^25 elements: 1,024 64x4 45.7; 4,096 256x4 47.4; 8,192 1024x2 47.7,
+// 512x4 48.9; 16,384 1024x4 50.2, wide 72.
+inline RowShape forward_shape(uint64_t cols, int vector_elements) {
+    const uint64_t need = (cols + vector_elements - 1) / vector_elements;
+    if (need <= 8) return {8, 1};
+    if (need <= 16) return {16, 1};
+    if (need <= 32) return {32, 1};
+    if (need <= 64) return {64, 1};
+    if (need <= 128) return {64, 2};
+    if (need <= 256) return {64, 4};
+    if (need <= 512) return {128, 4};
+    if (need <= 1024) return {256, 4};
+    if (need <= 2048) return {1024, 2};
+    if (need <= 4096 && vector_elements == 4) return {1024, 4};
     return {1024, 0};
 }
-// Rows that one workgroup works on at a time (256 threads, or one row).
-constexpr int rows_at_once(int threads_per_row) { return threads_per_row < 256 ? 256 / threads_per_row : 1; }
 
-// Partial sums of dgamma and dbeta that a rank's backward pass leaves: one a
-// workgroup.  Together the ranks start about kBackwardBlocks workgroups.
-constexpr uint32_t kBackwardBlocks = 512;
-inline uint32_t backward_blocks(uint64_t rows, uint64_t cols, int nranks) {
-    const uint64_t all = (rows + rows_at_once(row_shape(cols).threads) - 1) / rows_at_once(row_shape(cols).threads);
-    return static_cast<uint32_t>(std::min<uint64_t>(all, std::max(1, static_cast<int>(kBackwardBlocks) / nranks)));
+// The backward pass holds each column's two sums besides the row: fewer
+// vectors a thread.  Same sizes (68.4 us at 5.9 TB/s), bf16, us: 64 columns 8x1
+// 74, 16x1 107; 256 32x1 76, 64x1 90; 1,024 128x1 78, 64x2 82, 256x1 88; 2,048
+// 256x1 79, 128x2 91, 64x4 94; 4,096 256x2 80, 512x1 80, 128x4 85, 1024x1 103;
+// 8,192 512x2 89, 1024x1 91, 256x4 102, wide 158; float32: 1,024 256x1 78,
+// 128x2 75; 4,096 512x2 80; 8,192 512x4 87, wide 143.
+inline RowShape backward_shape(uint64_t cols, int vector_elements) {
+    const uint64_t need = (cols + vector_elements - 1) / vector_elements;
+    if (need <= 8) return {8, 1};
+    if (need <= 16) return {16, 1};
+    if (need <= 32) return {32, 1};
+    if (need <= 64) return {64, 1};
+    if (need <= 128) return {128, 1};
+    if (need <= 256) return {256, 1};
+    if (need <= 512) return {256, 2};
+    if (need <= 1024) return {512, 2};
+    if (need <= 2048) return {512, 4};
+    if (need <= 4096 && vector_elements == 4) return {512, 8};
+    return {1024, 0};
+}
+
+// Workgroups of a rank's backward pass; each leaves one partial sum of dgamma
+// and dbeta per column.  All ranks together: enough to fill the GPU, more when
+// every one still has 64 rows, over which its partial sums' traffic is small.
+constexpr uint64_t kBackwardBlocks = 512, kBackwardMostBlocks = 4096, kBackwardRows = 64;
+inline uint32_t backward_blocks(uint64_t rows, uint64_t cols, int nranks, int vector_elements) {
+    const int at_once = rows_at_once(backward_shape(cols, vector_elements).threads);
+    const uint64_t wanted =
+        std::min(kBackwardMostBlocks, std::max(kBackwardBlocks, rows * nranks / kBackwardRows)) / nranks;
+    return static_cast<uint32_t>(std::min<uint64_t>((rows + at_once - 1) / at_once, std::max<uint64_t>(1, wanted)));
 }
 
 hipError_t launch_norm_forward(const NormForwardArgs& a, int nranks, ar_dtype_t dtype, ar_dtype_t weight,

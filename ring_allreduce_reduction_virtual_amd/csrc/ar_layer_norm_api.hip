@@ -105,7 +105,8 @@ ar_result_t ar_layer_norm(const void* const* x, const void* const* gamma, const 
 
 size_t ar_layer_norm_workspace_bytes(size_t rows, size_t cols, int nranks) {
     if (nranks < 1 || nranks > AR_MAX_RANKS || rows > kMaxRows || cols > kMaxCols) return static_cast<size_t>(-1);
-    return static_cast<size_t>(nranks) * backward_blocks(rows, cols, nranks) * 2 * cols * sizeof(float);
+    const uint32_t blocks = std::max(backward_blocks(rows, cols, nranks, 4), backward_blocks(rows, cols, nranks, 8));
+    return static_cast<size_t>(nranks) * blocks * 2 * cols * sizeof(float);
 }
 
 ar_result_t ar_layer_norm_backward(const void* const* dy, const void* const* x, const void* const* gamma,
@@ -142,7 +143,7 @@ ar_result_t ar_layer_norm_backward(const void* const* dy, const void* const* x, 
                 (dbeta != nullptr && (rc = add_range(v, dbeta[r], cols * ws, ws, true, "dbeta", r)) != AR_SUCCESS))
                 return rc;
         }
-        const uint32_t blocks = backward_blocks(rows, cols, nranks);
+        const uint32_t blocks = backward_blocks(rows, cols, nranks, 16 / static_cast<int>(es));
         if (weights) {
             const uint64_t need = ar_layer_norm_workspace_bytes(rows, cols, nranks);
             if (need > 0 && (workspace == nullptr || workspace_bytes < need))

@@ -129,6 +129,16 @@ struct Raw {
             }
         }
     }
+    // all but the first `skip`
+    __device__ __forceinline__ void store_from(char* p, int skip) const {
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+            if (j >= skip) {
+                const uint32_t h = elem_size<DT>() == 4 ? w[j * elem_size<DT>() / 4] : w[j / 2] >> (16 * (j % 2));
+                store_elem<elem_size<DT>(), false>(p + j * elem_size<DT>(), h);
+            }
+        }
+    }
     __device__ __forceinline__ float get(int j) const {
         if constexpr (elem_size<DT>() == 4) {
             return as_f(w[j]);
@@ -177,6 +187,7 @@ __device__ __forceinline__ uint32_t dpp(uint32_t x) {
 }
 constexpr int kDppXor1 = 0xB1, kDppXor2 = 0x4E;             // quad permutations 1,0,3,2 and 2,3,0,1
 constexpr int kDppHalfMirror = 0x141, kDppMirror = 0x140;   // lanes of 8 and of 16 reversed
+constexpr int kDppRotate8 = 0x128;                          // 16 lanes turned by 8
 
 // The same lane's value in the other 16 (other 32) lanes, given that f combines
 // a pair regardless of its order.
@@ -191,7 +202,7 @@ __device__ __forceinline__ uint32_t across32(uint32_t x, F f) {
     return f(s[0], s[1]);
 }
 
-// f over each group of LANES (16, 32 or 64) neighbouring lanes, in every lane.
+// f over each group of LANES (8, 16, 32 or 64) neighbouring lanes, in every lane.
 // After two exchanges the four lanes of a quad agree, so a mirrored half row
 // brings the other quad's value, and a mirrored row the other half's.
 template <int LANES, class F>
@@ -199,7 +210,7 @@ __device__ __forceinline__ uint32_t over_lanes(uint32_t x, F f) {
     x = f(x, dpp<kDppXor1>(x));
     x = f(x, dpp<kDppXor2>(x));
     x = f(x, dpp<kDppHalfMirror>(x));
-    x = f(x, dpp<kDppMirror>(x));
+    if constexpr (LANES >= 16) x = f(x, dpp<kDppMirror>(x));
     if constexpr (LANES >= 32) x = across16(x, f);
     if constexpr (LANES >= 64) x = across32(x, f);
     return x;

@@ -360,3 +360,22 @@ def test_refusals(ar):
         ar.ar_layer_norm_backward([z(3, 8)], x, None, st + st, st)
     with pytest.raises(ar.ArError, match="workspace"):
         ar.ar_layer_norm_backward([z(3, 8)], x, None, st, st, workspace=torch.zeros(4, dtype=torch.uint8, device="cuda"))
+
+
+@pytest.mark.parametrize("cols", [31, 32, 33, 64, 65, 255, 256, 257, 767, 2047, 4096, 8191, 16383])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_bounds_of_the_row_forms(ar, dtype, cols):
+    """Widths at and beside the forms' bounds, with enough rows that every workgroup takes several."""
+    torch = _torch()
+    rng = np.random.default_rng(cols)
+    rows, n = (1500, 2) if cols < 1024 else (40, 2)
+    xs = make(rng, n, rows, cols, dtype, 1, 1.2, -0.3)
+    gammas = [t[0].clone() for t in make(rng, n, 1, cols, dtype, 0, 0.3, 1.0)]
+    _, means, rstds = check_forward(ar, xs, gammas, gammas, dtype)
+    dys = make(rng, n, rows, cols, dtype, 3)
+    dxs, _, _ = check_backward(ar, dys, xs, gammas, means, rstds, dtype, dtype)
+    # nothing is written beside the rows
+    wide = [torch.full((rows, cols + 9), 3.0, dtype=torch_dtype(dtype), device="cuda") for _ in range(n)]
+    ar.ar_layer_norm_backward(dys, xs, gammas, means, rstds, dxs=[w[:, 4:cols + 4] for w in wide])
+    for w, d in zip(wide, dxs):
+        assert torch.equal(w[:, 4:cols + 4], d) and (w[:, :4] == 3).all() and (w[:, cols + 4:] == 3).all()
