@@ -581,3 +581,89 @@ def test_binding_refusals(ar):
         step.start(seed=1, **good)
     with pytest.raises(ValueError):
         ar.ar_grad_norm_start(step)
+
+
+@pytest.mark.parametrize("eps", [0.0, 1e-20, 1e-13, 1e-8])
+def test_packed_tiny_gradients(ar, eps):
+    """Second moments down to float32's subnormals: the parameter moves as the formula says, for every eps.
+
+    Where the hardware's root would take such a moment for 0 the step must
+    not use it; the parameter is then the float32 formula's bit for bit.
+    """
+    torch = _torch()
+    n, lr = 600, 0.25
+    g = np.geomspace(1e-22, 1e-14, n).astype(np.float32)
+    p = torch.zeros(n, device="cuda")
+    m, v = (ar.PackedState.zeros(n, "cuda") for _ in range(2))
+    ar.ar_adamw_packed([p], [torch.from_numpy(g).cuda()], [m], [v], step=1, lr=lr, eps=eps, seed=0)
+    zero = np.zeros(n, np.float32)
+    m32, v32 = oracle.moments_f32(g, zero, zero, (0.9, 0.999), 1.0)
+    f = np.float32
+    with np.errstate(all="ignore"):
+        d = np.sqrt(v32) * f(1 / math.sqrt(1 - 0.999)) + f(eps)
+        want = zero * f(1) - (m32 / d) * f(lr / (1 - 0.9))
+    got = f32(p)
+    if eps < 1e-10:
+        assert np.array_equal(got, want)
+    # root, its product, the sum, reciprocal, product, step size: 2 + 1 + 1 + 2 + 1 + 1 half-ulps, twice over
+    assert np.allclose(got, want, rtol=16 * 2.0 ** -24, atol=1e-30)
+
+
+def test_packed_blocks_of_nan_stay_with_their_own(ar):
+    """A NaN block of one state keeps NaN there and in its parameters; the other state and other blocks go on."""
+    torch = _torch()
+    n = 1024
+    p, g = torch.zeros(n, device="cuda"), torch.ones(n, device="cuda")
+    for bad in (0, 1):
+        states = [ar.PackedState.zeros(n, "cuda") for _ in range(2)]
+        states[bad].scales[2] = 255
+        q = p.clone()
+        ar.ar_adamw_packed([q], [g], [states[0]], [states[1]], step=1, lr=0.5, seed=3)
+        block = slice(512, 768)
+        assert torch.isnan(q[block]).all() and int(torch.isnan(q).sum()) == 256
+        scales = [s.scales.tolist() for s in states]
+        assert scales[bad][2] == 255 and 255 not in scales[bad][:2] + scales[bad][3:] + scales[1 - bad]
+        other = ar.ar_unpack_states([states[1 - bad]], ("exp_avg", "exp_avg_sq")[1 - bad])[0]
+        assert torch.isfinite(other).all() and (other > 0).all()
+
+
+def test_packed_is_the_same_bits_every_time_and_follows_its_seed(ar):
+    torch = _torch()
+    g = torch.randn(100_003, device="cuda")
+    got = []
+    for seed in (1, 1, 2):
+        p = torch.zeros_like(g)
+        m, v = (ar.PackedState.zeros(g.numel(), "cuda") for _ in range(2))
+        for t in (1, 2):
+            ar.ar_adamw_packed([p], [g], [m], [v], step=t, lr=0.1, seed=seed)
+        got.append((p, m.codes, v.codes))
+    assert all(torch.equal(a, b) for a, b in zip(got[0], got[1]))
+    assert (got[0][1] != got[2][1]).any() and (got[0][2] != got[2][2]).any()
+
+
+@pytest.mark.parametrize("param,grad", [("f32", "f32"), ("f32", "bf16"), ("bf16", "bf16"), ("f16", "f16")])
+def test_large_forms_agree_with_small_ones(ar, param, grad):
+    """A tensor in a call large enough for the other kernel form gets the bits that it gets alone."""
+    torch = _torch()
+    sizes = [25_000_003, 70_001, 9]
+    torch.manual_seed(0)
+    ps = [torch.randn(n, device="cuda").to(torch_dtype(param)) for n in sizes]
+    gs = [torch.randn(n, device="cuda").to(torch_dtype(grad)) for n in sizes]
+    ms, vs = ([torch.randn(n, device="cuda") for n in sizes] for _ in range(2))
+    vs = [v.abs_() for v in vs]
+    alone = [[t[k:k + 1] for t in ([x.clone() for x in ps], gs, [x.clone() for x in ms], [x.clone() for x in vs])]
+             for k in (1, 2)]
+    ar.ar_adamw(ps, gs, ms, vs, **HYPER)
+    for k, a in zip((1, 2), alone):
+        ar.ar_adamw(*a, **HYPER)
+        assert torch.equal(a[0][0], ps[k]) and torch.equal(a[2][0], ms[k]) and torch.equal(a[3][0], vs[k])
+    pm, pv = ([ar.PackedState.zeros(n, "cuda") for n in sizes] for _ in range(2))
+    ar.ar_adamw_packed(ps, gs, pm, pv, seed=4, **HYPER)
+    for k in (1, 2):
+        want = oracle.moments_f32(f32(gs[k])[:600], np.zeros(min(600, sizes[k]), np.float32),
+                                  np.zeros(min(600, sizes[k]), np.float32), HYPER["betas"], 1.0)
+        for state, x, kind in ((pm[k], want[0], "exp_avg"), (pv[k], want[1], "exp_avg_sq")):
+            codes, scales = oracle.pack(x, oracle.random_bits(4, k, x.size), kind)
+            whole = x.size // 256 * 256 if x.size == 600 else x.size
+            assert np.array_equal(state.codes.cpu().numpy()[:whole], codes[:whole])
+            assert np.array_equal(state.scales.cpu().numpy()[:-(-whole // 256)], scales[:-(-whole // 256)])
