@@ -479,8 +479,9 @@ size_t ar_dtype_size(ar_dtype_t dtype);
  * no sum's order depends on which workgroup finishes first.
  * ------------------------------------------------------------------------ */
 
-/* Most tensors in one call or plan, and most tiles (about 2^11 to 2^13
- * elements each) that their elements may take. */
+/* Most tensors in one call or plan.  Their elements together may take 2^24 - 1
+ * tiles of 1,024 to 8,192 (what one launch's workgroups cover); beyond that a
+ * call is refused. */
 #define AR_MAX_TENSORS 65536
 
 /* Global 2-norm of `ntensors` gradients: *norm (device memory) receives
@@ -503,8 +504,8 @@ ar_result_t ar_grad_norm(const void* const* grads, const size_t* counts, int nte
  *   v' = beta2 * v + (1 - beta2) * (g' * g')
  *   d  = sqrt(v') * (1 / sqrt(1 - beta2^t)) + eps
  *   p' = p * (1 - lr * weight_decay) - (m' / d) * (lr / (1 - beta1^t))
- * with the scalars in parentheses computed in float64 on the host and rounded
- * once.  (Decoupled weight decay: Loshchilov and Hutter, "Decoupled Weight
+ * with the scalars that name no tensor computed in float64 on the host and
+ * rounded once; a norm that is NaN makes c NaN.  (Decoupled weight decay: Loshchilov and Hutter, "Decoupled Weight
  * Decay Regularization", 2019, algorithm 2.)  grad_scale undoes a loss scale
  * (its inverse), or averages a sum over ranks.  With skip_nonfinite, a norm
  * that is NaN or infinite makes the call leave every parameter and state as
@@ -571,7 +572,8 @@ ar_result_t ar_adamw(const ar_adamw_tensors_t* tensors, const ar_adamw_config_t*
  * NaN: a block that would hold a NaN, an infinity or a value past float32's
  * largest code gets it.  The step works on the decoded float32 states as
  * ar_adamw does, updates the parameters from the new states before they are
- * rounded, and rounds each new state to one of its two neighbouring codes, up
+ * rounded (their quotient within a few units of float32's last place, where
+ * ar_adamw rounds every operation correctly), and rounds each new state to one of its two neighbouring codes, up
  * with the probability of its place between them: a second moment moves by
  * 1 - beta2 of itself a step, far less than the distance of two codes, and
  * rounding to the nearest would never move it.  The 32 random bits of element i of

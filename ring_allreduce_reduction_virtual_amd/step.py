@@ -38,16 +38,16 @@ class _Pair(NamedTuple):
 class PackedState(_Pair):
     """One tensor's state in 8 bits: a code per element, a scale byte per 256 elements (both uint8).
 
-    The two tensors are checked here; calls only look at their sizes and
-    addresses again.
+    The two tensors' type, layout and device are checked here; calls only look
+    at their sizes and addresses again.
     """
 
     def __new__(cls, codes, scales):
         for t in (codes, scales):
-            if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dtype is not torch.uint8 or not t.is_contiguous():
-                raise ValueError("a packed state is two contiguous uint8 CUDA tensors: codes and scales")
-        if codes.get_device() != scales.get_device():
-            raise ValueError("a packed state's codes and scales must be on one GPU")
+            if not isinstance(t, torch.Tensor) or t.dtype is not torch.uint8 or not t.is_contiguous():
+                raise ValueError("a packed state is two contiguous uint8 tensors: codes and scales")
+        if codes.device != scales.device:
+            raise ValueError("a packed state's codes and scales must be on one device")
         self = super().__new__(cls, codes, scales)
         self._index = codes.get_device()
         return self

@@ -667,3 +667,24 @@ def test_large_forms_agree_with_small_ones(ar, param, grad):
             whole = x.size // 256 * 256 if x.size == 600 else x.size
             assert np.array_equal(state.codes.cpu().numpy()[:whole], codes[:whole])
             assert np.array_equal(state.scales.cpu().numpy()[:-(-whole // 256)], scales[:-(-whole // 256)])
+
+
+@pytest.mark.parametrize("count", [34, 35, 68, 69])
+def test_packed_at_the_ends_of_a_launch(ar, count):
+    """As many tensors as one launch's table holds, and one more: each as if it were alone but for its number."""
+    torch = _torch()
+    rng = np.random.default_rng(count)
+    gs = [on_device(rng.standard_normal(300 + 7 * k).astype(np.float32), "bf16", k % 3) for k in range(count)]
+    ps = [torch.zeros_like(g) for g in gs]
+    ms, vs = ([ar.PackedState.zeros(g.numel(), "cuda") for g in gs] for _ in range(2))
+    ar.ar_adamw_packed(ps, gs, ms, vs, step=1, lr=0.1, seed=11)
+    for k in (0, 33, count - 1):
+        n = gs[k].numel()
+        zero = np.zeros(n, np.float32)
+        m, v = oracle.moments_f32(f32(gs[k]), zero, zero, (0.9, 0.999), 1.0)
+        for state, x, kind in ((ms[k], m, "exp_avg"), (vs[k], v, "exp_avg_sq")):
+            codes, scales = oracle.pack(x, oracle.random_bits(11, k, n), kind)
+            assert np.array_equal(state.codes.cpu().numpy(), codes) and np.array_equal(state.scales.cpu().numpy(), scales)
+    values = ar.ar_unpack_states(ms, "exp_avg")
+    assert all(np.array_equal(f64(x), oracle.unpack(s.codes.cpu().numpy(), s.scales.cpu().numpy(), "exp_avg"))
+               for x, s in zip(values, ms))
