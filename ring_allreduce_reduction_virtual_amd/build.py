@@ -75,12 +75,41 @@ def build_probe(verbose: bool = False) -> str:
     return PROBE_PATH
 
 
+MARSHAL_SOURCE = "ar_marshal.cpp"
+MARSHAL_PATH = os.path.join(PKG_DIR, "_armarshal.so")
+
+
+def build_marshal(verbose: bool = False) -> str:
+    """Compile _armarshal.so, the binding's tensor marshalling (host code, against torch's and Python's headers)."""
+    import sysconfig
+
+    import torch
+
+    inc = os.path.join(os.path.dirname(torch.__file__), "include")
+    libs = os.path.join(os.path.dirname(torch.__file__), "lib")
+    with tempfile.TemporaryDirectory(prefix="ar_marshal_") as tmp:
+        tmp_lib = os.path.join(tmp, "_armarshal.so")
+        out = _run([shutil.which("g++") or "g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall",
+                    f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+                    "-isystem", inc, "-isystem", os.path.join(inc, "torch", "csrc", "api", "include"),
+                    "-isystem", sysconfig.get_paths()["include"], os.path.join(CSRC, MARSHAL_SOURCE),
+                    f"-L{libs}", "-ltorch_python", "-ltorch_cpu", "-lc10", "-o", tmp_lib])
+        if verbose and out.strip():
+            print(out)
+        staged = MARSHAL_PATH + ".tmp"
+        shutil.copyfile(tmp_lib, staged)
+        os.chmod(staged, 0o755)
+        os.replace(staged, MARSHAL_PATH)
+    return MARSHAL_PATH
+
+
 def build_library(verbose: bool = False) -> str:
-    """Compile and link libar.so (and the probe library beside it); return libar.so's path."""
-    with ThreadPoolExecutor(1) as ex:
-        probe = ex.submit(build_probe, verbose)
+    """Compile and link libar.so (and the probe and marshalling libraries beside it); return libar.so's path."""
+    with ThreadPoolExecutor(2) as ex:
+        beside = [ex.submit(build_probe, verbose), ex.submit(build_marshal, verbose)]
         path = _build_main(verbose)
-        probe.result()
+        for f in beside:
+            f.result()
     return path
 
 

@@ -27,30 +27,19 @@ import torch
 from . import _lib
 from .binding import _on_device, _stream_handle, _ws
 
+try:
+    from . import _armarshal as _fast   # csrc/ar_marshal.cpp: the same checks in one native pass
+except ImportError:
+    _fast = None
+
 _FLOATS = {torch.float32: "f32", torch.bfloat16: "bf16", torch.float16: "f16"}
 
 
-class _Pair(NamedTuple):
+class PackedState(NamedTuple):
+    """One tensor's state in 8 bits: a code per element, a scale byte per 256 elements (both uint8)."""
+
     codes: torch.Tensor
     scales: torch.Tensor
-
-
-class PackedState(_Pair):
-    """One tensor's state in 8 bits: a code per element, a scale byte per 256 elements (both uint8).
-
-    The two tensors' type, layout and device are checked here; calls only look
-    at their sizes and addresses again.
-    """
-
-    def __new__(cls, codes, scales):
-        for t in (codes, scales):
-            if not isinstance(t, torch.Tensor) or t.dtype is not torch.uint8 or not t.is_contiguous():
-                raise ValueError("a packed state is two contiguous uint8 tensors: codes and scales")
-        if codes.device != scales.device:
-            raise ValueError("a packed state's codes and scales must be on one device")
-        self = super().__new__(cls, codes, scales)
-        self._index = codes.get_device()
-        return self
 
     @classmethod
     def zeros(cls, numel: int, device) -> "PackedState":
@@ -67,24 +56,23 @@ def _dtype_of(t, what):
     return name
 
 
-_PLAIN = {torch.Tensor, torch.nn.Parameter}
-# a tensor list's properties in one pass each: a third faster than a loop over the tensors
-_numel, _data_ptr, _get_device, _is_contiguous = (
-    torch.Tensor.numel, torch.Tensor.data_ptr, torch.Tensor.get_device, torch.Tensor.is_contiguous)
+def _array(addresses: bytes):
+    """A ctypes array of addresses packed as bytes."""
+    n = len(addresses) // ctypes.sizeof(ctypes.c_void_p)
+    return (ctypes.c_void_p * n).from_buffer_copy(addresses) if n else (ctypes.c_void_p * 1)()
 
 
 def _pointers(tensors, dev, index, dtype, counts, what):
-    """Addresses of contiguous tensors on `dev` of one dtype and the given element counts (None: any)."""
+    """Addresses of contiguous tensors on `dev` of one dtype and the given element counts (a list; None: any)."""
     n = len(tensors)
     if counts is not None and len(counts) != n:
         raise ValueError(f"need one of {what} per tensor")
-    # cheap tests over the list; what is wrong is found out below
-    if not (_PLAIN.issuperset(map(type, tensors)) and {t.dtype for t in tensors} == {dtype}
-            and set(map(_get_device, tensors)) == {index} and all(map(_is_contiguous, tensors))
-            and (counts is None or list(map(_numel, tensors)) == counts)):
-        for i, t in enumerate(tensors):
-            _refuse(t, dev, index, dtype, None if counts is None else counts[i], what, i)
-    return (ctypes.c_void_p * max(n, 1))(*map(_data_ptr, tensors))
+    fast = _fast and _fast.pointers(tensors, dtype, index, counts)
+    if fast is not None:
+        return _array(fast)
+    for i, t in enumerate(tensors):
+        _refuse(t, dev, index, dtype, None if counts is None else counts[i], what, i)
+    return (ctypes.c_void_p * max(n, 1))(*[t.data_ptr() for t in tensors])
 
 
 def _refuse(t, dev, index, dtype, count, what, i):
@@ -181,29 +169,16 @@ def _config(step, lr, betas, eps, weight_decay, max_norm, grad_scale, skip_nonfi
                             seed & 0xFFFFFFFF, 1 if skip_nonfinite else 0)
 
 
-def _packed(states, what):
-    """The states as PackedState, which has checked them (a plain pair of codes and scales will do)."""
-    if {PackedState}.issuperset(map(type, states)):
-        return states
+def _packed_pointers(states, dev, index, counts, what):
+    """Addresses of the states' codes and scales, for the given element counts."""
+    fast = _fast and _fast.states(states, index, counts)
+    if fast is not None:
+        return _array(fast[0]), _array(fast[1])
     if not all(isinstance(s, (tuple, list)) and len(s) == 2 for s in states):
         raise ValueError(f"{what} must be PackedState pairs of codes and scales")
-    return [s if type(s) is PackedState else PackedState(*s) for s in states]
-
-
-def _packed_pointers(states, dev, index, counts, what):
-    """Addresses of the states' codes and scales (for the given element counts)."""
-    if len(states) != len(counts):
-        raise ValueError(f"need one of {what} per tensor")
-    codes, scales = [s[0] for s in states], [s[1] for s in states]
-    for i, s in enumerate(states):
-        if s._index != index:
-            raise ValueError(f"{what} must be tensors on {dev}")
-    if list(map(_numel, codes)) != counts:
-        raise ValueError(f"{what} must hold one code per element: {counts}")
-    if list(map(_numel, scales)) != [-(-c // _lib.STATE_BLOCK) for c in counts]:
-        raise ValueError(f"{what} must hold one scale per {_lib.STATE_BLOCK} elements")
-    arr = ctypes.c_void_p * max(len(states), 1)
-    return arr(*map(_data_ptr, codes)), arr(*map(_data_ptr, scales))
+    return (_pointers([s[0] for s in states], dev, index, torch.uint8, counts, f"the codes of {what}"),
+            _pointers([s[1] for s in states], dev, index, torch.uint8, [-(-c // _lib.STATE_BLOCK) for c in counts],
+                      f"the scales of {what}"))
 
 
 def _tensors(params, grads, exp_avgs, exp_avg_sqs, out, copies, packed):
@@ -224,7 +199,7 @@ def _tensors(params, grads, exp_avgs, exp_avg_sqs, out, copies, packed):
         if not packed:
             put(f"{name}s{suffix}", states, torch.float32)
             return
-        states = list(_packed(states, name + "s"))
+        states = list(states)
         codes, scales = _packed_pointers(states, dev, index, sizes, name + "s")
         keep.append((states, codes, scales))
         setattr(t, f"{name}s{suffix}", codes)
@@ -296,10 +271,10 @@ def ar_unpack_states(states, kind: str, outs=None, dtype=torch.float32, stream=N
 
     `kind` says which of the two states they are: "exp_avg" or "exp_avg_sq".
     """
-    states = _packed(states, "states")
-    c0 = _first([s[0] for s in states], "states")
+    codes = [s[0] for s in states]
+    c0 = _first(codes, "states")
     dev, index = c0.device, c0.get_device()
-    sizes = [s[0].numel() for s in states]
+    sizes = [c.numel() for c in codes]
     cp, sp = _packed_pointers(states, dev, index, sizes, "states")
     if outs is None:
         outs = [_empty(s, dtype, dev, stream) for s in sizes]
@@ -437,42 +412,39 @@ def _row_pointers(tensors, n, dev, index, dtype, rows, cols, what):
     """Addresses and common row stride of one [rows, cols] tensor per rank, rows contiguous."""
     if len(tensors) != n:
         raise ValueError(f"need one of {what} per rank")
-    shape = (rows, cols)
-    # cheap tests over the list; what is wrong is found out below
-    if not (_PLAIN.issuperset(map(type, tensors)) and {t.dtype for t in tensors} == {dtype}
-            and set(map(_get_device, tensors)) == {index} and {t.shape for t in tensors} == {shape}):
-        for t in tensors:
-            if not isinstance(t, torch.Tensor) or not t.is_cuda or t.get_device() != index:
-                raise ValueError(f"{what} must be tensors on {dev}")
-            if t.dtype is not dtype:
-                raise TypeError(f"{what} must have one dtype, {dtype}")
-            if t.shape != shape:
-                raise ValueError(f"{what} must be [{rows}, {cols}] tensors, one per rank")
-    strides = {t.stride() for t in tensors}
-    if any((cols > 1 and s[1] != 1) or (rows > 1 and s[0] < cols) for s in strides):
-        raise ValueError(f"{what} must have contiguous rows that do not overlap")
+    fast = _fast and _fast.rows(tensors, dtype, index, rows, cols)
+    if fast is not None:
+        return _array(fast[0]), fast[1]
     stride = cols
-    if rows > 1:
-        stride = next(iter(strides))[0]
-        if any(s[0] != stride for s in strides):
-            raise ValueError(f"{what} must have one row stride")
-    return (ctypes.c_void_p * n)(*map(_data_ptr, tensors)), stride
+    for i, t in enumerate(tensors):
+        if not isinstance(t, torch.Tensor) or not t.is_cuda or t.get_device() != index:
+            raise ValueError(f"{what} must be tensors on {dev}")
+        if t.dtype is not dtype:
+            raise TypeError(f"{what} must have one dtype, {dtype}")
+        if t.shape != (rows, cols):
+            raise ValueError(f"{what} must be [{rows}, {cols}] tensors, one per rank")
+        s = t.stride()
+        if (cols > 1 and s[1] != 1) or (rows > 1 and s[0] < cols):
+            raise ValueError(f"{what} must have contiguous rows that do not overlap")
+        if rows > 1:
+            if i > 0 and s[0] != stride:
+                raise ValueError(f"{what} must have one row stride")
+            stride = s[0]
+    return (ctypes.c_void_p * n)(*[t.data_ptr() for t in tensors]), stride
 
 
-def _rank_rows(n, rows, cols, dtype, dev, stream):
-    """A new [rows, cols] tensor per rank, and their addresses."""
-    whole = _empty((n, rows, cols), dtype, dev, stream)
-    at, step = whole.data_ptr(), rows * cols * whole.element_size()
-    return list(whole.unbind(0)), (ctypes.c_void_p * n)(*range(at, at + n * step, step) if step else [at] * n)
+def _new_parts(shape, dtype, dev, stream):
+    """shape[0] new tensors of one allocation, and their addresses (a list)."""
+    fast = _fast.new_parts(shape, dtype, dev.index) if _fast and stream is None else None
+    if fast is not None:
+        return fast[0], _array(fast[1])
+    parts = list(_empty(shape, dtype, dev, stream).unbind(0))
+    return parts, (ctypes.c_void_p * max(len(parts), 1))(*[t.data_ptr() for t in parts])
 
 
-def _rank_vectors(n, length, dtype, dev, stream):
-    """Two new vectors per rank, and the addresses of both sets."""
-    whole = _empty((2 * n, length), dtype, dev, stream)
-    at, step = whole.data_ptr(), length * whole.element_size()
-    ptrs = list(range(at, at + 2 * n * step, step)) if step else [at] * (2 * n)
-    parts = whole.unbind(0)
-    return list(parts[:n]), list(parts[n:]), (ctypes.c_void_p * n)(*ptrs[:n]), (ctypes.c_void_p * n)(*ptrs[n:])
+def _second_half(ptrs, n):
+    """Entries n to 2n of an address array, as an array of its own in the same memory."""
+    return (ctypes.c_void_p * n).from_buffer(ptrs, n * ctypes.sizeof(ctypes.c_void_p))
 
 
 def _rank_list(tensors, what):
@@ -518,12 +490,13 @@ def ar_layer_norm(xs, gammas=None, betas=None, ys=None, eps: float = 1e-5, stats
     gp = None if gammas is None else _weights(gammas, n, dev, index, wdt, cols, "gammas")
     bp = None if betas is None else _weights(betas, n, dev, index, wdt, cols, "betas")
     if ys is None:
-        (ys, yp), y_stride = _rank_rows(n, rows, cols, dt, dev, stream), cols
+        (ys, yp), y_stride = _new_parts((n, rows, cols), dt, dev, stream), cols
     else:
         yp, y_stride = _row_pointers(ys, n, dev, index, dt, rows, cols, "ys")
     means = rstds = mp = rp = None
     if stats:
-        means, rstds, mp, rp = _rank_vectors(n, rows, torch.float32, dev, stream)
+        both, ptrs = _new_parts((2 * n, rows), torch.float32, dev, stream)
+        means, rstds, mp, rp = both[:n], both[n:], ptrs, _second_half(ptrs, n)
     with _on_device(dev):
         rc = _lib.lib().ar_layer_norm(xp, gp, bp, yp, mp, rp, rows, cols, x_stride, y_stride, _lib.DTYPES[name],
                                       _lib.DTYPES[_FLOATS[wdt]], eps, n, _stream_handle(stream, dev.index))
@@ -560,11 +533,12 @@ def ar_layer_norm_backward(dys, xs, gammas, means, rstds, dxs=None, weight_grads
     mp = _pointers(means, dev, index, torch.float32, [rows] * n, "means")
     rp = _pointers(rstds, dev, index, torch.float32, [rows] * n, "rstds")
     if dxs is None:
-        (dxs, dxp), dx_stride = _rank_rows(n, rows, cols, dt, dev, stream), cols
+        (dxs, dxp), dx_stride = _new_parts((n, rows, cols), dt, dev, stream), cols
     else:
         dxp, dx_stride = _row_pointers(dxs, n, dev, index, dt, rows, cols, "dxs")
     if weight_grads and dgammas is None and dbetas is None:
-        dgammas, dbetas, gout, bout = _rank_vectors(n, cols, wdt, dev, stream)
+        both, ptrs = _new_parts((2 * n, cols), wdt, dev, stream)
+        dgammas, dbetas, gout, bout = both[:n], both[n:], ptrs, _second_half(ptrs, n)
     else:
         if weight_grads:
             made = list(_empty((n, cols), wdt, dev, stream).unbind(0))

@@ -262,3 +262,21 @@ def test_layer_norm_backward_errors(lib):
     assert call(dbeta=ptrs([0, BASE + 600 * GAP])) == INVALID
     assert call(cols=0, strides=(0, 0, 0)) == 0
     assert call(rows=0, dgamma=None, dbeta=None, ws=None, have=0) == 0
+
+
+def test_native_marshalling_declines_what_it_does_not_know():
+    """The native checks answer None, with no error left behind, for anything that is not theirs to take."""
+    import torch
+
+    m = pytest.importorskip("ring_allreduce_reduction_virtual_amd._armarshal")
+    cpu, f32 = torch.zeros(4), torch.float32
+    for bad in ([cpu], [None], [cpu, 3], 7, None):
+        assert m.pointers(bad, f32, 0, None) is None
+        assert m.rows(bad, f32, 0, 2, 2) is None
+        assert m.states(bad, 0, [4]) is None
+    assert m.pointers([], f32, 0, None) == b"" and m.states([], 0, []) == (b"", b"")
+    assert m.pointers([], f32, 0, [1]) is None and m.pointers([], "float32", 0, None) is None
+    assert m.pointers([], f32, 1 << 80, None) is None and m.pointers() is None
+    assert m.states([(cpu, cpu)], 0, [4]) is None and m.states([(cpu,)], 0, [4]) is None
+    assert m.new_parts([2, 3], f32, 0) is None and m.new_parts((), f32, 0) is None
+    assert m.new_parts((2, "x"), f32, 0) is None and m.new_parts((2, -1), f32, 0) is None

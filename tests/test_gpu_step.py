@@ -688,3 +688,52 @@ def test_packed_at_the_ends_of_a_launch(ar, count):
     values = ar.ar_unpack_states(ms, "exp_avg")
     assert all(np.array_equal(f64(x), oracle.unpack(s.codes.cpu().numpy(), s.scales.cpu().numpy(), "exp_avg"))
                for x, s in zip(values, ms))
+
+
+@pytest.fixture(params=["native", "python"])
+def marshalling(request, monkeypatch):
+    """Both ways of checking and addressing tensors."""
+    from ring_allreduce_reduction_virtual_amd import step
+
+    if request.param == "python":
+        monkeypatch.setattr(step, "_fast", None)
+    else:
+        assert step._fast is not None, "_armarshal.so is not built"
+    return request.param
+
+
+def test_marshalling_both_ways(ar, marshalling):
+    """Subclasses, Parameters, views, odd strides and empty tensors through every call, and the refusals' kinds."""
+    torch = _torch()
+    f = lambda *s, **k: torch.ones(*s, device="cuda", **k)              # noqa: E731
+    whole = f(100)
+    p = [torch.nn.Parameter(f(7)), whole[3:10], f(0)]
+    g = (f(7), whole[50:57], f(0))                                      # a tuple will do
+    m, v = ([f(7) * 0, f(7) * 0, f(0)] for _ in range(2))
+    assert abs(ar.ar_grad_norm(g).item() - math.sqrt(14)) < 1e-5
+    ar.ar_adamw(p, g, m, v, step=1, lr=0.5)
+    assert (p[0].detach() == 0.5).all() and (whole[3:10] == 0.5).all() and (whole[10:] == 1).all()
+    states = [[tuple(ar.PackedState.zeros(t.numel(), "cuda")) for t in p] for _ in range(2)]
+    ar.ar_adamw_packed(p, g, *states, step=1, lr=0.5, seed=1)
+    assert all(x.numel() == t.numel() for x, t in zip(ar.ar_unpack_states(states[0], "exp_avg"), p))
+    x = f(4, 12)
+    ys, means, _ = ar.ar_layer_norm((x[:, 1:8], f(4, 12)[:, :7]))
+    assert ys[0].shape == (4, 7) and (means[0] == 1).all()
+    with pytest.raises(TypeError):
+        ar.ar_grad_norm([f(3), f(3, dtype=torch.bfloat16)])
+    with pytest.raises(ValueError, match="contiguous"):
+        ar.ar_adamw([f(6)[::2]], [f(3)], [f(3)], [f(3)], step=1, lr=0.1)
+    with pytest.raises(ValueError, match="hold 3"):
+        ar.ar_adamw([f(3)], [f(4)], [f(3)], [f(3)], step=1, lr=0.1)
+    with pytest.raises(ValueError, match="PackedState"):
+        ar.ar_unpack_states([f(3, dtype=torch.uint8)], "exp_avg")
+    with pytest.raises(ValueError, match="scales"):
+        ar.ar_unpack_states([(f(300, dtype=torch.uint8), f(1, dtype=torch.uint8))], "exp_avg")
+    with pytest.raises(TypeError):
+        ar.ar_unpack_states([(f(3), f(1, dtype=torch.uint8))], "exp_avg")
+    with pytest.raises(ValueError, match="stride"):
+        ar.ar_layer_norm([f(4, 8)[:, :7], f(4, 9)[:, :7]])
+    with pytest.raises(ValueError, match="contiguous rows"):
+        ar.ar_layer_norm([f(7, 4).t()])
+    with pytest.raises(ValueError):
+        ar.ar_layer_norm([f(4, 7), f(4, 8)])
