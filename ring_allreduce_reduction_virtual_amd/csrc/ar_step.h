@@ -49,6 +49,8 @@ constexpr int packed_vectors(bool large) { return large ? 2 : 1; }
 
 // Most partial sums one launch of the gradient norm leaves (its workgroups).
 constexpr uint32_t kNormBlocks = 1024;
+// Up to this many, a plan's last workgroup adds them itself.
+constexpr uint32_t kNormJoinBlocks = 128;
 
 // One tensor's line in a table.  first_tile counts the tiles of the lines
 // before it in the same table; index is the tensor's number in the call.
@@ -138,7 +140,7 @@ struct AdamwScalars {
 // validated by the caller.
 template <class Table>
 hipError_t launch_norm(const Table& t, uint32_t tiles, uint32_t blocks, ar_dtype_t dtype, double* partials,
-                       float* norm, hipStream_t stream);
+                       float* norm, uint32_t* counter, hipStream_t stream);
 // What the steps' kernels are chosen by.
 struct StepForm {
     ar_dtype_t param, grad;

@@ -94,20 +94,22 @@ uint64_t table_bytes(uint64_t lines, uint64_t tiles) {
     return (lines * sizeof(Entry) + tiles * sizeof(uint32_t) + 7) / 8 * 8;
 }
 
+// Copies the table to `at`, after `zeros` bytes of zero.
 template <class Entry>
-ar_result_t upload(Lines<Entry>& lines, char* at, hipStream_t stream, DeviceTable<Entry>* out, uint32_t* out_tiles) {
+ar_result_t upload(Lines<Entry>& lines, char* at, size_t zeros, hipStream_t stream, DeviceTable<Entry>* out,
+                   uint32_t* out_tiles) {
     uint64_t tiles = 0;
     for (Entry& e : lines.e) {
         e.first_tile = static_cast<uint32_t>(tiles);
         tiles += tiles_of(e.n, lines.tile);
     }
-    *out = {reinterpret_cast<const Entry*>(at),
-            reinterpret_cast<const uint32_t*>(at + lines.e.size() * sizeof(Entry))};
+    *out = {reinterpret_cast<const Entry*>(at + zeros),
+            reinterpret_cast<const uint32_t*>(at + zeros + lines.e.size() * sizeof(Entry))};
     *out_tiles = static_cast<uint32_t>(tiles);
     if (tiles == 0) return AR_SUCCESS;
-    std::vector<char> host(lines.e.size() * sizeof(Entry) + tiles * sizeof(uint32_t));
-    std::memcpy(host.data(), lines.e.data(), lines.e.size() * sizeof(Entry));
-    char* to = host.data() + lines.e.size() * sizeof(Entry);
+    std::vector<char> host(zeros + lines.e.size() * sizeof(Entry) + tiles * sizeof(uint32_t));
+    std::memcpy(host.data() + zeros, lines.e.data(), lines.e.size() * sizeof(Entry));
+    char* to = host.data() + zeros + lines.e.size() * sizeof(Entry);
     for (uint32_t k = 0; k < lines.e.size(); ++k) {
         for (uint64_t j = tiles_of(lines.e[k].n, lines.tile); j > 0; --j, to += sizeof(uint32_t))
             std::memcpy(to, &k, sizeof(uint32_t));
@@ -143,6 +145,10 @@ ar_result_t add_workspace(std::vector<Range>& v, void* ws, size_t have, uint64_t
 // partial sums.
 uint32_t norm_blocks(uint64_t tiles) { return static_cast<uint32_t>(std::min<uint64_t>(tiles, kNormBlocks)); }
 
+// A plan's counter of finished workgroups stands between its partial sums and
+// its table.
+constexpr size_t kCounterBytes = 8;
+
 // Partial sums of a one-shot call (at most kNormBlocks a launch) or a plan.
 uint64_t norm_workspace(const size_t* counts, int n) {
     uint64_t lines = 0, tiles = 0;
@@ -151,7 +157,7 @@ uint64_t norm_workspace(const size_t* counts, int n) {
         tiles += tiles_of(counts[t], kNormTile);
     }
     const uint64_t partials = launches_of(lines, InlineTable<NormEntry>::kMax) * kNormBlocks * sizeof(double);
-    return partials + table_bytes<NormEntry>(lines, tiles);
+    return lines == 0 ? 0 : partials + kCounterBytes + table_bytes<NormEntry>(lines, tiles);
 }
 
 ar_result_t norm_lines(const void* const* grads, const size_t* counts, int n, ar_dtype_t dtype, float* norm, void* ws,
@@ -365,16 +371,22 @@ struct ar_update_s {
 
 namespace {
 
-// Enqueue the norm of `tiles` tiles: one launch when one workgroup does, else a
-// second that adds the partial sums.  No tiles: the second alone writes 0.
+// Launches of a norm of so many workgroups: one when one of them can finish
+// the sum, else a second that adds the partial sums (and writes 0 where there
+// is nothing to add).
+int norm_launches(uint32_t blocks) { return blocks <= kNormJoinBlocks ? 1 : 2; }
+
 ar_result_t start_norm(const ar_update_s& u, hipStream_t stream) {
     const uint32_t blocks = norm_blocks(u.tiles);
-    ar_result_t rc = AR_SUCCESS;
-    if (blocks > 0)
-        rc = hip_result(launch_norm(u.norm_table, u.tiles, blocks, u.form.grad, u.partials, blocks == 1 ? u.norm : nullptr,
-                                    stream),
-                        "grad_norm launch");
-    if (rc != AR_SUCCESS || blocks == 1) return rc;
+    if (blocks > 0) {
+        const bool join = norm_launches(blocks) == 1;
+        uint32_t* const counter = reinterpret_cast<uint32_t*>(u.partials + kNormBlocks);
+        const ar_result_t rc =
+            hip_result(launch_norm(u.norm_table, u.tiles, blocks, u.form.grad, u.partials, join ? u.norm : nullptr,
+                                   join ? counter : nullptr, stream),
+                       "grad_norm launch");
+        if (rc != AR_SUCCESS || join) return rc;
+    }
     return hip_result(launch_norm_final(u.partials, blocks, u.norm, stream), "grad_norm launch");
 }
 
@@ -404,9 +416,9 @@ ar_result_t init_adamw(const ar_adamw_tensors_t* a, void* ws, size_t ws_bytes, h
     if (lines.e.empty()) return AR_SUCCESS;   // nothing to place: no device is asked
     if ((rc = refuse_capture(stream)) != AR_SUCCESS || (rc = check_device_memory(ranges)) != AR_SUCCESS) return rc;
     if constexpr (PACKED) {
-        return upload(lines, static_cast<char*>(ws), stream, &u.packed_table, &u.tiles);
+        return upload(lines, static_cast<char*>(ws), 0, stream, &u.packed_table, &u.tiles);
     } else {
-        return upload(lines, static_cast<char*>(ws), stream, &u.adamw_table, &u.tiles);
+        return upload(lines, static_cast<char*>(ws), 0, stream, &u.adamw_table, &u.tiles);
     }
 }
 
@@ -427,7 +439,7 @@ ar_result_t ar_grad_norm(const void* const* grads, const size_t* counts, int nte
         rc = in_launches(lines, "grad_norm launch", [&](const InlineTable<NormEntry>& t, uint32_t tiles, uint32_t) {
             const uint32_t blocks = norm_blocks(tiles);
             const hipError_t e =
-                launch_norm(t, tiles, blocks, dtype, partials + written, single ? norm : nullptr, stream);
+                launch_norm(t, tiles, blocks, dtype, partials + written, single ? norm : nullptr, nullptr, stream);
             written += blocks;
             return e;
         });
@@ -506,8 +518,8 @@ ar_result_t ar_grad_norm_init(const void* const* grads, const size_t* counts, in
             u.form.grad = dtype;
             u.norm = norm;
             u.partials = static_cast<double*>(workspace);
-            return upload(lines, static_cast<char*>(workspace) + kNormBlocks * sizeof(double), stream, &u.norm_table,
-                          &u.tiles);
+            return upload(lines, static_cast<char*>(workspace) + kNormBlocks * sizeof(double), kCounterBytes, stream,
+                          &u.norm_table, &u.tiles);
         });
     });
 }
@@ -558,7 +570,7 @@ ar_result_t ar_adamw_start(ar_update_t update, const ar_adamw_config_t* config, 
 
 int ar_update_num_launches(ar_update_t update) {
     if (update == nullptr) return -1;
-    if (update->kind == AR_UPDATE_GRAD_NORM) return norm_blocks(update->tiles) > 1 ? 2 : 1;
+    if (update->kind == AR_UPDATE_GRAD_NORM) return norm_launches(norm_blocks(update->tiles));
     return update->tiles > 0 ? 1 : 0;
 }
 

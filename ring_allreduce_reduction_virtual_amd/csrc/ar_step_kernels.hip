@@ -56,12 +56,16 @@ __device__ __forceinline__ double block_sum(double x) {
 // Workgroup b takes tiles b, b + gridDim.x, ... and leaves one partial sum, or
 // the norm itself when it is the only one.  2^27 float32 in 8 tensors: 79 us
 // (6.8 TB/s, reads only), and 4.8 us for the sum of the partial sums; 9.7 million
-// bf16 in 97 tensors back to back 6.9 and 2.1 us.  Adding them in the workgroup
-// that finishes last instead saves the second launch (2 us) up to some 20
-// workgroups and costs 25-45 us at 1,024, each of which then has to write its
-// XCD's cache back.
+// bf16 in 97 tensors back to back 6.9 and 2.1 us.
+//
+// With a counter (of a plan's workspace, 0 between calls) the workgroup that
+// finishes last adds the partial sums, in their order, and no second launch
+// follows: 4.7 us against 6.7 for 3 workgroups, 5.1 against 6.6 for 70.  Each
+// workgroup has to write its XCD's cache back before it counts itself: 256 took
+// 9.2 us against 6.7, and 1,024 took 25-45 us more than the second launch.
 template <int DT, class Table>
-__global__ void __launch_bounds__(kStepThreads) k_grad_norm(Table t, uint32_t tiles, double* partials, float* norm) {
+__global__ void __launch_bounds__(kStepThreads) k_grad_norm(Table t, uint32_t tiles, double* partials, float* norm,
+                                                            uint32_t* counter) {
     constexpr int V = 16 / elem_size<DT>();
     constexpr int U = kNormTile / (kStepThreads * V);
     double acc[4] = {0, 0, 0, 0};
@@ -88,14 +92,26 @@ __global__ void __launch_bounds__(kStepThreads) k_grad_norm(Table t, uint32_t ti
         }
     }
     const double s = block_sum((acc[0] + acc[1]) + (acc[2] + acc[3]));
+    if (gridDim.x == 1 && norm != nullptr) {
+        if (threadIdx.x == 0) *norm = static_cast<float>(sqrt(s));
+        return;
+    }
+    if (threadIdx.x == 0) partials[blockIdx.x] = s;
+    if (counter == nullptr) return;
+    __shared__ bool last;
     if (threadIdx.x == 0) {
-        if (norm != nullptr) {
-            *norm = static_cast<float>(sqrt(s));
-        } else {
-            partials[blockIdx.x] = s;
-        }
+        // releases this partial sum, and acquires the others' when it is the last
+        last = __hip_atomic_fetch_add(counter, 1u, __ATOMIC_ACQ_REL, __HIP_MEMORY_SCOPE_AGENT) == gridDim.x - 1;
+    }
+    __syncthreads();
+    if (!last) return;
+    const double all = block_sum(threadIdx.x < gridDim.x ? partials[threadIdx.x] : 0.0);
+    if (threadIdx.x == 0) {
+        *norm = static_cast<float>(sqrt(all));
+        *counter = 0;
     }
 }
+static_assert(kNormJoinBlocks <= kStepThreads, "one thread per partial sum");
 
 __global__ void __launch_bounds__(kStepThreads) k_grad_norm_final(const double* partials, uint32_t n, float* norm) {
     double acc = 0;
@@ -387,17 +403,20 @@ __global__ void __launch_bounds__(kStepThreads) k_unpack(InlineTable<UnpackEntry
 
 template <class Table>
 hipError_t launch_norm(const Table& t, uint32_t tiles, uint32_t blocks, ar_dtype_t dtype, double* partials,
-                       float* norm, hipStream_t stream) {
+                       float* norm, uint32_t* counter, hipStream_t stream) {
     const dim3 grid(blocks), block(kStepThreads);
     switch (dtype) {
         case AR_FLOAT32:
-            hipLaunchKernelGGL((k_grad_norm<AR_FLOAT32, Table>), grid, block, 0, stream, t, tiles, partials, norm);
+            hipLaunchKernelGGL((k_grad_norm<AR_FLOAT32, Table>), grid, block, 0, stream, t, tiles, partials, norm,
+                               counter);
             break;
         case AR_BFLOAT16:
-            hipLaunchKernelGGL((k_grad_norm<AR_BFLOAT16, Table>), grid, block, 0, stream, t, tiles, partials, norm);
+            hipLaunchKernelGGL((k_grad_norm<AR_BFLOAT16, Table>), grid, block, 0, stream, t, tiles, partials, norm,
+                               counter);
             break;
         case AR_FLOAT16:
-            hipLaunchKernelGGL((k_grad_norm<AR_FLOAT16, Table>), grid, block, 0, stream, t, tiles, partials, norm);
+            hipLaunchKernelGGL((k_grad_norm<AR_FLOAT16, Table>), grid, block, 0, stream, t, tiles, partials, norm,
+                               counter);
             break;
         default: return hipErrorInvalidValue;
     }
@@ -512,9 +531,9 @@ hipError_t launch_unpack(const InlineTable<UnpackEntry>& t, uint32_t tiles, ar_s
 }
 
 template hipError_t launch_norm(const InlineTable<NormEntry>&, uint32_t, uint32_t, ar_dtype_t, double*, float*,
-                                hipStream_t);
+                                uint32_t*, hipStream_t);
 template hipError_t launch_norm(const DeviceTable<NormEntry>&, uint32_t, uint32_t, ar_dtype_t, double*, float*,
-                                hipStream_t);
+                                uint32_t*, hipStream_t);
 template hipError_t launch_adamw(const InlineTable<AdamwEntry>&, uint32_t, const AdamwScalars&, const StepForm&,
                                  hipStream_t);
 template hipError_t launch_adamw(const DeviceTable<AdamwEntry>&, uint32_t, const AdamwScalars&, const StepForm&,

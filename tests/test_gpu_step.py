@@ -737,3 +737,21 @@ def test_marshalling_both_ways(ar, marshalling):
         ar.ar_layer_norm([f(7, 4).t()])
     with pytest.raises(ValueError):
         ar.ar_layer_norm([f(4, 7), f(4, 8)])
+
+
+@pytest.mark.parametrize("tiles", [1, 2, 3, 20, 127, 128, 129, 1024, 1500])
+def test_norm_plan_started_again_and_again(ar, tiles):
+    """Every start of a plan finds its workspace as the first one did, around the number of workgroups that join."""
+    torch = _torch()
+    tile = 8192
+    g = [torch.zeros(tiles * tile // 2 - 5, device="cuda"), torch.zeros(tiles * tile - tiles * tile // 2 - 7, device="cuda")]
+    plan = ar.ar_grad_norm_init(g)
+    expected = []
+    for k in range(1, 40):
+        for t in g:
+            t.fill_(float(k))
+        plan.start()
+        expected.append((plan.norm.clone(), k * math.sqrt(sum(t.numel() for t in g))))
+    for got, want in expected:
+        assert abs(f64(got)[0] - want) <= norm_bound(want)
+    assert plan.num_launches == (1 if sum(-(-t.numel() // tile) for t in g) <= 128 else 2)
