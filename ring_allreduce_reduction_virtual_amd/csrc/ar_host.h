@@ -1,5 +1,5 @@
 // Host-side checks shared by the training-step entry points (ar_step_api.hip,
-// ar_layer_norm.hip): error texts, buffer ranges and their overlaps, and
+// ar_layer_norm_api.hip): error texts, buffer ranges and their overlaps, and
 // where buffers live.  Everything is inline in an unnamed namespace.
 #pragma once
 

@@ -81,8 +81,8 @@ def _refuse(t, dev, index, dtype, count, what, i):
         raise ValueError(f"{what} must be tensors on {dev}")
     if t.dtype is not dtype:
         raise TypeError(f"{what} must have one dtype, {dtype}")
-    if not t.is_contiguous():
-        raise ValueError(f"{what} must be contiguous")
+    if not t.is_contiguous() or t.is_neg():
+        raise ValueError(f"{what} must be contiguous, and no negative views")
     if count is not None and t.numel() != count:
         raise ValueError(f"{what}[{i}] must hold {count} elements")
 
@@ -424,7 +424,7 @@ def _row_pointers(tensors, n, dev, index, dtype, rows, cols, what):
         if t.shape != (rows, cols):
             raise ValueError(f"{what} must be [{rows}, {cols}] tensors, one per rank")
         s = t.stride()
-        if (cols > 1 and s[1] != 1) or (rows > 1 and s[0] < cols):
+        if t.is_neg() or (cols > 1 and s[1] != 1) or (rows > 1 and s[0] < cols):
             raise ValueError(f"{what} must have contiguous rows that do not overlap")
         if rows > 1:
             if i > 0 and s[0] != stride:

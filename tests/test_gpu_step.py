@@ -755,3 +755,14 @@ def test_norm_plan_started_again_and_again(ar, tiles):
     for got, want in expected:
         assert abs(f64(got)[0] - want) <= norm_bound(want)
     assert plan.num_launches == (1 if sum(-(-t.numel() // tile) for t in g) <= 128 else 2)
+
+
+def test_negative_views_refused(ar):
+    """A view whose elements are to be read negated holds other values in memory."""
+    torch = _torch()
+    g = torch._neg_view(torch.ones(64, device="cuda"))
+    with pytest.raises(ValueError, match="negative"):
+        ar.ar_grad_norm([g])
+    x = torch._neg_view(torch.ones(2, 64, device="cuda"))
+    with pytest.raises(ValueError, match="contiguous rows"):
+        ar.ar_layer_norm([x])
