@@ -10,11 +10,12 @@
 
 #include <torch/csrc/Dtype.h>
 #include <torch/csrc/autograd/python_variable.h>
+#include <torch/csrc/utils/object_ptr.h>
 
 #include <ATen/ops/empty.h>
-#include <ATen/ops/unbind.h>
 
 #include <cstdint>
+#include <utility>
 #include <vector>
 
 namespace {
@@ -179,26 +180,27 @@ PyObject* new_parts(PyObject*, PyObject* const* args, Py_ssize_t n_args) {
         }
         const at::Tensor whole = at::empty(
             shape, at::TensorOptions().dtype(type).device(at::Device(at::kCUDA, static_cast<at::DeviceIndex>(index))));
-        const std::vector<at::Tensor> parts = at::unbind(whole, 0);
+        const size_t n = static_cast<size_t>(shape[0]);
+        const at::IntArrayRef part = at::IntArrayRef(shape).slice(1);
+        const int64_t numel = n == 0 ? 0 : whole.numel() / shape[0];
         std::vector<uintptr_t> at;
-        at.reserve(parts.size());
-        PyObject* list = PyList_New(static_cast<Py_ssize_t>(parts.size()));
-        if (list == nullptr) return nullptr;
-        for (size_t i = 0; i < parts.size(); ++i) {
-            PyObject* t = THPVariable_Wrap(parts[i]);
-            if (t == nullptr) {
-                Py_DECREF(list);
-                return nullptr;
-            }
-            PyList_SET_ITEM(list, static_cast<Py_ssize_t>(i), t);
-            at.push_back(reinterpret_cast<uintptr_t>(parts[i].data_ptr()));
+        at.reserve(n);
+        THPObjectPtr list(PyList_New(static_cast<Py_ssize_t>(n)));
+        if (!list) return nullptr;
+        for (size_t i = 0; i < n; ++i) {
+            // a tensor of its own in the shared storage: no view for autograd to track
+            at::Tensor t = at::detail::make_tensor<c10::TensorImpl>(c10::Storage(whole.storage()), whole.key_set(),
+                                                                    whole.dtype());
+            t.unsafeGetTensorImpl()->set_storage_offset(static_cast<int64_t>(i) * numel);
+            t.unsafeGetTensorImpl()->set_sizes_contiguous(part);
+            at.push_back(reinterpret_cast<uintptr_t>(t.data_ptr()));
+            PyObject* o = THPVariable_Wrap(std::move(t));
+            if (o == nullptr) return nullptr;
+            PyList_SET_ITEM(list.get(), static_cast<Py_ssize_t>(i), o);
         }
         PyObject* bytes = address_bytes(at);
-        if (bytes == nullptr) {
-            Py_DECREF(list);
-            return nullptr;
-        }
-        return Py_BuildValue("(NN)", list, bytes);
+        if (bytes == nullptr) return nullptr;
+        return Py_BuildValue("(ON)", list.get(), bytes);
     });
 }
 

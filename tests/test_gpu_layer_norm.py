@@ -379,3 +379,24 @@ def test_bounds_of_the_row_forms(ar, dtype, cols):
     ar.ar_layer_norm_backward(dys, xs, gammas, means, rstds, dxs=[w[:, 4:cols + 4] for w in wide])
     for w, d in zip(wide, dxs):
         assert torch.equal(w[:, 4:cols + 4], d) and (w[:, :4] == 3).all() and (w[:, cols + 4:] == 3).all()
+
+
+def test_made_outputs_are_tensors_of_their_own(ar):
+    """The outputs a call makes share memory side by side, but are no views of one another."""
+    torch = _torch()
+    xs = [torch.randn(5, 33, device="cuda") for _ in range(3)]
+    ys, means, rstds = ar.ar_layer_norm(xs)
+    for group, shape in ((ys, (5, 33)), (means, (5,)), (rstds, (5,))):
+        assert [tuple(t.shape) for t in group] == [shape] * 3
+        assert all(t.is_contiguous() and not t._is_view() for t in group)
+    kept = [t.clone() for t in (*ys, *means, *rstds)]
+    ys[1].requires_grad_()
+    with torch.no_grad():
+        ys[1].fill_(7.0)
+        means[2].fill_(8.0)
+    for i, (a, b) in enumerate(zip((*ys, *means, *rstds), kept)):
+        assert torch.equal(a, torch.full_like(b, 7.0 if i == 1 else 8.0) if i in (1, 5) else b)
+    only = ys[2]
+    del ys, means, rstds
+    torch.empty(1 << 20, device="cuda").fill_(3.0)
+    assert torch.equal(only, kept[2])
