@@ -84,7 +84,8 @@ inline RowShape forward_shape(uint64_t cols, int vector_elements) {
 // 74, 16x1 107; 256 32x1 76, 64x1 90; 1,024 128x1 78, 64x2 82, 256x1 88; 2,048
 // 256x1 79, 128x2 91, 64x4 94; 4,096 256x2 80, 512x1 80, 128x4 85, 1024x1 103;
 // 8,192 512x2 89, 1024x1 91, 256x4 102, wide 158; float32: 1,024 256x1 78,
-// 128x2 75; 4,096 512x2 80; 8,192 512x4 87, wide 143.
+// 128x2 75; 4,096 512x2 80; 8,192 512x4 87, wide 143 (all with 512 workgroups;
+// with 256, as below, 8,192 86 in bf16, 81 in float32, and 16,384 bf16 100).
 inline RowShape backward_shape(uint64_t cols, int vector_elements) {
     const uint64_t need = (cols + vector_elements - 1) / vector_elements;
     if (need <= 8) return {8, 1};
@@ -103,12 +104,33 @@ inline RowShape backward_shape(uint64_t cols, int vector_elements) {
 // Workgroups of a rank's backward pass; each leaves one partial sum of dgamma
 // and dbeta per column.  All ranks together: enough to fill the GPU, more when
 // every one still has 64 rows, over which its partial sums' traffic is small.
-constexpr uint64_t kBackwardBlocks = 512, kBackwardMostBlocks = 4096, kBackwardRows = 64;
+// Rows over 512 threads fill it with half as many (us, 512 / 256 workgroups:
+// 4 x 1,024 x 8,192 bf16 56 / 49, 2 x 512 x 16,384 bf16 47 / 37, 4 x 512 x
+// 16,384 float32 103 / 93; 1,024 rows of 1,024 on 256 threads 14 / 18).
+//
+// Wide rows: their sums are made by stretches of kColumnThreads vectors, and
+// kColumnBlocks of these fill the GPU (us with about 4,000 / 2,000 / 1,000 /
+// 500 workgroups: 2 x 512 x 40,000 bf16 148 / 121 / 105 / 102; 1,024 x 50,257
+// bf16 168 / 158 / 165 for 3,200 / 1,600 / 800).
+constexpr uint64_t kBackwardBlocks = 512, kBackwardLongBlocks = 256, kBackwardMostBlocks = 4096, kBackwardRows = 64;
+constexpr int kColumnThreads = 256;
+constexpr uint64_t kColumnBlocks = 1024;
+inline uint64_t column_stretches(uint64_t cols, int vector_elements) {
+    const uint64_t per = static_cast<uint64_t>(kColumnThreads) * vector_elements;
+    return (cols + per - 1) / per;
+}
 inline uint32_t backward_blocks(uint64_t rows, uint64_t cols, int nranks, int vector_elements) {
-    const int at_once = rows_at_once(backward_shape(cols, vector_elements).threads);
-    const uint64_t wanted =
-        std::min(kBackwardMostBlocks, std::max(kBackwardBlocks, rows * nranks / kBackwardRows)) / nranks;
-    return static_cast<uint32_t>(std::min<uint64_t>((rows + at_once - 1) / at_once, std::max<uint64_t>(1, wanted)));
+    const RowShape shape = backward_shape(cols, vector_elements);
+    const int at_once = rows_at_once(shape.threads);
+    uint64_t wanted;
+    if (shape.vectors == 0) {
+        wanted = kColumnBlocks / column_stretches(cols, vector_elements);
+    } else {
+        wanted = std::max(shape.threads > 256 ? kBackwardLongBlocks : kBackwardBlocks, rows * nranks / kBackwardRows);
+        wanted = std::min(kBackwardMostBlocks, wanted);
+    }
+    wanted = std::max<uint64_t>(1, wanted / nranks);
+    return static_cast<uint32_t>(std::min<uint64_t>((rows + at_once - 1) / at_once, wanted));
 }
 
 hipError_t launch_norm_forward(const NormForwardArgs& a, int nranks, ar_dtype_t dtype, ar_dtype_t weight,

@@ -75,6 +75,10 @@ __global__ void __launch_bounds__(block_threads(THREADS)) k_layer_norm_backward(
     for (int u = 0; u < NV; ++u) {
         if (gamma != nullptr) RowPart<THREADS, V>(u, cols).template load<false>(g[u], gamma, cols);
     }
+    if (cols % V != 0) {   // an infinite weight times a cleared dy would be NaN
+#pragma unroll
+        for (int u = 0; u < NV; ++u) RowPart<THREADS, V>(u, cols).clear(g[u]);
+    }
 #pragma unroll
     for (int k = 0; k < EACH; ++k) dg[k] = db[k] = 0;
     int turn = 0;
@@ -186,8 +190,8 @@ __global__ void __launch_bounds__(block_threads(THREADS)) k_layer_norm_backward(
 }
 
 // Rows past what registers hold: dx alone, in two passes over the row; with the
-// columns' sums below, 2^26 bf16 elements take 183 us where a row in registers
-// takes 110.
+// columns' sums below, 2^26 bf16 elements take 149 us (rows of 16,640) where rows
+// in registers take 100 (16,384).
 template <int DT, int WDT>
 __global__ void __launch_bounds__(1024) k_layer_norm_backward_wide(NormBackwardArgs a) {
     constexpr int V = kRowVec<DT>;
@@ -240,12 +244,12 @@ __global__ void __launch_bounds__(1024) k_layer_norm_backward_wide(NormBackwardA
 }
 
 // The partial sums of such rows, before dx is written (dx may be dy): a
-// workgroup takes 256 vectors of columns and every a.blocks-th row.
+// workgroup takes one vector of columns a thread and every a.blocks-th row.
 template <int DT>
-__global__ void __launch_bounds__(256) k_layer_norm_columns(NormBackwardArgs a) {
+__global__ void __launch_bounds__(kColumnThreads) k_layer_norm_columns(NormBackwardArgs a) {
     constexpr int V = kRowVec<DT>;
     const int rank = blockIdx.z;
-    const uint64_t c = (static_cast<uint64_t>(blockIdx.x) * 256 + threadIdx.x) * V;
+    const uint64_t c = (static_cast<uint64_t>(blockIdx.x) * kColumnThreads + threadIdx.x) * V;
     if (c >= a.cols) return;
     float dg[V], db[V];
 #pragma unroll
@@ -304,9 +308,8 @@ hipError_t start(const NormBackwardArgs& a, int nranks, bool weights, hipStream_
     const dim3 block(block_threads(THREADS));
     if constexpr (NV == 0) {
         if (weights) {
-            constexpr uint64_t per = 256 * kRowVec<DT>;
-            const dim3 columns(static_cast<unsigned>((a.cols + per - 1) / per), a.blocks, nranks);
-            hipLaunchKernelGGL((k_layer_norm_columns<DT>), columns, dim3(256), 0, s, a);
+            const dim3 columns(static_cast<unsigned>(column_stretches(a.cols, kRowVec<DT>)), a.blocks, nranks);
+            hipLaunchKernelGGL((k_layer_norm_columns<DT>), columns, dim3(kColumnThreads), 0, s, a);
             const hipError_t e = hipGetLastError();
             if (e != hipSuccess) return e;
         }

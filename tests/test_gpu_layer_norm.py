@@ -400,3 +400,45 @@ def test_made_outputs_are_tensors_of_their_own(ar):
     del ys, means, rstds
     torch.empty(1 << 20, device="cuda").fill_(3.0)
     assert torch.equal(only, kept[2])
+
+
+@pytest.mark.parametrize("cols", [9, 17, 1003, 4095])
+def test_infinite_weight(ar, cols):
+    """One infinite weight in the last columns: the formula's infinities, and NaN only where it has them."""
+    torch = _torch()
+    for at in (cols - 1, cols - 5):
+        x = torch.randn(6, cols, device="cuda")
+        dy = torch.randn(6, cols, device="cuda").abs() + 0.1
+        g = torch.ones(cols, device="cuda")
+        g[at] = math.inf
+        _, m, s = ar.ar_layer_norm([x])
+        dxs, _, _ = ar.ar_layer_norm_backward([dy], [x], [g], m, s)
+        d, h = dy.double(), (x.double() - m[0].double()[:, None]) * s[0].double()[:, None]
+        w = d * g.double()
+        want = s[0].double()[:, None] * (w - w.mean(1, keepdim=True) - h * (w * h).mean(1, keepdim=True))
+        got = dxs[0].double()
+        assert torch.equal(torch.isnan(got), torch.isnan(want))
+        inf = torch.isinf(want)
+        assert inf.any() and torch.equal(got[inf], want[inf])
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("ranks,rows,cols", [(1, 70, 33000), (3, 11, 40001), (2, 300, 16385), (40, 3, 33001), (1, 5, 300007)])
+def test_wide_rows_weight_gradients(ar, dtype, ranks, rows, cols):
+    """Rows past the registers: every stretch of columns and every share of the rows reaches the sums."""
+    from step_util import UNIT
+
+    torch = _torch()
+    dt = {"f32": torch.float32, "bf16": torch.bfloat16}[dtype]
+    xs = [torch.randn(rows, cols, device="cuda").to(dt) for _ in range(ranks)]
+    dys = [torch.randn(rows, cols, device="cuda").to(dt) for _ in range(ranks)]
+    _, m, s = ar.ar_layer_norm(xs)
+    _, dg, db = ar.ar_layer_norm_backward(dys, xs, None, m, s)
+    for r in range(ranks):
+        d = dys[r].double()
+        h = (xs[r].double() - m[r].double()[:, None]) * s[r].double()[:, None]
+        for got, terms in ((dg[r], d * h), (db[r], d)):
+            want, size = terms.sum(0), terms.abs().sum(0)
+            # float32 sums of `rows` terms, each with three roundings, then the type's own
+            bound = size * (rows + 5) * 2.0 ** -23 + want.abs() * UNIT[dtype] + 1e-30
+            assert bool(((got.double() - want).abs() <= bound).all())
