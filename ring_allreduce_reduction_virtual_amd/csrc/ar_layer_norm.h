@@ -106,13 +106,17 @@ inline RowShape backward_shape(uint64_t cols, int vector_elements) {
 // every one still has 64 rows, over which its partial sums' traffic is small.
 // Rows over 512 threads fill it with half as many (us, 512 / 256 workgroups:
 // 4 x 1,024 x 8,192 bf16 56 / 49, 2 x 512 x 16,384 bf16 47 / 37, 4 x 512 x
-// 16,384 float32 103 / 93; 1,024 rows of 1,024 on 256 threads 14 / 18).
+// 16,384 float32 103 / 93).  Rows over 128 threads leave it half full, so up
+// to twice as many while every one has 8 rows (us, 512 / 1,024 workgroups: 4 x
+// 4,096 x 768 bf16 34 / 24, 8 x 1,024 x 768 20 / 16, 2 x 8,192 x 512 float32 30 /
+// 26, but 4,096 rows of 1,024 bf16 15.9 / 17.3).
 //
 // Wide rows: their sums are made by stretches of kColumnThreads vectors, and
 // kColumnBlocks of these fill the GPU (us with about 4,000 / 2,000 / 1,000 /
 // 500 workgroups: 2 x 512 x 40,000 bf16 148 / 121 / 105 / 102; 1,024 x 50,257
 // bf16 168 / 158 / 165 for 3,200 / 1,600 / 800).
-constexpr uint64_t kBackwardBlocks = 512, kBackwardLongBlocks = 256, kBackwardMostBlocks = 4096, kBackwardRows = 64;
+constexpr uint64_t kBackwardBlocks = 512, kBackwardLongBlocks = 256, kBackwardMostBlocks = 4096;
+constexpr uint64_t kBackwardRows = 64, kBackwardFewRows = 8;
 constexpr int kColumnThreads = 256;
 constexpr uint64_t kColumnBlocks = 1024;
 inline uint64_t column_stretches(uint64_t cols, int vector_elements) {
@@ -126,8 +130,10 @@ inline uint32_t backward_blocks(uint64_t rows, uint64_t cols, int nranks, int ve
     if (shape.vectors == 0) {
         wanted = kColumnBlocks / column_stretches(cols, vector_elements);
     } else {
-        wanted = std::max(shape.threads > 256 ? kBackwardLongBlocks : kBackwardBlocks, rows * nranks / kBackwardRows);
-        wanted = std::min(kBackwardMostBlocks, wanted);
+        const uint64_t total = rows * nranks;
+        uint64_t least = shape.threads > 256 ? kBackwardLongBlocks : kBackwardBlocks;
+        if (shape.threads == 128) least = std::min(2 * least, std::max(least, total / kBackwardFewRows));
+        wanted = std::min(kBackwardMostBlocks, std::max(least, total / kBackwardRows));
     }
     wanted = std::max<uint64_t>(1, wanted / nranks);
     return static_cast<uint32_t>(std::min<uint64_t>((rows + at_once - 1) / at_once, wanted));
