@@ -237,9 +237,9 @@ __device__ __forceinline__ float sum_over_lanes(float x) {
 template <bool SIGNED>
 constexpr int kCodeShift = SIGNED ? 15 : 31;
 
-// The scale byte of a block whose largest magnitude has these bits: adding just
-// under an eighth of the exponent's step carries when the mantissa is above
-// 1.875.
+// The scale byte of a block whose largest magnitude, finite or infinite, has
+// these bits: adding just under an eighth of the exponent's step carries when
+// the mantissa is above 1.875.
 __device__ __forceinline__ uint32_t scale_for(uint32_t top_bits) {
     const uint32_t e = (top_bits + 0x000fffffu) >> 23;
     return e == 0 ? 1 : (e > 255 ? 255 : e);

@@ -329,11 +329,12 @@ __device__ __forceinline__ void packed_tile(const PackedEntry& e, const AdamwSca
         vtop = as_u(vn[j]) > vtop ? as_u(vn[j]) : vtop;   // v is never negative
     }
     // The maximum of m passes over NaN.  One comes only with the gradient's, and
-    // that makes v, whose bits compare as integers, a NaN too.
+    // that makes v, whose bits compare as integers, a NaN too, of the gradient's
+    // sign: no magnitude that scale_for could take.
     vtop = max_over_lanes<32>(vtop);
     const bool nan = vtop > 0x7f800000u;
     const uint32_t me_new = mbad || nan ? 255 : scale_for(max_over_lanes<32>(as_u(mtop)));
-    const uint32_t ve_new = vbad ? 255 : scale_for(vtop);
+    const uint32_t ve_new = vbad || nan ? 255 : scale_for(vtop);
     const uint32_t key = mix32(s.seed + 0x9e3779b9u * (e.index + 1)) + 0x9e3779b9u * static_cast<uint32_t>(at);
     uint32_t mo[V], vo[V], least = 0xffffffffu;
 #pragma unroll

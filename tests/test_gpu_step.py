@@ -766,3 +766,37 @@ def test_negative_views_refused(ar):
     x = torch._neg_view(torch.ones(2, 64, device="cuda"))
     with pytest.raises(ValueError, match="contiguous rows"):
         ar.ar_layer_norm([x])
+
+
+NAN_BITS = {"f32": [0x7FC00000, 0xFFC00000, 0x7FFFFFFF, 0xFFFFFFFF, 0xFFF00001, 0xFF800001, 0xFFFF0000],
+            "bf16": [0x7FC0, 0xFFC0, 0x7FFF, 0xFFFF, 0xFFF1, 0xFF81], "f16": [0x7E00, 0xFE00, 0x7FFF, 0xFFFF, 0xFF81, 0xFC01]}
+
+
+@pytest.mark.parametrize("param,grad", [("f32", "f32"), ("f32", "bf16"), ("bf16", "bf16"), ("f16", "f16")])
+def test_packed_nan_gradients(ar, param, grad):
+    """A NaN gradient of any sign and payload makes its block of both states NaN, and no other block."""
+    torch = _torch()
+    n, at = 1030, 700
+    rng = np.random.default_rng(21)
+    block = slice(at // 256 * 256, at // 256 * 256 + 256)
+    values = rng.standard_normal(n).astype(np.float32)
+    for bits in NAN_BITS[grad]:
+        g = on_device(values, grad)
+        whole = g.view(torch.int32 if grad == "f32" else torch.int16)
+        whole[at] = bits - (1 << (32 if grad == "f32" else 16)) if bits >> (31 if grad == "f32" else 15) else bits
+        assert int(torch.isnan(g).sum()) == 1
+        p = torch.zeros(n, dtype=torch_dtype(param), device="cuda")
+        m, v = (ar.PackedState.zeros(n, "cuda") for _ in range(2))
+        ar.ar_adamw_packed([p], [g], [m], [v], step=1, lr=0.1, seed=3)
+        clean = f32(g)
+        clean[at] = 0.0
+        zero = np.zeros(n, np.float32)
+        new = oracle.moments_f32(clean, zero, zero, (0.9, 0.999), 1.0)
+        for state, x, kind in ((m, new[0], "exp_avg"), (v, new[1], "exp_avg_sq")):
+            codes, scales = oracle.pack(x, oracle.random_bits(3, 0, n), kind)
+            codes[block], scales[at // 256] = 0, 255
+            assert np.array_equal(state.scales.cpu().numpy(), scales), (hex(bits), kind)
+            assert np.array_equal(state.codes.cpu().numpy(), codes), (hex(bits), kind)
+            bad = torch.isnan(ar.ar_unpack_states([state], kind)[0])
+            assert bad[block].all() and int(bad.sum()) == 256, (hex(bits), kind)
+        assert torch.isnan(p[at]) and int((~torch.isfinite(p)).sum()) == 1, hex(bits)
