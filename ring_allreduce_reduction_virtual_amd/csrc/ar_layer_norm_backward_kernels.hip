@@ -75,10 +75,10 @@ __global__ void __launch_bounds__(block_threads(THREADS)) k_layer_norm_backward(
     for (int u = 0; u < NV; ++u) {
         if (gamma != nullptr) RowPart<THREADS, V>(u, cols).template load<false>(g[u], gamma, cols);
     }
-    if (cols % V != 0) {   // an infinite weight times a cleared dy would be NaN
+    // an infinite weight times a cleared dy would be NaN: a moved-back vector has
+    // one of each, also where a whole number of vectors leaves threads without any
 #pragma unroll
-        for (int u = 0; u < NV; ++u) RowPart<THREADS, V>(u, cols).clear(g[u]);
-    }
+    for (int u = 0; u < NV; ++u) RowPart<THREADS, V>(u, cols).clear(g[u]);
 #pragma unroll
     for (int k = 0; k < EACH; ++k) dg[k] = db[k] = 0;
     int turn = 0;

@@ -442,3 +442,26 @@ def test_wide_rows_weight_gradients(ar, dtype, ranks, rows, cols):
             # float32 sums of `rows` terms, each with three roundings, then the type's own
             bound = size * (rows + 5) * 2.0 ** -23 + want.abs() * UNIT[dtype] + 1e-30
             assert bool(((got.double() - want).abs() <= bound).all())
+
+
+@pytest.mark.parametrize("dtype,wdtype", [("f32", "f32"), ("bf16", "bf16"), ("bf16", "f32"), ("f16", "f16")])
+@pytest.mark.parametrize("cols", [72, 768, 1000, 1024, 1536, 5120, 6144, 12288])
+def test_infinite_weight_in_rows_of_whole_vectors(ar, dtype, wdtype, cols):
+    """The same where the row is a whole number of vectors, which leaves some of its threads without one."""
+    torch = _torch()
+    dt, wdt = torch_dtype(dtype), torch_dtype(wdtype)
+    for at in (cols - 1, cols - 4, 0):
+        x = torch.randn(6, cols, device="cuda").to(dt)
+        dy = (torch.randn(6, cols, device="cuda").abs() + 0.1).to(dt)
+        g = torch.ones(cols, device="cuda", dtype=wdt)
+        g[at] = math.inf
+        _, m, s = ar.ar_layer_norm([x])
+        dxs, dgs, dbs = ar.ar_layer_norm_backward([dy], [x], [g], m, s)
+        d, h = dy.double(), (x.double() - m[0].double()[:, None]) * s[0].double()[:, None]
+        w = d * g.double()
+        want = s[0].double()[:, None] * (w - w.mean(1, keepdim=True) - h * (w * h).mean(1, keepdim=True))
+        got = dxs[0].double()
+        assert torch.equal(torch.isnan(got), torch.isnan(want))
+        inf = torch.isinf(want)
+        assert inf.any() and torch.equal(got[inf], want[inf])
+        assert torch.isfinite(dgs[0]).all() and torch.isfinite(dbs[0]).all()
