@@ -571,13 +571,14 @@ ar_result_t ar_adamw(const ar_adamw_tensors_t* tensors, const ar_adamw_config_t*
  * So zeroed codes and scales are zero states.  e = 255 makes the whole block
  * NaN: a block that would hold a NaN, an infinity or a value past float32's
  * largest code gets it.  The step works on the decoded float32 states as
- * ar_adamw does, updates the parameters from the new states before they are
- * rounded (their quotient within a few units of float32's last place, where
- * ar_adamw rounds every operation correctly), and rounds each new state to one of its two neighbouring codes, up
- * with the probability of its place between them: a second moment moves by
- * 1 - beta2 of itself a step, far less than the distance of two codes, and
- * rounding to the nearest would never move it.  The 32 random bits of element i of
- * tensor t are h(h(seed + 0x9E3779B9 * (t + 1)) + 0x9E3779B9 * i) in 32-bit
+ * ar_adamw does and updates the parameters from the new states before they
+ * are rounded (16-bit parameters by a quotient within a few units of float32's
+ * last place, where ar_adamw, and this step for float32 parameters, round every
+ * operation correctly).  It rounds each new state to one of its two
+ * neighbouring codes, up with the probability of its place between them: a
+ * second moment moves by 1 - beta2 of itself a step, far less than the distance
+ * of two codes, and rounding to the nearest would never move it.  The 32
+ * random bits of element i of tensor t are h(h(seed + 0x9E3779B9 * (t + 1)) + 0x9E3779B9 * i) in 32-bit
  * arithmetic, h(x): x ^= x >> 16, x *= 0x7FEB352D, x ^= x >> 15,
  * x *= 0x846CA68B, x ^= x >> 16 (a 32-bit mixer from C. Wellons' published
  * search for integer hash functions); the lower 16 serve exp_avg, the upper

@@ -800,3 +800,22 @@ def test_packed_nan_gradients(ar, param, grad):
             bad = torch.isnan(ar.ar_unpack_states([state], kind)[0])
             assert bad[block].all() and int(bad.sum()) == 256, (hex(bits), kind)
         assert torch.isnan(p[at]) and int((~torch.isfinite(p)).sum()) == 1, hex(bits)
+
+
+@pytest.mark.parametrize("grad,copy", [("f32", None), ("bf16", "bf16"), ("f16", "f16")])
+@pytest.mark.parametrize("eps", [1e-8, 1e-3])
+def test_packed_float32_parameters_are_the_plain_steps(ar, grad, copy, eps):
+    """With float32 parameters both steps round every operation: from the same states the same bits."""
+    torch = _torch()
+    rng = np.random.default_rng(31)
+    n = 50_003
+    p, g, _, _ = make_inputs(rng, n, "f32", grad)
+    (m, m32), (v, v32) = packed_inputs(ar, rng, n, 1)
+    config = dict(HYPER, eps=eps)
+    copies = [None if copy is None else [torch.zeros(n, dtype=torch_dtype(copy), device="cuda")] for _ in range(2)]
+    plain = [[p.clone()], [g], [on_device(m32, "f32")], [on_device(v32, "f32")]]
+    ar.ar_adamw(*plain, copies=copies[0], **config)
+    ar.ar_adamw_packed([p], [g], [m], [v], copies=copies[1], seed=2, **config)
+    assert torch.equal(p, plain[0][0])
+    if copy is not None:
+        assert torch.equal(copies[0][0], copies[1][0])
