@@ -505,7 +505,9 @@ ar_result_t ar_grad_norm(const void* const* grads, const size_t* counts, int nte
  *   d  = sqrt(v') * (1 / sqrt(1 - beta2^t)) + eps
  *   p' = p * (1 - lr * weight_decay) - (m' / d) * (lr / (1 - beta1^t))
  * with the scalars that name no tensor computed in float64 on the host and
- * rounded once; a norm that is NaN makes c NaN.  (Decoupled weight decay: Loshchilov and Hutter, "Decoupled Weight
+ * rounded once; a norm that is NaN makes c NaN.  A positive eps, max_norm or
+ * grad_scale that float32 rounds to 0 is refused, and so is a scalar past its
+ * range.  (Decoupled weight decay: Loshchilov and Hutter, "Decoupled Weight
  * Decay Regularization", 2019, algorithm 2.)  grad_scale undoes a loss scale
  * (its inverse), or averages a sum over ranks.  With skip_nonfinite, a norm
  * that is NaN or infinite makes the call leave every parameter and state as
@@ -650,8 +652,9 @@ ar_result_t ar_update_free(ar_update_t update);
  * (rows float32 each; both arrays NULL when no backward pass follows).
  * weight_dtype is dtype or AR_FLOAT32.  y[r] may be x[r] with the same
  * stride (two buffers interleaved in one, their strides equal and their rows
- * apart, are also fine); outputs overlap nothing else.  rows == 0 or
- * cols == 0 is a successful no-op. */
+ * apart, are also fine); outputs overlap nothing else.  eps >= 0; a positive
+ * one that float32 rounds to 0 is refused.  rows == 0 or cols == 0 is a
+ * successful no-op. */
 ar_result_t ar_layer_norm(const void* const* x, const void* const* gamma, const void* const* beta, void* const* y,
                           float* const* mean, float* const* rstd, size_t rows, size_t cols, size_t x_stride,
                           size_t y_stride, ar_dtype_t dtype, ar_dtype_t weight_dtype, double eps, int nranks,

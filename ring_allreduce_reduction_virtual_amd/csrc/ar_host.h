@@ -46,6 +46,9 @@ ar_result_t guarded(Body body) {
 
 inline bool float_type(ar_dtype_t dt) { return dt == AR_FLOAT32 || dt == AR_BFLOAT16 || dt == AR_FLOAT16; }
 
+// A positive setting that float32 takes for 0.
+inline bool rounds_to_zero(double x) { return x > 0 && static_cast<float>(x) == 0.0f; }
+
 // A buffer of `bytes` bytes (rows of `row` bytes, `stride` bytes apart, when
 // stride is not 0).
 struct Range {

@@ -59,6 +59,7 @@ ar_result_t ar_layer_norm(const void* const* x, const void* const* gamma, const 
             (rc = check_stride(y_stride, rows, cols, "y_stride")) != AR_SUCCESS)
             return rc;
         if (!(eps >= 0 && eps < 1e30)) return fail_with(AR_ERR_INVALID_ARGUMENT, "eps %g is not a finite number >= 0", eps);
+        if (rounds_to_zero(eps)) return fail_with(AR_ERR_INVALID_ARGUMENT, "eps %g is 0 in float32", eps);
         if (x == nullptr || y == nullptr) return fail_with(AR_ERR_INVALID_ARGUMENT, "null pointer array");
         if ((mean == nullptr) != (rstd == nullptr))
             return fail_with(AR_ERR_INVALID_ARGUMENT, "mean and rstd are wanted together or not at all");

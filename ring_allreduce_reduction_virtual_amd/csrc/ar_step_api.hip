@@ -11,6 +11,7 @@
 #include <cmath>
 #include <cstring>
 #include <limits>
+#include <utility>
 
 #include "ar_host.h"
 #include "ar_step.h"
@@ -201,7 +202,19 @@ ar_result_t scalars(const ar_adamw_config_t* c, const float* grad_norm, ar_dtype
         return fail_with(AR_ERR_INVALID_ARGUMENT, "max_norm and skip_nonfinite need grad_norm");
     if (reinterpret_cast<uintptr_t>(grad_norm) % alignof(float) != 0)
         return fail_with(AR_ERR_INVALID_ARGUMENT, "grad_norm not aligned to its 4-byte element");
+    // what the kernels get is float32: a setting that is on must not round to off
+    for (const auto& [x, name] : {std::pair<double, const char*>{c->eps, "eps"},
+                                  {c->max_norm, "max_norm"},
+                                  {c->grad_scale, "grad_scale"}}) {
+        if (rounds_to_zero(x)) return fail_with(AR_ERR_INVALID_ARGUMENT, "%s %g is 0 in float32", name, x);
+    }
     const double t = static_cast<double>(c->step);
+    const double step_size = c->lr / (1 - std::pow(c->beta1, t)), decay = 1 - c->lr * c->weight_decay;
+    if (!(step_size <= most))
+        return fail_with(AR_ERR_INVALID_ARGUMENT, "lr %g / (1 - beta1^step) is past float32's range", c->lr);
+    if (!(decay >= -most))
+        return fail_with(AR_ERR_INVALID_ARGUMENT, "lr %g * weight_decay %g is past float32's range", c->lr,
+                         c->weight_decay);
     AdamwScalars s{};
     s.grad_norm = grad_norm;
     s.beta1 = static_cast<float>(c->beta1);
@@ -209,8 +222,8 @@ ar_result_t scalars(const ar_adamw_config_t* c, const float* grad_norm, ar_dtype
     s.beta2 = static_cast<float>(c->beta2);
     s.one_minus_beta2 = static_cast<float>(1 - c->beta2);
     s.eps = static_cast<float>(c->eps);
-    s.decay = static_cast<float>(1 - c->lr * c->weight_decay);
-    s.step_size = static_cast<float>(c->lr / (1 - std::pow(c->beta1, t)));
+    s.decay = static_cast<float>(decay);
+    s.step_size = static_cast<float>(step_size);
     s.rsqrt_correction2 = static_cast<float>(1 / std::sqrt(1 - std::pow(c->beta2, t)));
     s.max_norm = static_cast<float>(c->max_norm);
     s.grad_scale = static_cast<float>(c->grad_scale);

@@ -280,3 +280,36 @@ def test_native_marshalling_declines_what_it_does_not_know():
     assert m.states([(cpu, cpu)], 0, [4]) is None and m.states([(cpu,)], 0, [4]) is None
     assert m.new_parts([2, 3], f32, 0) is None and m.new_parts((), f32, 0) is None
     assert m.new_parts((2, "x"), f32, 0) is None and m.new_parts((2, -1), f32, 0) is None
+
+
+@pytest.mark.parametrize("packed", [False, True])
+def test_settings_that_float32_cannot_hold_are_refused(lib, packed):
+    """A positive setting that would round to 0 would switch itself off, and an infinite scalar spoils parameters."""
+    fn = lib.ar_adamw_packed if packed else lib.ar_adamw
+    t = tensors(2, [0, 0], packed=packed)
+    norm = BASE + 801 * GAP
+
+    def call(**change):
+        return fn(ctypes.byref(t), ctypes.byref(config(**change)), norm, None)
+
+    for name in ("max_norm", "grad_scale", "eps"):
+        for small in (1e-46, 5e-324):
+            assert call(**{name: small}) == INVALID and name in detail(lib), (name, small)
+        assert call(**{name: 1e-45}) == 0 and call(**{name: 3.4e38}) == 0, name
+    assert call(eps=0.0, max_norm=0.0) == 0
+    assert call(lr=3e38, beta1=0.99) == INVALID and "lr" in detail(lib)
+    assert call(lr=3e38, beta1=0.0) == 0 and call(lr=3e38, beta1=0.99, step=10**6) == 0
+    assert call(lr=1e30, weight_decay=1e30) == INVALID and "weight_decay" in detail(lib)
+    assert call(lr=1e-46, weight_decay=1e-46) == 0
+    handle = ctypes.c_void_p()
+    init = lib.ar_adamw_packed_init if packed else lib.ar_adamw_init
+    assert init(ctypes.byref(t), None, 0, None, ctypes.byref(handle)) == 0
+    assert lib.ar_adamw_start(handle, ctypes.byref(config(max_norm=1e-46)), norm, None) == INVALID
+    assert lib.ar_update_free(handle) == 0
+
+
+def test_layer_norm_eps_that_float32_cannot_hold_is_refused(lib):
+    x, y = ptrs([BASE]), ptrs([BASE + GAP])
+    for eps, want in ((1e-46, INVALID), (5e-324, INVALID), (1e-45, 0), (0.0, 0)):
+        assert lib.ar_layer_norm(x, None, None, y, None, None, 0, 8, 8, 8, 0, 0, eps, 1, None) == want, eps
+        assert want == 0 or "eps" in detail(lib)
