@@ -91,10 +91,12 @@ inline ar_result_t check_ranges(std::vector<Range>& v) {
             if ((!x->writable && !cur.writable) || rows_apart(*x, cur)) continue;
             return fail_with(AR_ERR_INVALID_ARGUMENT, "%s[%d] overlaps %s[%d]", x->what, x->index, cur.what, cur.index);
         }
-        // read-only ranges that share their end and start say the same thing once
-        // (many ranks reading one weight)
+        // read-only ranges of the same bytes, rows and gaps alike, say the same thing
+        // once (many ranks reading one weight)
         bool same = false;
-        for (const Range* x : active) same = same || (x->lo == cur.lo && x->hi == cur.hi && !cur.writable);
+        for (const Range* x : active)
+            same = same || (x->lo == cur.lo && x->hi == cur.hi && x->row == cur.row && x->stride == cur.stride &&
+                            !cur.writable);
         if (!same) active.push_back(&cur);
     }
     return AR_SUCCESS;

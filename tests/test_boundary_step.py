@@ -313,3 +313,15 @@ def test_layer_norm_eps_that_float32_cannot_hold_is_refused(lib):
     for eps, want in ((1e-46, INVALID), (5e-324, INVALID), (1e-45, 0), (0.0, 0)):
         assert lib.ar_layer_norm(x, None, None, y, None, None, 0, 8, 8, 8, 0, 0, eps, 1, None) == want, eps
         assert want == 0 or "eps" in detail(lib)
+
+
+def test_read_only_buffers_of_one_span_are_each_checked(lib):
+    """Rows with gaps and a whole buffer may start and end together: an output in the gaps overlaps the whole one."""
+    names = ("dy", "x", "gamma", "mean", "rstd", "dx", "dgamma", "dbeta")
+    good = {k: ptrs([BASE + 10 * i * GAP]) for i, k in enumerate(names)}
+    x = good["x"][0]
+    for a in ("mean", "rstd"):
+        # two rows of one 2-byte element, 6 bytes apart: bytes 0-7 with x, and 2-9 with dx in x's gap
+        args = dict(good, gamma=None, dgamma=None, dbeta=None, dx=ptrs([x + 2]), **{a: ptrs([x])})
+        rc = lib.ar_layer_norm_backward(*[args[k] for k in names], 2, 1, 3, 3, 3, 1, 1, 1, None, 0, None)
+        assert rc == INVALID and "overlaps" in detail(lib) and a in detail(lib)
