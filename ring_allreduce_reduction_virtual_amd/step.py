@@ -117,6 +117,8 @@ def _scalar(t, dev, what):
     """Address of a one-element float32 tensor on `dev`."""
     if not isinstance(t, torch.Tensor) or t.device != dev or t.dtype is not torch.float32 or t.numel() != 1:
         raise ValueError(f"{what} must be a float32 tensor of one element on {dev}")
+    if t.is_neg():
+        raise ValueError(f"{what} must be no negative view")
     return t.data_ptr()
 
 

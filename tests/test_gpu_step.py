@@ -819,3 +819,21 @@ def test_packed_float32_parameters_are_the_plain_steps(ar, grad, copy, eps):
     assert torch.equal(p, plain[0][0])
     if copy is not None:
         assert torch.equal(copies[0][0], copies[1][0])
+
+
+def test_negative_norms_refused(ar):
+    """The norm's own tensor neither: read in place it is another number, written it would read as minus the norm."""
+    torch = _torch()
+    g = [torch.ones(64, device="cuda")]
+    norm = torch._neg_view(torch.full((1,), 4.0, device="cuda"))
+    with pytest.raises(ValueError, match="negative"):
+        ar.ar_grad_norm(g, norm=norm)
+    with pytest.raises(ValueError, match="negative"):
+        ar.ar_grad_norm_init(g, norm=norm)
+    args = [[torch.ones(64, device="cuda")] for _ in range(4)]
+    with pytest.raises(ValueError, match="negative"):
+        ar.ar_adamw(*args, step=1, lr=0.1, grad_norm=norm, max_norm=1.0)
+    plan = ar.ar_adamw_init(*args)
+    with pytest.raises(ValueError, match="negative"):
+        plan.start(step=1, lr=0.1, grad_norm=norm, max_norm=1.0)
+    assert all((a[0] == 1).all() for a in args)
