@@ -15,6 +15,11 @@ one tensor per virtual rank, as the collectives do.
 Tensors the functions make themselves come from torch's allocator, in the
 memory of the stream that the work is enqueued on, as if the call were made
 under ``torch.cuda.stream(stream)``.
+
+Autograd records none of these functions: their outputs require no gradient.
+What a call or a plan's start writes into counts as changed in place (the
+tensor's version), so that a backward pass which still needs the old values
+raises; the replays of a HIP graph count nothing.
 """
 
 from __future__ import annotations
@@ -87,6 +92,17 @@ def _refuse(t, dev, index, dtype, count, what, i):
         raise ValueError(f"{what}[{i}] must hold {count} elements")
 
 
+def _written(*groups):
+    """Count a write into every tensor of the sequences (of tensors or packed states; None: none)."""
+    for group in groups:
+        if group is None or (_fast and _fast.written(group)):
+            continue
+        for item in group:
+            for t in (item,) if isinstance(item, torch.Tensor) else item:
+                if not t.is_inference():
+                    torch.autograd.graph.increment_version(t)
+
+
 def _counts(sizes):
     return (ctypes.c_size_t * max(len(sizes), 1))(*sizes)
 
@@ -152,10 +168,13 @@ def _norm_call(grads, norm, workspace, stream):
 
 def ar_grad_norm(grads, norm=None, workspace=None, stream=None):
     """The global 2-norm of all the gradients, in a float32 tensor of one element (`norm`, made if not given)."""
+    given = norm
     dev, args, norm, workspace = _norm_call(grads, norm, workspace, stream)
     with _on_device(dev):
         rc = _lib.lib().ar_grad_norm(*args, _stream_handle(stream, dev.index))
     _lib.check("ar_grad_norm", rc)
+    if given is not None:
+        _written((given,))
     return norm
 
 
@@ -240,7 +259,9 @@ def _adamw(packed, params, grads, exp_avgs, exp_avg_sqs, out, copies, config, gr
         rc = getattr(_lib.lib(), name)(ctypes.byref(t), ctypes.byref(config), norm, _stream_handle(stream, dev.index))
     _lib.check(name, rc)
     del keep
-    return (params, exp_avgs, exp_avg_sqs) if out is None else out
+    new = (params, exp_avgs, exp_avg_sqs) if out is None else out
+    _written(*new, copies)
+    return new
 
 
 def ar_adamw(params, grads, exp_avgs, exp_avg_sqs, out=None, copies=None, *, step, lr, betas=(0.9, 0.999), eps=1e-8,
@@ -278,6 +299,7 @@ def ar_unpack_states(states, kind: str, outs=None, dtype=torch.float32, stream=N
     dev, index = c0.device, c0.get_device()
     sizes = [c.numel() for c in codes]
     cp, sp = _packed_pointers(states, dev, index, sizes, "states")
+    given = outs
     if outs is None:
         outs = [_empty(s, dtype, dev, stream) for s in sizes]
     o0 = _first(outs, "outs")
@@ -286,6 +308,7 @@ def ar_unpack_states(states, kind: str, outs=None, dtype=torch.float32, stream=N
         rc = _lib.lib().ar_unpack_states(cp, sp, op, _counts(sizes), len(sizes), _lib.STATES[kind],
                                          _lib.DTYPES[_dtype_of(o0, "outs")], _stream_handle(stream, dev.index))
     _lib.check("ar_unpack_states", rc)
+    _written(given)
     return outs
 
 
@@ -302,13 +325,14 @@ class Update:
     keep the tensors alive until then.
     """
 
-    def __init__(self, kind, handle, device, keep, norm=None):
+    def __init__(self, kind, handle, device, keep, writes, norm=None):
         self.kind = kind
         self.device = device
         self.norm = norm
         self._handle = handle
         self._index = device.index
         self._keep = keep
+        self._writes = writes
 
     @property
     def num_launches(self) -> int:
@@ -324,6 +348,7 @@ class Update:
                 raise TypeError(f"a gradient norm takes no {sorted(config)}")
             rc = _lib.lib().ar_grad_norm_start(self._handle, _stream_handle(stream, self._index))
             _lib.check("ar_grad_norm_start", rc)
+            _written(self._writes)
             return self.norm
         self._start_step(stream, **config)
         return None
@@ -336,12 +361,13 @@ class Update:
         norm = None if grad_norm is None else _scalar(grad_norm, self.device, "grad_norm")
         rc = _lib.lib().ar_adamw_start(self._handle, ctypes.byref(config), norm, _stream_handle(stream, self._index))
         _lib.check("ar_adamw_start", rc)
+        _written(self._writes)
 
     def close(self):
         if self._handle is not None:
             _lib.lib().ar_update_free(self._handle)
             self._handle = None
-            self._keep = None
+            self._keep = self._writes = None
 
     def __del__(self):
         try:
@@ -357,7 +383,7 @@ def ar_grad_norm_init(grads, norm=None, workspace=None) -> Update:
     with _on_device(dev):
         rc = _lib.lib().ar_grad_norm_init(*args, _stream_handle(None, dev.index), ctypes.byref(handle))
     _lib.check("ar_grad_norm_init", rc)
-    return Update("grad_norm", handle, dev, (list(grads), norm, workspace), norm)
+    return Update("grad_norm", handle, dev, (list(grads), workspace), (norm,), norm)
 
 
 def _adamw_init(kind, params, grads, exp_avgs, exp_avg_sqs, out, copies, workspace):
@@ -369,7 +395,10 @@ def _adamw_init(kind, params, grads, exp_avgs, exp_avg_sqs, out, copies, workspa
         rc = getattr(_lib.lib(), f"ar_{kind}_init")(ctypes.byref(t), wp, wb, _stream_handle(None, dev.index),
                                                     ctypes.byref(handle))
     _lib.check(f"ar_{kind}_init", rc)
-    return Update(kind, handle, dev, (keep, workspace))
+    new = (params, exp_avgs, exp_avg_sqs) if out is None else out
+    writes = [t for group in (*new, copies or ()) for item in group
+              for t in ((item,) if isinstance(item, torch.Tensor) else item)]
+    return Update(kind, handle, dev, (keep, workspace), writes)
 
 
 def ar_adamw_init(params, grads, exp_avgs, exp_avg_sqs, out=None, copies=None, workspace=None) -> Update:
@@ -482,6 +511,8 @@ def ar_layer_norm(xs, gammas=None, betas=None, ys=None, eps: float = 1e-5, stats
     are None.  Rows may lie further apart than their length, by the same
     stride on every rank.  Weights are one per rank, in the activations' type
     or float32; None means 1 (`gammas`) or 0 (`betas`).  In place: ``ys=xs``.
+    Autograd does not see the call: the gradients are the caller's to take
+    with :func:`ar_layer_norm_backward`.
     """
     x0 = _rank_list(xs, "xs")
     n, dev, index, dt = len(xs), x0.device, x0.get_device(), x0.dtype
@@ -491,6 +522,7 @@ def ar_layer_norm(xs, gammas=None, betas=None, ys=None, eps: float = 1e-5, stats
     wdt = _weight_dtype(dt, gammas, betas)
     gp = None if gammas is None else _weights(gammas, n, dev, index, wdt, cols, "gammas")
     bp = None if betas is None else _weights(betas, n, dev, index, wdt, cols, "betas")
+    given = ys
     if ys is None:
         (ys, yp), y_stride = _new_parts((n, rows, cols), dt, dev, stream), cols
     else:
@@ -503,6 +535,7 @@ def ar_layer_norm(xs, gammas=None, betas=None, ys=None, eps: float = 1e-5, stats
         rc = _lib.lib().ar_layer_norm(xp, gp, bp, yp, mp, rp, rows, cols, x_stride, y_stride, _lib.DTYPES[name],
                                       _lib.DTYPES[_FLOATS[wdt]], eps, n, _stream_handle(stream, dev.index))
     _lib.check("ar_layer_norm", rc)
+    _written(given)
     return ys, means, rstds
 
 
@@ -532,6 +565,7 @@ def ar_layer_norm_backward(dys, xs, gammas, means, rstds, dxs=None, weight_grads
     gp = None if gammas is None else _weights(gammas, n, dev, index, wdt, cols, "gammas")
     if len(means) != n or len(rstds) != n:
         raise ValueError("need one of means and rstds per rank")
+    given = (dxs, dgammas, dbetas)
     mp = _pointers(means, dev, index, torch.float32, [rows] * n, "means")
     rp = _pointers(rstds, dev, index, torch.float32, [rows] * n, "rstds")
     if dxs is None:
@@ -555,4 +589,5 @@ def ar_layer_norm_backward(dys, xs, gammas, means, rstds, dxs=None, weight_grads
                                                dx_stride, _lib.DTYPES[name], _lib.DTYPES[_FLOATS[wdt]], n, wp, wb,
                                                _stream_handle(stream, dev.index))
     _lib.check("ar_layer_norm_backward", rc)
+    _written(*given)
     return dxs, dgammas, dbetas

@@ -325,3 +325,20 @@ def test_read_only_buffers_of_one_span_are_each_checked(lib):
         args = dict(good, gamma=None, dgamma=None, dbeta=None, dx=ptrs([x + 2]), **{a: ptrs([x])})
         rc = lib.ar_layer_norm_backward(*[args[k] for k in names], 2, 1, 3, 3, 3, 1, 1, 1, None, 0, None)
         assert rc == INVALID and "overlaps" in detail(lib) and a in detail(lib)
+
+
+def test_native_marshalling_counts_writes():
+    """Tensors and pairs of them rise by one version each; tensors without a counter and other things are passed over."""
+    import torch
+
+    m = pytest.importorskip("ring_allreduce_reduction_virtual_amd._armarshal")
+    a, b, c = (torch.zeros(4) for _ in range(3))
+    assert m.written([a, (b, c), a[1:]]) is True and m.written(()) is True
+    assert [t._version for t in (a, b, c)] == [2, 1, 1]
+    with torch.inference_mode():
+        d = torch.zeros(4)
+        assert m.written([d, a]) is True
+    assert m.written([d]) is True and a._version == 3
+    for bad in (7, None, [3], [(a, 3)], [None]):
+        assert m.written(bad) is None
+    assert m.written() is None and m.written([a], [b]) is None

@@ -837,3 +837,74 @@ def test_negative_norms_refused(ar):
     with pytest.raises(ValueError, match="negative"):
         plan.start(step=1, lr=0.1, grad_norm=norm, max_norm=1.0)
     assert all((a[0] == 1).all() for a in args)
+
+
+def versions(*tensors):
+    return [t._version for t in tensors]
+
+
+def test_written_tensors_raise_their_versions(ar, marshalling):
+    """Every tensor that a call or a plan's start writes counts as changed in place, and no other one does."""
+    torch = _torch()
+    f = lambda n=300: torch.ones(n, device="cuda")                       # noqa: E731
+    good = dict(step=1, lr=0.1)
+
+    def changed(call, *tensors):
+        before = versions(*tensors)
+        call()
+        return [a > b for a, b in zip(versions(*tensors), before)]
+
+    p, g, m, v = f(), f(), f(), f()
+    c = torch.zeros(300, dtype=torch.bfloat16, device="cuda")
+    new = [f() for _ in range(3)]
+    assert changed(lambda: ar.ar_adamw([p], [g], [m], [v], copies=[c], **good), p, g, m, v, c) == [1, 0, 1, 1, 1]
+    assert changed(lambda: ar.ar_adamw([p], [g], [m], [v], out=[[t] for t in new], **good), p, g, m, v, *new) == \
+        [0, 0, 0, 0, 1, 1, 1]
+    plan = ar.ar_adamw_init([p], [g], [m], [v], copies=[c])
+    assert changed(lambda: plan.start(**good), p, g, m, v, c) == [1, 0, 1, 1, 1]
+    a, b = (ar.PackedState.zeros(300, "cuda") for _ in range(2))
+    assert changed(lambda: ar.ar_adamw_packed([p], [g], [a], [b], seed=0, **good), p, g, *a, *b) == [1, 0, 1, 1, 1, 1]
+    plan = ar.ar_adamw_packed_init([p], [g], [a], [b], out=([new[0]], [ar.PackedState.zeros(300, "cuda")], [b]))
+    assert changed(lambda: plan.start(seed=0, **good), p, g, *a, *b, new[0]) == [0, 0, 0, 0, 1, 1, 1]
+    out = f()
+    assert changed(lambda: ar.ar_unpack_states([a], "exp_avg", outs=[out]), out, *a) == [1, 0, 0]
+    norm = torch.zeros(1, device="cuda")
+    assert changed(lambda: ar.ar_grad_norm([g], norm=norm), norm, g) == [1, 0]
+    plan = ar.ar_grad_norm_init([g], norm=norm)
+    assert changed(lambda: plan.start(), norm, g) == [1, 0]
+    x, w, y, dy, dx, dg, db = (f().view(3, 100), f(100), f().view(3, 100), f().view(3, 100), f().view(3, 100), f(100),
+                               f(100))
+    assert changed(lambda: ar.ar_layer_norm([x], [w], ys=[y]), x, w, y) == [0, 0, 1]
+    assert changed(lambda: ar.ar_layer_norm([x], [w], ys=[x]), x, w) == [1, 0]
+    _, ms, rs = ar.ar_layer_norm([x], [w])
+    assert changed(lambda: ar.ar_layer_norm_backward([dy], [x], [w], ms, rs, dxs=[dx], dgammas=[dg], dbetas=[db]),
+                   x, w, dy, *ms, *rs, dx, dg, db) == [0, 0, 0, 0, 0, 1, 1, 1]
+    # a refused call has written nothing
+    with pytest.raises(ar.ArError):
+        ar.ar_adamw([p], [g], [m], [v], step=1, lr=-1.0)
+    assert changed(lambda: pytest.raises(ar.ArError, ar.ar_adamw, [p], [g], [m], [v], step=1, lr=-1.0), p, m, v) == \
+        [0, 0, 0]
+
+
+def test_stale_graphs_are_refused(ar, marshalling):
+    """A backward pass through a parameter that a step has since replaced raises, as torch's own updates make it."""
+    torch = _torch()
+    for planned in (False, True):
+        p = torch.nn.Parameter(torch.ones(8, 8, device="cuda"))
+        g, m, v = (torch.ones(64, device="cuda") for _ in range(3))
+        x = torch.ones(8, 8, device="cuda", requires_grad=True)
+        loss = (x @ p).sum()
+        if planned:
+            ar.ar_adamw_init([p.view(64)], [g], [m], [v]).start(step=1, lr=0.1)
+        else:
+            ar.ar_adamw([p], [g], [m], [v], step=1, lr=0.1)
+        torch.cuda.synchronize()
+        with pytest.raises(RuntimeError, match="inplace operation"):
+            loss.backward()
+    with torch.inference_mode():           # such tensors have no counter, and need none
+        p = torch.ones(8, device="cuda")
+        ar.ar_adamw([p], [torch.ones(8, device="cuda")], [torch.zeros(8, device="cuda")],
+                    [torch.zeros(8, device="cuda")], step=1, lr=0.5)
+    ar.ar_adamw([p], [torch.ones(8, device="cuda")], [torch.zeros(8, device="cuda")],
+                [torch.zeros(8, device="cuda")], step=1, lr=0.5)
+    assert (p == 0).all()
