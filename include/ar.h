@@ -610,15 +610,15 @@ ar_result_t ar_unpack_states(const void* const* codes, const void* const* scales
  * done).  The table is copied on `stream`, and *_init returns when it is
  * there; it cannot run while the stream is being captured
  * (AR_ERR_UNSUPPORTED).  A start then enqueues one launch over all the
- * tensors (two for the norm of more than a million elements or so), however
- * many they are, where the one-shot calls need a launch for every few dozen
- * tensors; it can be captured into a HIP graph, which replays the config it
- * was captured with.  A workspace serves one start at a time: starts of one
- * plan follow each other on a stream or are ordered by events.  Same results
- * as the one-shot calls (the norm's float64 sum is grouped differently beyond
- * 160 tensors).  ar_adamw_start takes a plan of ar_adamw_init or
- * ar_adamw_packed_init; grad_norm must not be one of the plan's output
- * buffers. */
+ * tensors, however many they are, where the one-shot calls need a launch for
+ * every few dozen tensors (a norm of more than 128 tiles starts two; a tile is
+ * up to 8,192 elements of one tensor).  It can be captured into a HIP graph,
+ * which replays the config it was captured with.  A workspace serves one start
+ * at a time: starts of one plan follow each other on a stream or are ordered by
+ * events.  Same results as the one-shot calls (the norm's float64 sum is
+ * grouped differently beyond 160 tensors).  ar_adamw_start takes a plan of
+ * ar_adamw_init or ar_adamw_packed_init; grad_norm must not be one of the
+ * plan's output buffers. */
 typedef struct ar_update_s* ar_update_t;
 typedef enum {
     AR_UPDATE_GRAD_NORM = 0,

@@ -908,3 +908,19 @@ def test_stale_graphs_are_refused(ar, marshalling):
     ar.ar_adamw([p], [torch.ones(8, device="cuda")], [torch.zeros(8, device="cuda")],
                 [torch.zeros(8, device="cuda")], step=1, lr=0.5)
     assert (p == 0).all()
+
+
+@pytest.mark.parametrize("counts,launches", [([1] * 128, 1), ([1] * 129, 2), ([0, 8192] * 128, 1), ([0] * 200, 1),
+                                             ([8193] * 64, 1), ([8193] * 64 + [1], 2), ([1 << 20], 1),
+                                             ([(1 << 20) + 1], 2)])
+def test_norm_plan_launches(ar, counts, launches):
+    """One launch up to 128 tiles, of 8,192 elements and at least one a tensor that holds anything."""
+    torch = _torch()
+    rng = np.random.default_rng(len(counts))
+    gs = [on_device(rng.standard_normal(n).astype(np.float32), "f32") for n in counts]
+    plan = ar.ar_grad_norm_init(gs)
+    assert plan.num_launches == ar.ar_update_num_launches(plan) == launches
+    want = oracle.grad_norm([f64(g) for g in gs])
+    for _ in range(2):
+        assert abs(f64(plan.start())[0] - want) <= norm_bound(want)
+    torch.cuda.synchronize()
