@@ -104,12 +104,23 @@ def build_marshal(verbose: bool = False) -> str:
 
 
 def build_library(verbose: bool = False) -> str:
-    """Compile and link libar.so (and the probe and marshalling libraries beside it); return libar.so's path."""
+    """Compile and link libar.so (and the probe and marshalling libraries beside it); return libar.so's path.
+
+    The marshalling module only makes the binding's checks of tensors faster,
+    and needs torch's headers and g++, which libar.so does not: where it
+    cannot be built that is a warning, and one built before, perhaps for
+    another torch, is taken away.
+    """
     with ThreadPoolExecutor(2) as ex:
-        beside = [ex.submit(build_probe, verbose), ex.submit(build_marshal, verbose)]
+        probe, marshal = ex.submit(build_probe, verbose), ex.submit(build_marshal, verbose)
         path = _build_main(verbose)
-        for f in beside:
-            f.result()
+        probe.result()
+        try:
+            marshal.result()
+        except Exception as e:  # noqa: BLE001 - whatever is missing, the library stands
+            if os.path.exists(MARSHAL_PATH):
+                os.remove(MARSHAL_PATH)
+            print(f"warning: _armarshal.so was not built, tensors are checked in Python: {e}", file=sys.stderr)
     return path
 
 
