@@ -591,9 +591,11 @@ ar_result_t ar_adamw_packed(const ar_adamw_tensors_t* tensors, const ar_adamw_co
                             const float* grad_norm, hipStream_t stream);
 
 /* Values of packed states, for checkpoints and inspection: outs[t] receives
- * the counts[t] values that codes[t] and scales[t] stand for, in `dtype`
- * (float32 and, but for its subnormals, bfloat16 hold every value exactly;
- * binary16 rounds). */
+ * the counts[t] values that codes[t] and scales[t] stand for, in `dtype`.
+ * Every value that a step writes is one of float32's, and but for its
+ * subnormals one of bfloat16's; binary16 rounds.  (An exp_avg_sq code under a
+ * scale byte below 11 that no step writes can lie between float32's subnormals:
+ * it is rounded.) */
 typedef enum {
     AR_STATE_EXP_AVG = 0,
     AR_STATE_EXP_AVG_SQ = 1

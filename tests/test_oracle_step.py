@@ -155,3 +155,19 @@ def test_layer_norm_gradient_against_differences(affine):
         for c in range(cols):
             assert slope(gamma, c, name="gamma") == pytest.approx(dgamma[c], abs=1e-7)
             assert slope(beta, c, name="beta") == pytest.approx(dbeta[c], abs=1e-7)
+
+
+@pytest.mark.parametrize("kind", ["exp_avg", "exp_avg_sq"])
+@pytest.mark.parametrize("e", [1, 2, 5, 10, 11, 12, 30])
+def test_written_codes_are_exact_in_float32(kind, e):
+    """Down to float32's subnormals, whose spacing some codes undercut: a state that was rounded from a float32
+    value reads back exactly, and a positive second moment not as 0."""
+    rng = np.random.default_rng(e)
+    for seed in range(4):
+        x = (np.exp2(rng.uniform(-149, e - 127, 256))).astype(np.float32)
+        x[0], x[1], x[2] = 1.5 * 2.0 ** (e - 127), 2.0 ** -149, 3 * 2.0 ** -149
+        codes, scales = step.pack(x, step.random_bits(seed, 0, 256), kind)
+        got = step.unpack(codes, scales, kind)
+        assert scales.tolist() == [e]
+        assert np.array_equal(got.astype(np.float32).astype(np.float64), got)
+        assert (got > 0).all() or kind == "exp_avg"
