@@ -924,3 +924,43 @@ def test_norm_plan_launches(ar, counts, launches):
     for _ in range(2):
         assert abs(f64(plan.start())[0] - want) <= norm_bound(want)
     torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+def test_packed_large_form_agrees_with_the_small_one(ar, dtype):
+    """2^24 elements take two vectors a thread: each tensor's parameters, codes and scales, over its whole length,
+    are those of a smaller call that gives it the same number, and the oracle's in the second vector of a tile."""
+    torch = _torch()
+    odd = [70_001, 4096 + 2048 + 300, 4096 + 2047, 4096, 2049, 9]
+    torch.manual_seed(5)
+    rng = np.random.default_rng(5)
+    config = dict(HYPER, seed=8)
+    sets = []
+    for last in ((1 << 24) - sum(odd), 7):
+        sizes = odd + [last]
+        if not sets:
+            ps = [torch.randn(n, device="cuda").to(torch_dtype(dtype)) for n in sizes]
+            gs = [torch.randn(n, device="cuda").to(torch_dtype(dtype)) for n in sizes]
+            states = [packed_inputs(ar, rng, n, k % 5) for k, n in enumerate(odd)]
+            ms, vs = ([s[i][0] for s in states] + [ar.PackedState.zeros(last, "cuda")] for i in (0, 1))
+        sets.append(([p.clone()[:n] for p, n in zip(ps, sizes)], [g[:n] for g, n in zip(gs, sizes)],
+                     *([ar.PackedState(s.codes.clone()[:n], s.scales.clone()[:oracle.blocks_of(n)])
+                        for s, n in zip(x, sizes)] for x in (ms, vs))))
+    assert sum(t.numel() for t in sets[0][0]) == 1 << 24
+    for s in sets:
+        ar.ar_adamw_packed(*s, **config)
+    large, small = sets
+    for k, n in enumerate(odd):
+        assert torch.equal(large[0][k], small[0][k]), n
+        for i in (2, 3):
+            assert torch.equal(large[i][k].codes, small[i][k].codes), n
+            assert torch.equal(large[i][k].scales, small[i][k].scales), n
+        if n > 10_000:
+            continue
+        new = oracle.moments_f32(f32(gs[k]), states[k][0][1], states[k][1][1], HYPER["betas"], 1.0)
+        bits = oracle.random_bits(8, k, n)
+        for i, x, kind in ((2, new[0], "exp_avg"), (3, new[1], "exp_avg_sq")):
+            codes, scales = oracle.pack(x, bits, kind)
+            assert np.array_equal(large[i][k].scales.cpu().numpy(), scales), (n, kind)
+            assert np.array_equal(large[i][k].codes.cpu().numpy(), codes), (n, kind)
+        check_param(large[0][k], ps[k], gs[k], states[k][0][1], states[k][1][1], dtype)
