@@ -615,12 +615,16 @@ ar_result_t ar_unpack_states(const void* const* codes, const void* const* scales
  * tensors, however many they are, where the one-shot calls need a launch for
  * every few dozen tensors (a norm of more than 128 tiles starts two; a tile is
  * up to 8,192 elements of one tensor).  It can be captured into a HIP graph,
- * which replays the config it was captured with.  A workspace serves one start
- * at a time: starts of one plan follow each other on a stream or are ordered by
- * events.  Same results as the one-shot calls (the norm's float64 sum is
- * grouped differently beyond 160 tensors).  ar_adamw_start takes a plan of
- * ar_adamw_init or ar_adamw_packed_init; grad_norm must not be one of the
- * plan's output buffers. */
+ * which replays the config it was captured with: a replayed step keeps its step
+ * count, learning rate and seed, so a graph replayed step after step is not a
+ * training loop.  With packed states every replay gives an element the same
+ * random bits, and a state that they round back to its code goes back each
+ * time: enqueue (or capture) every step with values of its own.  A
+ * workspace serves one start at a time: starts of one plan follow each other on
+ * a stream or are ordered by events.  Same results as the one-shot calls (the
+ * norm's float64 sum is grouped differently beyond 160 tensors).
+ * ar_adamw_start takes a plan of ar_adamw_init or ar_adamw_packed_init;
+ * grad_norm must not be one of the plan's output buffers. */
 typedef struct ar_update_s* ar_update_t;
 typedef enum {
     AR_UPDATE_GRAD_NORM = 0,

@@ -340,7 +340,13 @@ class Update:
 
     def start(self, stream=None, **config):
         """Enqueue it.  A norm takes the stream only and returns its `norm` tensor; a step takes the
-        keyword arguments of :func:`ar_adamw` (or :func:`ar_adamw_packed`) after the tensors."""
+        keyword arguments of :func:`ar_adamw` (or :func:`ar_adamw_packed`) after the tensors.
+
+        Captured into a HIP graph, a step replays with the arguments it was
+        captured with: `step`, `lr` and, with packed states, the random bits
+        of `seed` stay the same at every replay, which a training loop must
+        not have.
+        """
         if self._handle is None:
             raise ValueError("update is closed")
         if self.kind == "grad_norm":
