@@ -7,8 +7,8 @@
 // workgroup leaves one partial sum per column; a second launch adds them in
 // the order of the workgroups, so that the result does not depend on which
 // one finishes first.  The activations' two reads and one write bound it: 8
-// ranks x 4,096 x 4,096 bf16 152.6 us (825 MB with the partial sums, 5.4 TB/s)
-// and 4.7 us for the second launch.  Without partial sums dx takes 142 us; more
+// ranks x 4,096 x 4,096 bf16 150-153 us (825 MB with the partial sums, 5.4-5.5
+// TB/s) and 4.8 us for the second launch.  Without partial sums dx takes 142 us; more
 // workgroups would bring it to 135 and cost more than that in partial sums.
 
 #include <hip/hip_runtime.h>

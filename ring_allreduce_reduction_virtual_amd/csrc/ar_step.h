@@ -40,8 +40,8 @@ static_assert(kPackedTile % AR_STATE_BLOCK == 0 && kUnpackTile % AR_STATE_BLOCK 
 // Packed states: two vectors from kPackedLargeElements when parameters and
 // gradients both have 16 bits; 32-bit ones fill a thread's loads with one.  us,
 // small / two vectors: bf16 2^22 elements 12.7 / 15.4, 2^23 18.9 / 19.5, 2^24
-// 37.2 / 35.5, 2^27 247 / 227; 2^26 float32 186 / 206, float32 with bf16
-// gradients and copies 187 / 206.
+// 37.2 / 35.5, 2^27 247 / 227; 2^26 float32 192 / 207, float32 with bf16
+// gradients 179 / 177, with copies too 192 / 203.
 constexpr uint64_t kAdamwLargeBytes = 128ull << 20;
 constexpr uint64_t kPackedLargeElements = 1ull << 24;
 constexpr int adamw_vectors(bool large, bool all_f32) { return large ? (all_f32 ? 4 : 2) : 1; }

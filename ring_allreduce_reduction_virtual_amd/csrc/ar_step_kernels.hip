@@ -291,7 +291,7 @@ __device__ __forceinline__ void packed_update(const AdamwScalars& s, float corre
 // the block's largest magnitude is a maximum over 32 lanes, with no LDS.  About
 // 60 instructions an element, of which a quarter is the hash, against 10 bytes
 // (bf16): both HBM and the vector units are near their limit.  2^27 bf16
-// elements 227-235 us, 5.8 TB/s; with the codes taken apart by multiplications
+// elements 224-235 us, 5.8 TB/s; with the codes taken apart by multiplications
 // and the quotient rounded correctly, 100 instructions, it took 304.
 template <int PD, int GD, bool LARGE, bool EXACT, bool FULL>
 __device__ __forceinline__ void packed_tile(const PackedEntry& e, const AdamwScalars& s, uint64_t at, uint64_t n) {
