@@ -686,6 +686,82 @@ ar_result_t ar_layer_norm_backward(const void* const* dy, const void* const* x, 
 /* (size_t)-1 for invalid arguments. */
 size_t ar_layer_norm_workspace_bytes(size_t rows, size_t cols, int nranks);
 
+/* ------------------------------------------------------------------------
+ * The model's ends, and the activations kept between forward and backward
+ *
+ * What a language model's step has besides: the embedding of its tokens with
+ * the table's gradient, the loss of its logits against targets with the
+ * gradients of both factors, and activations kept in 8 bits for the backward
+ * pass.  As for layer norm, rank r owns the r-th entry of every array, its
+ * tokens, its activations and its replica of each weight, and the weights'
+ * gradients are the rank's part, for the AllReduce to sum over the ranks.
+ * ------------------------------------------------------------------------ */
+
+/* Type of tokens and targets. */
+typedef enum {
+    AR_INDEX_INT32 = 0,
+    AR_INDEX_INT64 = 1
+} ar_index_t;
+
+/* Embedding lookup: row i of out[r] (`rows` rows of `cols` elements of dtype,
+ * out_stride elements apart) receives scale * row tokens[r][i] of table[r]
+ * (`vocab` rows of `cols` elements of table_dtype, which is dtype or
+ * AR_FLOAT32, table_stride apart): a float32 product, rounded to dtype (to
+ * binary16 in the same step).  A token outside [0, vocab) reads nothing; its row becomes NaN.  Outputs
+ * overlap nothing else; several ranks may read one table.  scale is any number
+ * in float32's range but one that it rounds to 0.  rows == 0 or cols == 0 is a
+ * successful no-op. */
+ar_result_t ar_embedding(const void* const* tokens, const void* const* table, void* const* out, size_t rows,
+                         size_t vocab, size_t cols, size_t table_stride, size_t out_stride, ar_index_t index_type,
+                         ar_dtype_t dtype, ar_dtype_t table_dtype, double scale, int nranks, hipStream_t stream);
+
+/* Its gradient: row v of dtable[r] (table_dtype, dtable_stride apart) receives
+ * scale * the sum of the rows of dy[r] whose token is v, added in float32 in an
+ * order that depends on the tokens alone (they are sorted by token, then by
+ * place), and rounded once.  Rows that no token names become 0.  With
+ * `accumulate` the sum is added to what the row holds (before the rounding),
+ * and rows that no token names are not touched: a table that is also the
+ * head's weight gets both gradients in one buffer.  Tokens outside [0, vocab)
+ * and those equal to padding_index (negative: none) take no part.
+ * `workspace`: at least ar_embedding_workspace_bytes(...) bytes of device
+ * memory, 4-byte aligned (the sorted tokens and partial sums).  rows < 2^31. */
+ar_result_t ar_embedding_backward(const void* const* dy, const void* const* tokens, void* const* dtable, size_t rows,
+                                  size_t vocab, size_t cols, size_t dy_stride, size_t dtable_stride,
+                                  ar_index_t index_type, ar_dtype_t dtype, ar_dtype_t table_dtype, double scale,
+                                  long long padding_index, int accumulate, int nranks, void* workspace,
+                                  size_t workspace_bytes, hipStream_t stream);
+/* (size_t)-1 for invalid arguments. */
+size_t ar_embedding_workspace_bytes(size_t rows, size_t vocab, size_t cols, int nranks);
+
+/* Activations in 8 bits.  A block is AR_ACTIVATION_BLOCK consecutive elements
+ * of a row (the row's last one may be short).  It has a scale byte e, worth
+ * 2^(e-133): the smallest e >= 1 whose 127 * 2^(e-133) reaches the block's
+ * largest magnitude.  An element's code is a signed byte, the element divided
+ * by the scale and rounded to the nearest integer, ties to even, so that a
+ * value moves by at most half a scale: 1/127 of the block's largest magnitude.
+ * e = 255 makes the whole block NaN (its codes are 0): a block that holds a
+ * NaN, an infinity or a magnitude above 127 * 2^121 gets it.  codes[r] is
+ * rows x cols bytes, scales[r] rows x ceil(cols / AR_ACTIVATION_BLOCK) bytes,
+ * both without gaps.  float32 and bfloat16 hold every code's value exactly;
+ * unpacking to binary16 rounds once where it has to.  e = 0, as in zeroed
+ * memory, means 1. */
+#define AR_ACTIVATION_BLOCK 32
+ar_result_t ar_pack_activations(const void* const* x, void* const* codes, void* const* scales, size_t rows,
+                                size_t cols, size_t x_stride, ar_dtype_t dtype, int nranks, hipStream_t stream);
+ar_result_t ar_unpack_activations(const void* const* codes, const void* const* scales, void* const* x, size_t rows,
+                                  size_t cols, size_t x_stride, ar_dtype_t dtype, int nranks, hipStream_t stream);
+
+/* ar_layer_norm_backward with the forward pass's input kept in 8 bits: the
+ * same formulas, x being the values that codes and scales stand for, mean and
+ * rstd those of the forward pass on the input as it was.  dtype is that of dy
+ * and dx.  The same workspace, rules and errors. */
+ar_result_t ar_layer_norm_backward_packed(const void* const* dy, const void* const* codes, const void* const* scales,
+                                          const void* const* gamma, const float* const* mean,
+                                          const float* const* rstd, void* const* dx, void* const* dgamma,
+                                          void* const* dbeta, size_t rows, size_t cols, size_t dy_stride,
+                                          size_t dx_stride, ar_dtype_t dtype, ar_dtype_t weight_dtype, int nranks,
+                                          void* workspace, size_t workspace_bytes, hipStream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -30,6 +30,15 @@ from .binding import (  # noqa: F401
     ar_reduce_scatter_noalloc,
     ar_workspace_bytes,
 )
+from .model import (  # noqa: F401
+    PackedRows,
+    ar_embedding,
+    ar_embedding_backward,
+    ar_embedding_workspace_bytes,
+    ar_layer_norm_backward_packed,
+    ar_pack_activations,
+    ar_unpack_activations,
+)
 from .step import (  # noqa: F401
     PackedState,
     Update,
@@ -61,4 +70,6 @@ __all__ = [
     "ar_adamw", "ar_adamw_init", "ar_adamw_packed", "ar_adamw_packed_init", "ar_adamw_start", "ar_unpack_states",
     "ar_update_workspace_bytes", "ar_update_num_launches", "ar_update_free",
     "ar_layer_norm", "ar_layer_norm_backward", "ar_layer_norm_workspace_bytes",
+    "ar_embedding", "ar_embedding_backward", "ar_embedding_workspace_bytes",
+    "PackedRows", "ar_pack_activations", "ar_unpack_activations", "ar_layer_norm_backward_packed",
 ]

@@ -39,11 +39,16 @@ EXPORTS = (
     "ar_adamw", "ar_adamw_init", "ar_adamw_packed", "ar_adamw_packed_init", "ar_adamw_start",
     "ar_unpack_states", "ar_update_workspace_bytes", "ar_update_num_launches", "ar_update_free",
     "ar_layer_norm", "ar_layer_norm_backward", "ar_layer_norm_workspace_bytes",
+    "ar_embedding", "ar_embedding_backward", "ar_embedding_workspace_bytes",
+    "ar_pack_activations", "ar_unpack_activations", "ar_layer_norm_backward_packed",
 )
 # the training-step operators' enums and constants
 STATES = {"exp_avg": 0, "exp_avg_sq": 1}
 UPDATES = {"grad_norm": 0, "adamw": 1, "adamw_packed": 2}
 STATE_BLOCK = 256
+# the model's ends: types of tokens and targets, elements of a packed activations' block
+INDICES = {"i32": 0, "i64": 1}
+ACTIVATION_BLOCK = 32
 # bytes of the fixed device array behind ar_reduce_scatter_noalloc
 NOALLOC_SCRATCH_BYTES = 64 << 20
 
@@ -117,6 +122,13 @@ def _declare(lib):
                                  ctypes.c_double, _int, _vp]),
         "ar_layer_norm_backward": (_int, [_vpp] * 8 + [_sz] * 5 + [_int, _int, _int, _vp, _sz, _vp]),
         "ar_layer_norm_workspace_bytes": (_sz, [_sz, _sz, _int]),
+        "ar_embedding": (_int, [_vpp] * 3 + [_sz] * 5 + [_int] * 3 + [ctypes.c_double, _int, _vp]),
+        "ar_embedding_backward": (_int, [_vpp] * 3 + [_sz] * 5 + [_int] * 3
+                                  + [ctypes.c_double, ctypes.c_longlong, _int, _int, _vp, _sz, _vp]),
+        "ar_embedding_workspace_bytes": (_sz, [_sz, _sz, _sz, _int]),
+        "ar_pack_activations": (_int, [_vpp] * 3 + [_sz] * 3 + [_int, _int, _vp]),
+        "ar_unpack_activations": (_int, [_vpp] * 3 + [_sz] * 3 + [_int, _int, _vp]),
+        "ar_layer_norm_backward_packed": (_int, [_vpp] * 9 + [_sz] * 4 + [_int, _int, _int, _vp, _sz, _vp]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)

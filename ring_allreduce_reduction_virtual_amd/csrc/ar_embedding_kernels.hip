@@ -1,0 +1,551 @@
+// HIP kernels of the embedding lookup and of its gradient (include/ar.h states
+// the formulas).
+//
+// The lookup copies rows: the table's rows that tokens name are read, each row
+// of the output is written once.
+//
+// The gradient is a sum by token whose order must not depend on which
+// workgroup comes first, so no row is added to with atomics.  The places are
+// sorted by token, stably; the sorted order is cut into chunks of kSumChunk
+// places, and a group of threads adds up each chunk's rows of dy.  A token
+// whose places lie within one chunk is done there.  One that crosses a chunk's
+// end leaves a partial sum in each chunk, and a second launch adds these in
+// order: a frequent token is spread over as many groups as it has chunks, and
+// no token makes one group longer than another.  The launch that sums also
+// writes the zeros of rows that no token names.
+
+#include <hip/hip_runtime.h>
+
+#include "ar_embedding.h"
+#include "ar_step_device.h"
+
+namespace arimpl {
+namespace {
+
+__device__ __forceinline__ int64_t token_at(const char* tokens, uint64_t i, int wide) {
+    return wide ? reinterpret_cast<const int64_t*>(tokens)[i] : reinterpret_cast<const int32_t*>(tokens)[i];
+}
+
+// Threads of a row: rows of up to 64 vectors of V elements have several to a wavefront.
+template <int TPR>
+constexpr int kRowsAtOnce = 256 / TPR;
+
+template <int DT, int TDT, int TPR>
+__global__ void __launch_bounds__(256) k_embedding(EmbeddingArgs a) {
+    constexpr int V = 16 / elem_size<DT>();
+    const int rank = blockIdx.y;
+    const uint64_t step = static_cast<uint64_t>(gridDim.x) * kRowsAtOnce<TPR>;
+    for (uint64_t row = static_cast<uint64_t>(blockIdx.x) * kRowsAtOnce<TPR> + threadIdx.x / TPR; row < a.rows;
+         row += step) {
+        const int64_t t = token_at(a.tokens[rank], row, a.wide_index);
+        const bool known = t >= 0 && static_cast<uint64_t>(t) < a.vocab;
+        const char* const from = a.table[rank] + (known ? static_cast<uint64_t>(t) : 0) * a.table_stride * elem_size<TDT>();
+        char* const to = a.out[rank] + row * a.out_stride * elem_size<DT>();
+        for (uint64_t c = (threadIdx.x % TPR) * V; c < a.cols; c += TPR * V) {
+            Raw<TDT, V> r;
+            if (known) load_at<false, false>(r, from, c, a.cols);
+            float x[V];
+#pragma unroll
+            for (int j = 0; j < V; ++j) x[j] = known ? r.get(j) * a.scale : as_f(0x7fc00000u);
+            Raw<DT, V> o;
+            o.set_all(x);
+            store_at<false, true>(o, to, c, a.cols);
+        }
+    }
+}
+
+// ---------------------------------------------------------------------------
+// the sort
+// ---------------------------------------------------------------------------
+
+// A place's key: its token, or vocab (behind all tokens) when it takes no part.
+__device__ __forceinline__ uint32_t key_at(const EmbeddingBackwardArgs& a, int rank, uint64_t i) {
+    const int64_t t = token_at(a.tokens[rank], i, a.wide_index);
+    const bool part = t >= 0 && static_cast<uint64_t>(t) < a.vocab && t != a.padding;
+    return static_cast<uint32_t>(part ? static_cast<uint64_t>(t) : a.vocab);
+}
+
+// The lanes of the wavefront whose digit is this lane's.
+__device__ __forceinline__ uint64_t same_digit(uint32_t digit, int bits) {
+    uint64_t same = ~0ull;
+    for (int b = 0; b < bits; ++b) {
+        const bool set = (digit >> b) & 1u;
+        const uint64_t with = __ballot(set);
+        same &= set ? with : ~with;
+    }
+    return same;
+}
+
+// How many places of the wavefront's so far have this digit, this lane's among
+// the lanes below it; `count` is the wavefront's own row of counters.
+__device__ __forceinline__ uint32_t take_rank(uint32_t* count, uint32_t digit, int bits) {
+    const uint64_t same = same_digit(digit, bits);
+    const uint32_t below = __popcll(same & ((1ull << (threadIdx.x & 63)) - 1));
+    const uint32_t before = count[digit];
+    // every lane has read before the first lane of each digit writes
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    if (below == 0) count[digit] = before + __popcll(same);
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    return before + below;
+}
+
+// Sum of the wavefront's values up to and with this lane's.
+__device__ __forceinline__ uint32_t sum_to_lane(uint32_t x) {
+    const int lane = threadIdx.x & 63;
+#pragma unroll
+    for (int d = 1; d < 64; d *= 2) {
+        const uint32_t y = __shfl_up(x, d, 64);
+        if (lane >= d) x += y;
+    }
+    return x;
+}
+
+// Turns the wavefronts' counters into what precedes each wavefront's places of
+// a digit, and `digits` into what precedes the digit.  Called by all threads of
+// the workgroup, with at least kDigits of them or a loop over the rest.
+template <int THREADS>
+__device__ __forceinline__ void scan_counts(uint32_t (*count)[kDigits], uint32_t* digits, uint32_t* totals) {
+    constexpr int kWaves = THREADS / 64;
+    uint32_t carry = 0;
+    for (int d0 = 0; d0 < kDigits; d0 += THREADS) {
+        const int d = d0 + static_cast<int>(threadIdx.x);
+        uint32_t sum = 0;
+        if (d < kDigits) {
+#pragma unroll
+            for (int w = 0; w < kWaves; ++w) {
+                const uint32_t c = count[w][d];
+                count[w][d] = sum;
+                sum += c;
+            }
+        }
+        const uint32_t to = sum_to_lane(sum);
+        if ((threadIdx.x & 63) == 63) totals[threadIdx.x >> 6] = to;
+        __syncthreads();
+        uint32_t before = carry;
+        for (int w = 0; w < kWaves; ++w) {
+            if (w < static_cast<int>(threadIdx.x >> 6)) before += totals[w];
+            carry += totals[w];
+        }
+        if (d < kDigits) digits[d] = before + to - sum;
+        __syncthreads();
+    }
+}
+
+// One rank's places in one workgroup, up to kSortOne of them, all passes.
+__global__ void __launch_bounds__(kSortThreads) k_sort_one(EmbeddingBackwardArgs a) {
+    constexpr int kWaves = kSortThreads / 64;
+    __shared__ uint32_t count[kWaves][kDigits];
+    __shared__ uint32_t digits[kDigits], totals[kWaves];
+    __shared__ uint32_t keys[kSortOne];
+    __shared__ uint16_t places[kSortOne];
+    static_assert(kSortOne <= 65536, "places of 16 bits");
+    const int rank = blockIdx.x, wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+    const uint32_t n = static_cast<uint32_t>(a.rows);
+    uint32_t key[kSortEach], place[kSortEach], at[kSortEach];
+#pragma unroll
+    for (int i = 0; i < kSortEach; ++i) {
+        place[i] = (wave * kSortEach + i) * 64 + lane;
+        key[i] = place[i] < n ? key_at(a, rank, place[i]) : 0xffffffffu;   // stays behind all others
+    }
+    const uint32_t mask = (1u << a.digit_bits) - 1;
+    for (int pass = 0; pass < a.passes; ++pass) {
+        const int shift = pass * a.digit_bits;
+        for (int d = threadIdx.x; d < kWaves * kDigits; d += kSortThreads) (&count[0][0])[d] = 0;
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < kSortEach; ++i) at[i] = take_rank(count[wave], (key[i] >> shift) & mask, a.digit_bits);
+        __syncthreads();
+        scan_counts<kSortThreads>(count, digits, totals);
+#pragma unroll
+        for (int i = 0; i < kSortEach; ++i) {
+            const uint32_t d = (key[i] >> shift) & mask;
+            const uint32_t to = digits[d] + count[wave][d] + at[i];
+            keys[to] = key[i];
+            places[to] = static_cast<uint16_t>(place[i]);
+        }
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < kSortEach; ++i) {
+            const uint32_t from = (wave * kSortEach + i) * 64 + lane;
+            key[i] = keys[from];
+            place[i] = places[from];
+        }
+        __syncthreads();
+    }
+    uint32_t* const keys_to = a.keys + rank * sort_words(a.rows);
+    uint32_t* const places_to = a.places + rank * sort_words(a.rows);
+#pragma unroll
+    for (int i = 0; i < kSortEach; ++i) {
+        const uint32_t to = (wave * kSortEach + i) * 64 + lane;
+        if (to < n) {
+            keys_to[to] = key[i];
+            places_to[to] = place[i];
+        }
+    }
+}
+
+// The key of a pass's i-th place: from the tokens, or from the pass before.
+__device__ __forceinline__ uint32_t pass_key(const EmbeddingBackwardArgs& a, int rank, int pass, uint64_t i) {
+    if (pass == 0) return key_at(a, rank, i);
+    return a.keys[rank * sort_words(a.rows) + ((pass - 1) & 1) * a.rows + i];
+}
+
+__global__ void __launch_bounds__(kSortTileThreads) k_sort_count(EmbeddingBackwardArgs a, int pass) {
+    __shared__ uint32_t count[kDigits];
+    const int rank = blockIdx.y;
+    const uint64_t tile = blockIdx.x;
+    for (int d = threadIdx.x; d < kDigits; d += kSortTileThreads) count[d] = 0;
+    __syncthreads();
+    const uint32_t mask = (1u << a.digit_bits) - 1;
+#pragma unroll
+    for (int i = 0; i < kSortTileEach; ++i) {
+        const uint64_t at = tile * kSortTile + i * kSortTileThreads + threadIdx.x;
+        if (at < a.rows) atomicAdd(&count[(pass_key(a, rank, pass, at) >> (pass * a.digit_bits)) & mask], 1u);
+    }
+    __syncthreads();
+    uint32_t* const to = a.counts + rank * a.tiles * kDigits + tile;
+    for (int d = threadIdx.x; d < kDigits; d += kSortTileThreads) to[d * a.tiles] = count[d];
+}
+
+// Each count becomes the sum of those before it, digit by digit and tile by tile.
+__global__ void __launch_bounds__(1024) k_sort_scan(EmbeddingBackwardArgs a) {
+    __shared__ uint32_t totals[2][16];
+    uint32_t* const count = a.counts + blockIdx.x * a.tiles * kDigits;
+    const uint64_t n = a.tiles * kDigits;
+    uint32_t carry = 0;
+    int turn = 0;
+    for (uint64_t first = 0; first < n; first += 4096) {
+        uint32_t x[4], sum = 0;
+        const uint64_t at = first + threadIdx.x * 4;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            x[k] = at + k < n ? count[at + k] : 0;
+            sum += x[k];
+        }
+        const uint32_t to = sum_to_lane(sum);
+        if ((threadIdx.x & 63) == 63) totals[turn][threadIdx.x >> 6] = to;
+        __syncthreads();
+        uint32_t before = carry + to - sum;
+        for (int w = 0; w < 16; ++w) {
+            if (w < static_cast<int>(threadIdx.x >> 6)) before += totals[turn][w];
+            carry += totals[turn][w];
+        }
+        turn ^= 1;   // the next turn's totals go elsewhere: one barrier a turn
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            if (at + k < n) count[at + k] = before;
+            before += x[k];
+        }
+    }
+}
+
+__global__ void __launch_bounds__(kSortTileThreads) k_sort_place(EmbeddingBackwardArgs a, int pass) {
+    constexpr int kWaves = kSortTileThreads / 64;
+    __shared__ uint32_t count[kWaves][kDigits];
+    const int rank = blockIdx.y, wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+    const uint64_t tile = blockIdx.x;
+    uint32_t key[kSortTileEach], at[kSortTileEach];
+    for (int d = threadIdx.x; d < kWaves * kDigits; d += kSortTileThreads) (&count[0][0])[d] = 0;
+    __syncthreads();
+    const uint32_t mask = (1u << a.digit_bits) - 1;
+    const int shift = pass * a.digit_bits;
+    const uint64_t first = tile * kSortTile + wave * kSortTileEach * 64 + lane;
+#pragma unroll
+    for (int i = 0; i < kSortTileEach; ++i)
+        key[i] = first + i * 64 < a.rows ? pass_key(a, rank, pass, first + i * 64) : 0xffffffffu;
+#pragma unroll
+    for (int i = 0; i < kSortTileEach; ++i) {
+        // past the last place: of the last digit, behind all others of the last tile
+        at[i] = take_rank(count[wave], (key[i] >> shift) & mask, a.digit_bits);
+    }
+    __syncthreads();
+    const uint32_t* const starts = a.counts + rank * a.tiles * kDigits + tile;
+    for (int d = threadIdx.x; d < kDigits; d += kSortTileThreads) {
+        uint32_t sum = starts[d * a.tiles];
+#pragma unroll
+        for (int w = 0; w < kWaves; ++w) {
+            const uint32_t c = count[w][d];
+            count[w][d] = sum;
+            sum += c;
+        }
+    }
+    __syncthreads();
+    const uint64_t part = rank * sort_words(a.rows);
+    const uint32_t* const places_from = a.places + part + ((pass + 1) & 1) * a.rows;
+    uint32_t* const keys_to = a.keys + part + (pass & 1) * a.rows;
+    uint32_t* const places_to = a.places + part + (pass & 1) * a.rows;
+#pragma unroll
+    for (int i = 0; i < kSortTileEach; ++i) {
+        const uint64_t from = first + i * 64;
+        if (from < a.rows) {
+            const uint32_t to = count[wave][(key[i] >> shift) & mask] + at[i];
+            keys_to[to] = key[i];
+            places_to[to] = pass == 0 ? static_cast<uint32_t>(from) : places_from[from];
+        }
+    }
+}
+
+// ---------------------------------------------------------------------------
+// the sums
+// ---------------------------------------------------------------------------
+
+// First place of the sorted keys that is not below v.
+__device__ __forceinline__ uint64_t lower_bound(const uint32_t* keys, uint64_t n, uint32_t v) {
+    uint64_t lo = 0;
+    while (n > 0) {
+        const uint64_t half = n / 2;
+        const bool below = keys[lo + half] < v;
+        lo = below ? lo + half + 1 : lo;
+        n = below ? n - half - 1 : half;
+    }
+    return lo;
+}
+
+template <int DT, int V>
+__device__ __forceinline__ void write_row(const EmbeddingBackwardArgs& a, int rank, uint32_t token, uint64_t c,
+                                          const float (&sum)[V]) {
+    char* const to = a.dtable[rank] + token * a.dtable_stride * elem_size<DT>();
+    float x[V];
+#pragma unroll
+    for (int j = 0; j < V; ++j) x[j] = sum[j] * a.scale;
+    Raw<DT, V> r;
+    if (a.accumulate) {
+        load_at<false, false>(r, to, c, a.cols);
+#pragma unroll
+        for (int j = 0; j < V; ++j) x[j] += r.get(j);
+    }
+    r.set_all(x);
+    store_at<false, true>(r, to, c, a.cols);
+}
+
+__device__ __forceinline__ float* partial_at(const EmbeddingBackwardArgs& a, int rank, uint64_t chunk, int which) {
+    return a.partials + ((rank * a.chunks + chunk) * 2 + which) * a.cols;
+}
+
+constexpr uint64_t kZeroRows = 64;   // rows of the table that a workgroup looks at
+
+// blockIdx.x below sum_blocks: chunks, one for each group of TPR threads;
+// above: rows of the table without a token.  blockIdx.y: stretches of TPR * V
+// columns.
+template <int DT, int TDT, int TPR>
+__global__ void __launch_bounds__(256) k_embedding_sums(EmbeddingBackwardArgs a, uint32_t sum_blocks,
+                                                        uint32_t zero_blocks) {
+    constexpr int V = 8;
+    constexpr int kAhead = 8;   // rows on their way
+    const int rank = blockIdx.z;
+    const uint32_t* const keys = a.keys + rank * sort_words(a.rows) + a.sorted * a.rows;
+    const uint32_t* const places = a.places + rank * sort_words(a.rows) + a.sorted * a.rows;
+    const uint32_t vocab = static_cast<uint32_t>(a.vocab);
+    if (blockIdx.x >= sum_blocks) {
+        const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+        const uint64_t c_end = std::min<uint64_t>(a.cols, (blockIdx.y + 1ull) * TPR * V);
+        Raw<TDT, V> zero = {};
+        for (uint64_t first = (blockIdx.x - sum_blocks) * kZeroRows + wave * 16; first < a.vocab;
+             first += zero_blocks * kZeroRows) {
+            bool empty = false;
+            if (lane < 16 && first + lane < a.vocab) {
+                const uint32_t v = static_cast<uint32_t>(first + lane);
+                const uint64_t at = lower_bound(keys, a.rows, v);
+                empty = at >= a.rows || keys[at] != v;
+            }
+            for (uint64_t rows = __ballot(empty); rows != 0; rows &= rows - 1) {
+                char* const to = a.dtable[rank] + (first + __builtin_ctzll(rows)) * a.dtable_stride * elem_size<TDT>();
+                for (uint64_t c = blockIdx.y * static_cast<uint64_t>(TPR) * V + lane * V; c < c_end; c += 64 * V)
+                    store_at<false, true>(zero, to, c, a.cols);
+            }
+        }
+        return;
+    }
+    const uint64_t c = (blockIdx.y * static_cast<uint64_t>(TPR) + threadIdx.x % TPR) * V;
+    if (c >= a.cols) return;
+    uint32_t group = threadIdx.x / TPR;
+    if constexpr (TPR >= 64) group = __builtin_amdgcn_readfirstlane(group);
+    const uint64_t step = static_cast<uint64_t>(sum_blocks) * kRowsAtOnce<TPR>;
+    for (uint64_t chunk = static_cast<uint64_t>(blockIdx.x) * kRowsAtOnce<TPR> + group; chunk < a.chunks; chunk += step) {
+        const uint64_t first = chunk * kSumChunk;
+        const uint64_t end = std::min(a.rows, first + kSumChunk);
+        float sum[V];
+#pragma unroll
+        for (int j = 0; j < V; ++j) sum[j] = 0;
+        uint32_t token = keys[first];
+        bool begins = first == 0 || keys[first - 1] != token;   // in this chunk
+        const auto leave = [&](bool ends) {
+            if (token >= vocab) return;
+            if (begins && ends) {
+                write_row<TDT>(a, rank, token, c, sum);
+            } else {
+                float* const to = partial_at(a, rank, chunk, begins ? 1 : 0);
+#pragma unroll
+                for (int j = 0; j < V; ++j) {
+                    if (c + j < a.cols) to[c + j] = sum[j];
+                }
+            }
+        };
+        for (uint64_t at = first; at < end; at += kAhead) {
+            uint32_t key[kAhead];
+            Raw<DT, V> r[kAhead];
+#pragma unroll
+            for (int k = 0; k < kAhead; ++k) {
+                key[k] = at + k < end ? keys[at + k] : 0xffffffffu;
+                if (key[k] < vocab)
+                    load_at<false, true>(r[k], a.dy[rank] + places[at + k] * a.dy_stride * elem_size<DT>(), c, a.cols);
+            }
+#pragma unroll
+            for (int k = 0; k < kAhead; ++k) {
+                if (at + k >= end) break;
+                if (key[k] != token) {
+                    leave(true);
+                    token = key[k];
+                    begins = true;
+#pragma unroll
+                    for (int j = 0; j < V; ++j) sum[j] = 0;
+                }
+                if (token < vocab) {
+#pragma unroll
+                    for (int j = 0; j < V; ++j) sum[j] += r[k].get(j);
+                }
+            }
+        }
+        leave(end == a.rows || keys[end] != token);
+    }
+}
+
+// The tokens that cross the end of a chunk: from the chunk where one begins, the
+// partial sums up to the one where it ends.  A wavefront takes 64 columns, and
+// one chunk after another of those that its workgroup looks at.
+constexpr uint64_t kJoinChunks = 16;
+
+template <int TDT>
+__global__ void __launch_bounds__(256) k_embedding_join(EmbeddingBackwardArgs a) {
+    const int rank = blockIdx.z;
+    const uint32_t* const keys = a.keys + rank * sort_words(a.rows) + a.sorted * a.rows;
+    const uint64_t c = blockIdx.y * 64ull + (threadIdx.x & 63);
+    if (c >= a.cols) return;
+    const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    for (uint64_t k = wave; k < kJoinChunks; k += 4) {
+        const uint64_t chunk = blockIdx.x * kJoinChunks + k;
+        const uint64_t first = chunk * kSumChunk, end = first + kSumChunk;
+        if (end >= a.rows) return;
+        const uint32_t token = keys[end - 1];
+        if (token >= a.vocab || keys[end] != token || (first > 0 && keys[first - 1] == token)) continue;
+        const uint64_t last = (lower_bound(keys, a.rows, token + 1) - 1) / kSumChunk;
+        float sum = partial_at(a, rank, chunk, 1)[c];
+#pragma unroll 8
+        for (uint64_t j = chunk + 1; j <= last; ++j) sum += partial_at(a, rank, j, 0)[c];
+        char* const to = a.dtable[rank] + (token * a.dtable_stride + c) * elem_size<TDT>();
+        float x = sum * a.scale;
+        if (a.accumulate) x += widen<TDT>(load_elem<elem_size<TDT>()>(to));
+        store_elem<elem_size<TDT>(), false>(to, narrow<TDT>(x));
+    }
+}
+
+// Vectors of a row to threads of a row: all of one wavefront's or workgroup's
+// threads work on rows as short as 8 vectors.
+int row_threads(uint64_t cols, int vector) {
+    const uint64_t need = (cols + vector - 1) / vector;
+    return need <= 8 ? 8 : need <= 16 ? 16 : need <= 32 ? 32 : need <= 64 ? 64 : 256;
+}
+
+constexpr uint64_t kMostBlocks = 1u << 16;
+
+template <int DT, int TDT, int TPR>
+hipError_t start_embedding(const EmbeddingArgs& a, int nranks, hipStream_t s) {
+    const uint64_t need = (a.rows + kRowsAtOnce<TPR> - 1) / kRowsAtOnce<TPR>;
+    const dim3 grid(static_cast<unsigned>(std::min(need, kMostBlocks)), nranks);
+    hipLaunchKernelGGL((k_embedding<DT, TDT, TPR>), grid, dim3(256), 0, s, a);
+    return hipGetLastError();
+}
+
+template <int DT, int TDT>
+hipError_t embedding_by_width(const EmbeddingArgs& a, int nranks, hipStream_t s) {
+    switch (row_threads(a.cols, 16 / elem_size<DT>())) {
+        case 8: return start_embedding<DT, TDT, 8>(a, nranks, s);
+        case 16: return start_embedding<DT, TDT, 16>(a, nranks, s);
+        case 32: return start_embedding<DT, TDT, 32>(a, nranks, s);
+        case 64: return start_embedding<DT, TDT, 64>(a, nranks, s);
+        default: return start_embedding<DT, TDT, 256>(a, nranks, s);
+    }
+}
+
+hipError_t start_sort(const EmbeddingBackwardArgs& a, int nranks, hipStream_t s) {
+    if (a.rows <= kSortOne) {
+        hipLaunchKernelGGL(k_sort_one, dim3(nranks), dim3(kSortThreads), 0, s, a);
+        return hipGetLastError();
+    }
+    const dim3 tiles(static_cast<unsigned>(a.tiles), nranks);
+    for (int pass = 0; pass < a.passes; ++pass) {
+        hipLaunchKernelGGL(k_sort_count, tiles, dim3(kSortTileThreads), 0, s, a, pass);
+        hipLaunchKernelGGL(k_sort_scan, dim3(nranks), dim3(1024), 0, s, a);
+        hipLaunchKernelGGL(k_sort_place, tiles, dim3(kSortTileThreads), 0, s, a, pass);
+        const hipError_t e = hipGetLastError();
+        if (e != hipSuccess) return e;
+    }
+    return hipSuccess;
+}
+
+template <int DT, int TDT, int TPR>
+hipError_t start_sums(const EmbeddingBackwardArgs& a, int nranks, hipStream_t s) {
+    const uint64_t sums = (a.chunks + kRowsAtOnce<TPR> - 1) / kRowsAtOnce<TPR>;
+    const uint64_t zeros = a.accumulate ? 0 : (a.vocab + kZeroRows - 1) / kZeroRows;
+    const uint32_t sum_blocks = static_cast<uint32_t>(std::min(sums, kMostBlocks));
+    const uint32_t zero_blocks = static_cast<uint32_t>(std::min(zeros, kMostBlocks));
+    if (sum_blocks + zero_blocks == 0) return hipSuccess;
+    const dim3 grid(sum_blocks + zero_blocks, static_cast<unsigned>((a.cols + TPR * 8 - 1) / (TPR * 8)), nranks);
+    hipLaunchKernelGGL((k_embedding_sums<DT, TDT, TPR>), grid, dim3(256), 0, s, a, sum_blocks, zero_blocks);
+    hipError_t e = hipGetLastError();
+    if (e != hipSuccess || a.chunks < 2) return e;
+    const dim3 joins(static_cast<unsigned>((a.chunks + kJoinChunks - 1) / kJoinChunks),
+                     static_cast<unsigned>((a.cols + 63) / 64), nranks);
+    hipLaunchKernelGGL((k_embedding_join<TDT>), joins, dim3(256), 0, s, a);
+    return hipGetLastError();
+}
+
+template <int DT, int TDT>
+hipError_t backward_by_width(const EmbeddingBackwardArgs& a, int nranks, hipStream_t s) {
+    if (a.rows > 0) {
+        const hipError_t e = start_sort(a, nranks, s);
+        if (e != hipSuccess) return e;
+    }
+    switch (row_threads(a.cols, 8)) {
+        case 8: return start_sums<DT, TDT, 8>(a, nranks, s);
+        case 16: return start_sums<DT, TDT, 16>(a, nranks, s);
+        case 32: return start_sums<DT, TDT, 32>(a, nranks, s);
+        case 64: return start_sums<DT, TDT, 64>(a, nranks, s);
+        default: return start_sums<DT, TDT, 256>(a, nranks, s);
+    }
+}
+
+}  // namespace
+
+hipError_t launch_embedding(const EmbeddingArgs& a, int nranks, ar_dtype_t dtype, ar_dtype_t table, hipStream_t s) {
+    const bool wide = table == AR_FLOAT32;
+    switch (dtype) {
+        case AR_FLOAT32: return embedding_by_width<AR_FLOAT32, AR_FLOAT32>(a, nranks, s);
+        case AR_BFLOAT16:
+            return wide ? embedding_by_width<AR_BFLOAT16, AR_FLOAT32>(a, nranks, s)
+                        : embedding_by_width<AR_BFLOAT16, AR_BFLOAT16>(a, nranks, s);
+        case AR_FLOAT16:
+            return wide ? embedding_by_width<AR_FLOAT16, AR_FLOAT32>(a, nranks, s)
+                        : embedding_by_width<AR_FLOAT16, AR_FLOAT16>(a, nranks, s);
+        default: return hipErrorInvalidValue;
+    }
+}
+
+hipError_t launch_embedding_backward(const EmbeddingBackwardArgs& a, int nranks, ar_dtype_t dtype, ar_dtype_t table,
+                                     hipStream_t s) {
+    const bool wide = table == AR_FLOAT32;
+    switch (dtype) {
+        case AR_FLOAT32: return backward_by_width<AR_FLOAT32, AR_FLOAT32>(a, nranks, s);
+        case AR_BFLOAT16:
+            return wide ? backward_by_width<AR_BFLOAT16, AR_FLOAT32>(a, nranks, s)
+                        : backward_by_width<AR_BFLOAT16, AR_BFLOAT16>(a, nranks, s);
+        case AR_FLOAT16:
+            return wide ? backward_by_width<AR_FLOAT16, AR_FLOAT32>(a, nranks, s)
+                        : backward_by_width<AR_FLOAT16, AR_FLOAT16>(a, nranks, s);
+        default: return hipErrorInvalidValue;
+    }
+}
+
+}  // namespace arimpl

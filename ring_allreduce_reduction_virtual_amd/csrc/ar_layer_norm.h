@@ -1,6 +1,6 @@
 // Internal interface of layer norm: what the host entry points
 // (ar_layer_norm_api.hip) hand to the kernels (ar_layer_norm_kernels.hip, the
-// forward pass, and ar_layer_norm_backward_kernels.hip).  Not installed;
+// forward pass, and ar_layer_norm_backward_device.h).  Not installed;
 // include/ar.h is the public ABI.
 #pragma once
 
@@ -30,7 +30,8 @@ struct NormForwardArgs {
 
 struct NormBackwardArgs {
     const char* dy[kNormRanks];
-    const char* x[kNormRanks];
+    const char* x[kNormRanks];       // packed: the codes
+    const uint8_t* scales[kNormRanks];
     const char* gamma[kNormRanks];
     const float* mean[kNormRanks];
     const float* rstd[kNormRanks];
@@ -144,5 +145,8 @@ hipError_t launch_norm_forward(const NormForwardArgs& a, int nranks, ar_dtype_t 
 // dx, and the partial sums when `weights`; then the sums.
 hipError_t launch_norm_backward(const NormBackwardArgs& a, int nranks, bool weights, ar_dtype_t dtype,
                                 ar_dtype_t weight, hipStream_t stream);
+// The same from x's codes and scales.
+hipError_t launch_norm_backward_packed(const NormBackwardArgs& a, int nranks, bool weights, ar_dtype_t dtype,
+                                       ar_dtype_t weight, hipStream_t stream);
 
 }  // namespace arimpl

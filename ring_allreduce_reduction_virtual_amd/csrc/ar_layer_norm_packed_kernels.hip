@@ -1,0 +1,13 @@
+// Layer norm's backward pass from the forward pass's input kept in 8 bits
+// (ar_layer_norm_backward_device.h has the kernels).
+
+#include "ar_layer_norm_backward_device.h"
+
+namespace arimpl {
+
+hipError_t launch_norm_backward_packed(const NormBackwardArgs& a, int nranks, bool weights, ar_dtype_t dtype,
+                                       ar_dtype_t weight, hipStream_t s) {
+    return launch_backward<true>(a, nranks, weights, dtype, weight, s);
+}
+
+}  // namespace arimpl

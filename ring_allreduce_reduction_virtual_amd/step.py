@@ -562,10 +562,19 @@ def ar_layer_norm_backward(dys, xs, gammas, means, rstds, dxs=None, weight_grads
     those not passed are not made.  In place: ``dxs=dys``.
     """
     x0 = _rank_list(xs, "xs")
-    n, dev, index, dt = len(xs), x0.device, x0.get_device(), x0.dtype
-    name = _dtype_of(x0, "xs")
+    _dtype_of(x0, "xs")
     rows, cols = x0.shape
-    xp, x_stride = _row_pointers(xs, n, dev, index, dt, rows, cols, "xs")
+    xp, x_stride = _row_pointers(xs, len(xs), x0.device, x0.get_device(), x0.dtype, rows, cols, "xs")
+    return _norm_backward("ar_layer_norm_backward", (xp,), (x_stride,), x0, len(xs), dys, gammas, means, rstds, dxs,
+                          weight_grads, dgammas, dbetas, workspace, stream)
+
+
+def _norm_backward(call, inputs, strides, x0, n, dys, gammas, means, rstds, dxs, weight_grads, dgammas, dbetas,
+                   workspace, stream):
+    """The backward pass `call` from the addresses `inputs` of x, its row stride in `strides` if it has one; `x0` is
+    a tensor of dx's shape, type and device."""
+    dev, index, dt = x0.device, x0.get_device(), x0.dtype
+    rows, cols = x0.shape
     dyp, dy_stride = _row_pointers(dys, n, dev, index, dt, rows, cols, "dys")
     wdt = _weight_dtype(dt, gammas, dgammas, dbetas)
     gp = None if gammas is None else _weights(gammas, n, dev, index, wdt, cols, "gammas")
@@ -591,9 +600,9 @@ def ar_layer_norm_backward(dys, xs, gammas, means, rstds, dxs=None, weight_grads
         if gout is not None or bout is not None:
             workspace = _scratch(ar_layer_norm_workspace_bytes(rows, cols, n), workspace, dev, stream)
         wp, wb = _ws(workspace, dev)
-        rc = _lib.lib().ar_layer_norm_backward(dyp, xp, gp, mp, rp, dxp, gout, bout, rows, cols, dy_stride, x_stride,
-                                               dx_stride, _lib.DTYPES[name], _lib.DTYPES[_FLOATS[wdt]], n, wp, wb,
-                                               _stream_handle(stream, dev.index))
-    _lib.check("ar_layer_norm_backward", rc)
+        rc = getattr(_lib.lib(), call)(dyp, *inputs, gp, mp, rp, dxp, gout, bout, rows, cols, dy_stride, *strides,
+                                       dx_stride, _lib.DTYPES[_FLOATS[dt]], _lib.DTYPES[_FLOATS[wdt]], n, wp, wb,
+                                       _stream_handle(stream, dev.index))
+    _lib.check(call, rc)
     _written(*given)
     return dxs, dgammas, dbetas
