@@ -733,6 +733,49 @@ ar_result_t ar_embedding_backward(const void* const* dy, const void* const* toke
 /* (size_t)-1 for invalid arguments. */
 size_t ar_embedding_workspace_bytes(size_t rows, size_t vocab, size_t cols, int nranks);
 
+/* Softmax cross entropy of logits that are never stored.  Rank r's logits are
+ * z = x W^T: x[r] is `rows` x `cols` (rows x_stride elements apart), weight[r]
+ * `vocab` x `cols` (weight_stride apart), both of dtype, and
+ *   lse[i] = log(sum over v of exp(z[i][v])),  loss[i] = lse[i] - z[i][t]
+ * for the target t = targets[r][i].  loss[r] and lse[r] are `rows` float32
+ * each; the backward pass needs lse.  A target equal to ignore_index gives
+ * loss 0; any other outside [0, vocab) gives NaN.  A NaN or +infinity among a
+ * row's logits makes its lse and loss NaN.  The vocabulary is worked off in
+ * pieces: products of 16-bit elements are summed in float32 by the matrix
+ * cores (float32 ones too), maxima and sums of exponentials kept per piece and
+ * joined in order.  Outputs overlap nothing else; ranks may share one weight.
+ * rows == 0 is a successful no-op; cols == 0 means logits of 0.
+ * `workspace`: at least ar_cross_entropy_workspace_bytes(...) bytes of device
+ * memory, 16-byte aligned.  vocab of 1 to 2^31 - 1, rows < 2^31. */
+ar_result_t ar_cross_entropy(const void* const* x, const void* const* weight, const void* const* targets,
+                             float* const* loss, float* const* lse, size_t rows, size_t vocab, size_t cols,
+                             size_t x_stride, size_t weight_stride, ar_index_t index_type, long long ignore_index,
+                             ar_dtype_t dtype, int nranks, void* workspace, size_t workspace_bytes,
+                             hipStream_t stream);
+
+/* Its gradients, the logits being made again piece by piece.  With
+ * g[i] = scale * dloss[r][i] (dloss: float32; the array NULL: 1),
+ *   dz[i][v] = g[i] * (exp(z[i][v] - lse[i]) - (v == t)),
+ *   dx = dz W,  dweight = dz^T x.
+ * dx[r] has rows dx_stride apart, dweight[r] dweight_stride; either array may
+ * be NULL.  dz is rounded to dtype before the two products, as their operands
+ * have to be (binary16: after scaling by a power of two that brings the
+ * largest |g| near 2^14, so that small gradients do not underflow), and the
+ * sums are float32, rounded once.  Rows that are ignored, or whose g is 0,
+ * take no part whatever x holds there: their dx is 0.  A target outside
+ * [0, vocab) that is not ignored makes its row of dx, and dweight, NaN.
+ * dx[r] may be x[r] with the same stride; outputs overlap nothing else.
+ * The workspace as above, with the backward pass's size. */
+ar_result_t ar_cross_entropy_backward(const float* const* dloss, const void* const* x, const void* const* weight,
+                                      const void* const* targets, const float* const* lse, void* const* dx,
+                                      void* const* dweight, size_t rows, size_t vocab, size_t cols, size_t x_stride,
+                                      size_t weight_stride, size_t dx_stride, size_t dweight_stride,
+                                      ar_index_t index_type, long long ignore_index, ar_dtype_t dtype, double scale,
+                                      int nranks, void* workspace, size_t workspace_bytes, hipStream_t stream);
+/* backward: not 0 for the backward pass.  (size_t)-1 for invalid arguments. */
+size_t ar_cross_entropy_workspace_bytes(size_t rows, size_t vocab, size_t cols, ar_dtype_t dtype, int nranks,
+                                        int backward);
+
 /* Activations in 8 bits.  A block is AR_ACTIVATION_BLOCK consecutive elements
  * of a row (the row's last one may be short).  It has a scale byte e, worth
  * 2^(e-133): the smallest e >= 1 whose 127 * 2^(e-133) reaches the block's

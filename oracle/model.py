@@ -75,3 +75,41 @@ def unpack_activations(codes, scales):
     e = np.repeat(np.asarray(scales).astype(np.int64), ACTIVATION_BLOCK, axis=1)[:, :codes.shape[1]]
     scale = np.where(e == 255, np.nan, np.exp2(np.maximum(e, 1).astype(np.float64) - 133))
     return codes.astype(np.float64) * scale
+
+
+# --------------------------------------------------------------------------
+# cross entropy
+# --------------------------------------------------------------------------
+
+def cross_entropy(x, weight, targets, ignore=-100):
+    """(loss, lse) of every row's logits x W^T."""
+    z = np.asarray(x, dtype=np.float64) @ np.asarray(weight, dtype=np.float64).T
+    with np.errstate(all="ignore"):
+        top = z.max(1)
+        lse = top + np.log(np.exp(z - top[:, None]).sum(1))
+    loss = np.full(len(targets), np.nan)
+    for i, t in enumerate(targets):
+        if t == ignore:
+            loss[i] = 0.0
+        elif 0 <= t < z.shape[1]:
+            loss[i] = lse[i] - z[i, t]
+    return loss, lse
+
+
+def cross_entropy_backward(g, x, weight, targets, lse, ignore=-100):
+    """(dx, dweight, dz) with dz = g (exp(z - lse) - onehot); ignored rows and rows of g = 0 take no part."""
+    x, weight = np.array(x, dtype=np.float64), np.asarray(weight, dtype=np.float64)
+    g = np.asarray(g, dtype=np.float64)
+    live = np.array([t != ignore for t in targets], dtype=bool) & (g != 0)
+    x[~live] = 0
+    dz = np.zeros((x.shape[0], weight.shape[0]))
+    with np.errstate(all="ignore"):
+        dz[live] = np.exp(x[live] @ weight.T - np.asarray(lse, dtype=np.float64)[live, None])
+    for i, t in enumerate(targets):
+        if live[i]:
+            if 0 <= t < weight.shape[0]:
+                dz[i, t] -= 1
+            else:
+                dz[i] = np.nan
+    dz[live] *= g[live, None]
+    return dz @ weight, dz.T @ x, dz

@@ -1,0 +1,258 @@
+// A tile of a matrix product on the matrix cores: out[m][n] = sum over k of
+// A[m][k] B[n][k], float32 sums of 16-bit or float32 elements, kept in
+// registers for the caller's epilogue.  Inline device code in an unnamed
+// namespace, so each kernel source gets its own copy.
+//
+// A workgroup brings 128 bytes of k of each of its rows of A and B to shared
+// memory at a time (global_load_lds: 16 bytes a lane, no registers in between),
+// into one of two buffers while the matrix instructions work on the other.  An
+// operand may lie along k (rows of A or B) or across (rows of k); shared memory
+// holds it as it lies, and 16-bit operands across k are turned on the way to
+// the registers by ds_read_tr16_b64.  Both kinds exchange 16-byte chunks within
+// a row by its number, so that the lanes that read at a time meet different
+// banks.
+#pragma once
+
+#include "ar_step_device.h"
+
+namespace arimpl {
+namespace {
+
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+typedef short s16x8 __attribute__((ext_vector_type(8)));
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
+
+constexpr int kStepBytes = 128;   // of k at a time
+constexpr int kChunk = 16;
+
+// EM x EN outputs by WM x WN wavefronts, each TM x TN squares of 32.
+template <int EM_, int EN_, int WM_, int WN_>
+struct TileOf {
+    static constexpr int EM = EM_, EN = EN_, WM = WM_, WN = WN_;
+    static constexpr int kThreads = WM * WN * 64;
+    static constexpr int TM = EM / WM / 32, TN = EN / WN / 32;
+    static constexpr int kBytes = (EM + EN) * kStepBytes;   // of one buffer
+};
+
+// What out-of-range k reads.
+__device__ const u32x4 kZeroChunk = {0, 0, 0, 0};
+
+// One operand: E rows of it (columns, when it lies across k) from `first` on,
+// of which those from `limit` on are not wanted (the last wanted one is read in
+// their place: nothing of it reaches another output).
+template <int DT, int E, int THREADS, bool ALONG>
+struct Operand {
+    static constexpr int kEs = elem_size<DT>();
+    static constexpr int kChunkElems = kChunk / kEs;
+    static constexpr int kStep = kStepBytes / kEs;             // k at a time
+    static constexpr int kLoads = E * kStepBytes / kChunk / THREADS;
+    static constexpr int kRowChunks = ALONG ? kStepBytes / kChunk : E * kEs / kChunk;
+    static_assert(E * kStepBytes % (kChunk * THREADS) == 0, "whole loads");
+    static_assert(THREADS % kRowChunks == 0, "a thread keeps its chunk of a row");
+
+    const char* p[kLoads];
+    uint64_t advance;
+    int k0[kLoads];   // first k of each load within a step
+
+    // which chunk of a row stands at a place, and where a chunk stands
+    static __device__ __forceinline__ int swap(int row, int chunk) {
+        if constexpr (ALONG) {
+            return chunk ^ ((row >> 1) & 7);
+        } else if constexpr (kEs == 2) {
+            return chunk ^ (((row & 3) << 2) & (kRowChunks - 1));
+        } else {
+            return chunk ^ (((row >> 2) & 1) << 3);
+        }
+    }
+
+    __device__ __forceinline__ void start(const char* base, uint64_t stride, uint64_t first, uint64_t limit) {
+        const int place = threadIdx.x % kRowChunks;
+#pragma unroll
+        for (int j = 0; j < kLoads; ++j) {
+            const int row = (j * THREADS + static_cast<int>(threadIdx.x)) / kRowChunks;
+            const int chunk = swap(row, place);
+            if constexpr (ALONG) {
+                const uint64_t r = std::min<uint64_t>(first + row, limit - 1);
+                p[j] = base + r * stride + chunk * kChunk;
+                k0[j] = chunk * kChunkElems;
+            } else {
+                const uint64_t c = std::min<uint64_t>(first + chunk * kChunkElems,
+                                                      (limit - 1) / kChunkElems * kChunkElems);
+                p[j] = base + row * stride + c * kEs;
+                k0[j] = row;
+            }
+        }
+        advance = ALONG ? kStepBytes : kStep * stride;
+    }
+
+    // Brings the next step of k, of which `left` are in range (ALONG: rounded up
+    // to whole chunks, whose rest must be zeros), to shared memory at `to`.
+    __device__ __forceinline__ void issue(uint32_t to, uint64_t left) {
+        to = __builtin_amdgcn_readfirstlane(to + (threadIdx.x & ~63u) * kChunk);
+#pragma unroll
+        for (int j = 0; j < kLoads; ++j) {
+            const char* q = p[j];
+            if (left < kStep && static_cast<uint64_t>(k0[j]) >= left) q = reinterpret_cast<const char*>(&kZeroChunk);
+            // m0 says where in shared memory, and needs a wait before the load uses it; the
+            // compiler keeps nothing there in kernels without indexed registers
+            asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(to + j * THREADS * kChunk),
+                         "v"(q)
+                         : "memory");
+            p[j] += advance;
+        }
+    }
+
+    // Where this lane reads in the operand's part of a buffer: for the T squares
+    // of 32 from row (column) `first` on.  A lane's part of a square is 16 bytes
+    // along k for each half of the wavefront: chunk 2 kk + lane / 32 of a step.
+    template <int T>
+    struct Lane {
+        uint32_t at[ALONG ? 1 : T];
+    };
+    template <int T>
+    static __device__ __forceinline__ Lane<T> lane(int first) {
+        const int l = threadIdx.x & 63, half = l >> 5;
+        Lane<T> r;
+        if constexpr (ALONG) {
+            const int row = first + (l & 31);
+            r.at[0] = row * kStepBytes + swap(row, half) * kChunk;
+        } else if constexpr (kEs == 2) {
+            const int j = l & 15, k = half * 8 + j / 4;
+#pragma unroll
+            for (int t = 0; t < T; ++t) {
+                const int chunk = (first + t * 32 + ((l >> 4) & 1) * 16) / 8 + (j % 4) / 2;
+                r.at[t] = k * E * kEs + swap(k, chunk) * kChunk + (j % 2) * 8;
+            }
+        } else {
+#pragma unroll
+            for (int t = 0; t < T; ++t) {
+                const int m = first + t * 32 + (l & 31);
+                r.at[t] = half * 4 * E * kEs + swap(half * 4, m / 4) * kChunk + (m % 4) * 4;
+            }
+        }
+        return r;
+    }
+    template <int T>
+    static __device__ __forceinline__ u32x4 read(const char* part, const Lane<T>& r, int t, int kk) {
+        if constexpr (ALONG) {
+            // the rows of a square differ from the next one's by 32: the same exchange
+            return *reinterpret_cast<const u32x4*>(part + t * 32 * kStepBytes + (r.at[0] ^ (kk << 5)));
+        } else if constexpr (kEs == 2) {
+            typedef __attribute__((address_space(3))) s16x4 shared_s16x4;
+            const char* const q = part + r.at[t] + kk * 16 * E * kEs;
+            const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((shared_s16x4*)(q));
+            const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((shared_s16x4*)(q + 4 * E * kEs));
+            return __builtin_bit_cast(u32x4, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
+        } else {
+            const char* const q = part + r.at[t] + kk * 8 * E * kEs;
+            u32x4 v;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) v[i] = *reinterpret_cast<const uint32_t*>(q + i * E * kEs);
+            return v;
+        }
+    }
+};
+
+template <int DT>
+__device__ __forceinline__ f32x16 multiply(u32x4 a, u32x4 b, f32x16 c) {
+    if constexpr (DT == AR_BFLOAT16) {
+        return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0,
+                                                       0, 0);
+    } else if constexpr (DT == AR_FLOAT16) {
+        return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, b), c, 0, 0,
+                                                      0);
+    } else {
+        // k in another order than in memory, the same for both
+#pragma unroll
+        for (int i = 0; i < 4; ++i) c = __builtin_amdgcn_mfma_f32_32x32x2f32(as_f(a[i]), as_f(b[i]), c, 0, 0, 0);
+        return c;
+    }
+}
+
+// Lane l of a square's sums has column n = l % 32, and in register i the row
+// m = row_of(i) + 4 * (l / 32).
+constexpr int row_of(int i) { return 8 * (i / 4) + i % 4; }
+
+// The sums of one tile, from k = 0 to `depth`.  `buffers`: 2 * Tile::kBytes of
+// shared memory, free again when every wavefront has passed a barrier.
+template <int DT, class Tile, bool A_ALONG, bool B_ALONG>
+__device__ __forceinline__ void product(char* buffers, const char* a, uint64_t a_stride, uint64_t a_first,
+                                        uint64_t a_limit, const char* b, uint64_t b_stride, uint64_t b_first,
+                                        uint64_t b_limit, uint64_t depth, f32x16 (&sum)[Tile::TM][Tile::TN]) {
+    typedef Operand<DT, Tile::EM, Tile::kThreads, A_ALONG> A;
+    typedef Operand<DT, Tile::EN, Tile::kThreads, B_ALONG> B;
+    constexpr int kStep = A::kStep;
+#pragma unroll
+    for (int i = 0; i < Tile::TM; ++i) {
+#pragma unroll
+        for (int j = 0; j < Tile::TN; ++j) sum[i][j] = f32x16{};
+    }
+    if (depth == 0) return;
+    A oa;
+    B ob;
+    oa.start(a, a_stride, a_first, a_limit);
+    ob.start(b, b_stride, b_first, b_limit);
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const auto la = A::template lane<Tile::TM>((wave / Tile::WN) * Tile::TM * 32);
+    const auto lb = B::template lane<Tile::TN>((wave % Tile::WN) * Tile::TN * 32);
+    typedef __attribute__((address_space(3))) char shared_char;
+    const uint32_t base = static_cast<uint32_t>(reinterpret_cast<uintptr_t>((shared_char*)buffers));
+    constexpr uint32_t kA = Tile::EM * kStepBytes;
+    oa.issue(base, depth);
+    ob.issue(base + kA, depth);
+    uint32_t now = 0;
+    for (uint64_t k = 0; k < depth; k += kStep) {
+        // this step's loads have come, every wavefront's after the barrier; and every
+        // wavefront has read the other buffer's step
+        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+        __syncthreads();
+        const uint32_t next = now ^ 1u;
+        if (k + kStep < depth) {
+            oa.issue(base + next * Tile::kBytes, depth - k - kStep);
+            ob.issue(base + next * Tile::kBytes + kA, depth - k - kStep);
+        }
+        const char* const pa = buffers + now * Tile::kBytes;
+        const char* const pb = pa + kA;
+#pragma unroll
+        for (int kk = 0; kk < 4; ++kk) {
+            u32x4 fa[Tile::TM], fb[Tile::TN];
+#pragma unroll
+            for (int i = 0; i < Tile::TM; ++i) fa[i] = A::template read<Tile::TM>(pa, la, i, kk);
+#pragma unroll
+            for (int j = 0; j < Tile::TN; ++j) fb[j] = B::template read<Tile::TN>(pb, lb, j, kk);
+#pragma unroll
+            for (int i = 0; i < Tile::TM; ++i) {
+#pragma unroll
+                for (int j = 0; j < Tile::TN; ++j) sum[i][j] = multiply<DT>(fa[i], fb[j], sum[i][j]);
+            }
+        }
+        now = next;
+    }
+}
+
+// A launch's tiles to workgroups.  Workgroups go to the XCDs in turn; each XCD
+// takes a stretch of neighbouring tiles, walked `kAcross` n-tiles wide, so that
+// the tiles that it works on at a time share their operands in its L2.
+constexpr uint32_t kAcross = 4;
+struct TilePlace {
+    uint32_t rank, m, n;
+    bool valid;
+    __device__ __forceinline__ TilePlace(uint32_t block, uint32_t tiles_m, uint32_t tiles_n, uint32_t ranks) {
+        const uint32_t all = tiles_m * tiles_n * ranks, each = (all + 7) / 8;
+        const uint32_t t = (block & 7) * each + (block >> 3);
+        valid = (block >> 3) < each && t < all;
+        rank = t / (tiles_m * tiles_n);
+        const uint32_t in = t % (tiles_m * tiles_n);
+        const uint32_t group = in / (kAcross * tiles_m), rest = in % (kAcross * tiles_m);
+        const uint32_t width = std::min(kAcross, tiles_n - group * kAcross);
+        m = rest / width;
+        n = group * kAcross + rest % width;
+    }
+};
+inline uint64_t tile_blocks(uint64_t tiles) { return (tiles + 7) / 8 * 8; }
+
+}  // namespace
+}  // namespace arimpl

@@ -1,5 +1,5 @@
-"""Python binding of the operators at a model's ends (include/ar.h): the embedding with its gradient, and
-activations in 8 bits.
+"""Python binding of the operators at a model's ends (include/ar.h): the embedding with its gradient, the
+cross entropy of unstored logits with its gradients, and activations in 8 bits.
 
 Argument marshalling only, in the manner of the training-step operators: one
 tensor per virtual rank in each sequence, checks of device, type and shape,
@@ -129,6 +129,104 @@ def ar_embedding_backward(dys, tokens, vocab=None, dtables=None, scale: float = 
     _lib.check("ar_embedding_backward", rc)
     _written(given)
     return dtables
+
+
+# --------------------------------------------------------------------------
+# cross entropy
+# --------------------------------------------------------------------------
+
+def ar_cross_entropy_workspace_bytes(rows: int, vocab: int, cols: int, dtype: str, nranks: int,
+                                     backward: bool = False) -> int:
+    v = _lib.lib().ar_cross_entropy_workspace_bytes(rows, vocab, cols, _lib.DTYPES[dtype], nranks, 1 if backward else 0)
+    if v == ctypes.c_size_t(-1).value:
+        raise ValueError("invalid arguments for ar_cross_entropy_workspace_bytes: "
+                         + _lib.lib().ar_get_last_error_detail().decode())
+    return v
+
+
+def _cross_inputs(xs, weights, targets):
+    """What both passes read: (first x, dev, index, (rows, vocab, cols), addresses, strides, index type)."""
+    x0 = _rank_list(xs, "xs")
+    w0 = _rank_list(weights, "weights")
+    t0, index_type = _index_list(targets, "targets")
+    n, dev, index = len(xs), x0.device, x0.get_device()
+    _dtype_of(x0, "xs")
+    (rows, cols), vocab = x0.shape, w0.shape[0]
+    xp, x_stride = _row_pointers(xs, n, dev, index, x0.dtype, rows, cols, "xs")
+    wp, w_stride = _row_pointers(weights, n, dev, index, x0.dtype, vocab, cols, "weights")
+    tp = _pointers(targets, dev, index, t0.dtype, [rows] * n, "targets")
+    _per_rank(targets, n, "targets")
+    return x0, n, dev, index, (rows, vocab, cols), (xp, wp, tp), (x_stride, w_stride), index_type
+
+
+def ar_cross_entropy(xs, weights, targets, losses=None, lses=None, ignore_index: int = -100, workspace=None,
+                     stream=None):
+    """Softmax cross entropy of every rank's logits ``x @ weight.t()``, which are never stored.
+
+    `xs` are [rows, cols], `weights` [vocab, cols] of the same type, `targets`
+    flat int32 or int64 tensors.  Returns (losses, lses): each row's loss (0
+    where the target is `ignore_index`, NaN where it is outside the
+    vocabulary) and the logarithm of its sum of exponentials, which
+    :func:`ar_cross_entropy_backward` takes; float32, one tensor per rank in
+    each.
+    """
+    x0, n, dev, index, shape, inputs, strides, index_type = _cross_inputs(xs, weights, targets)
+    rows = shape[0]
+    name = _FLOATS[x0.dtype]
+    given = (losses, lses)
+    got = []
+    for outs, what in ((losses, "losses"), (lses, "lses")):
+        if outs is None:
+            got.append(_new_parts((n, rows), torch.float32, dev, stream))
+        else:
+            _per_rank(outs, n, what)
+            got.append((outs, _pointers(outs, dev, index, torch.float32, [rows] * n, what)))
+    (losses, lp), (lses, sp) = got
+    with _on_device(dev):
+        workspace = _scratch(ar_cross_entropy_workspace_bytes(*shape, name, n), workspace, dev, stream)
+        wp, wb = _ws(workspace, dev)
+        rc = _lib.lib().ar_cross_entropy(*inputs, lp, sp, *shape, *strides, index_type, ignore_index,
+                                         _lib.DTYPES[name], n, wp, wb, _stream_handle(stream, dev.index))
+    _lib.check("ar_cross_entropy", rc)
+    _written(*given)
+    return losses, lses
+
+
+def ar_cross_entropy_backward(dlosses, xs, weights, targets, lses, dxs=None, dweights=None, input_grads: bool = True,
+                              weight_grads: bool = True, ignore_index: int = -100, scale: float = 1.0, workspace=None,
+                              stream=None):
+    """Gradients of :func:`ar_cross_entropy`; returns (dxs, dweights), one tensor per rank in each.
+
+    Row i's loss counts `scale` times ``dlosses[r][i]`` (None: 1).  Tensors may
+    be passed for the results (a rank's slice of its gradient bucket); with
+    ``input_grads=False`` or ``weight_grads=False`` those not passed are not
+    made.  In place: ``dxs=xs``.
+    """
+    x0, n, dev, index, shape, inputs, strides, index_type = _cross_inputs(xs, weights, targets)
+    rows, vocab, cols = shape
+    dt, name = x0.dtype, _FLOATS[x0.dtype]
+    _per_rank(lses, n, "lses")
+    sp = _pointers(lses, dev, index, torch.float32, [rows] * n, "lses")
+    dp = None
+    if dlosses is not None:
+        _per_rank(dlosses, n, "dlosses")
+        dp = _pointers(dlosses, dev, index, torch.float32, [rows] * n, "dlosses")
+    given = (dxs, dweights)
+    gx = gw = None
+    x_stride = w_stride = cols
+    if dxs is not None or input_grads:
+        dxs, gx, x_stride = _out_rows(dxs, (rows, cols), n, dt, dev, index, "dxs", stream)
+    if dweights is not None or weight_grads:
+        dweights, gw, w_stride = _out_rows(dweights, (vocab, cols), n, dt, dev, index, "dweights", stream)
+    with _on_device(dev):
+        workspace = _scratch(ar_cross_entropy_workspace_bytes(*shape, name, n, True), workspace, dev, stream)
+        wp, wb = _ws(workspace, dev)
+        rc = _lib.lib().ar_cross_entropy_backward(dp, *inputs, sp, gx, gw, *shape, *strides, x_stride, w_stride,
+                                                  index_type, ignore_index, _lib.DTYPES[name], scale, n, wp, wb,
+                                                  _stream_handle(stream, dev.index))
+    _lib.check("ar_cross_entropy_backward", rc)
+    _written(*given)
+    return dxs, dweights
 
 
 # --------------------------------------------------------------------------

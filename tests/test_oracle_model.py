@@ -71,3 +71,40 @@ def test_layer_norm_gradient_holds_for_the_packed_input():
         slope = ((step.layer_norm(x + d)[0] - step.layer_norm(x - d)[0]) * dy).sum() / (2 * h)
         # the difference's own rounding: 2^-52 of terms of order one over 2h, and its h^2 term
         assert abs(slope - dx[at]) < 1e-8
+
+
+def test_cross_entropy_of_known_logits():
+    x = np.array([[1.0, 0.0], [0.0, 0.0], [0.0, 2.0]])
+    w = np.array([[np.log(3.0), 0.0], [0.0, 1.0], [0.0, 1.0]])
+    loss, lse = model.cross_entropy(x, w, [0, 1, -100])
+    assert np.allclose(lse, [np.log(5), np.log(3), np.log(1 + 2 * np.e ** 2)])
+    assert np.allclose(loss, [np.log(5 / 3), np.log(3), 0])
+    assert np.isnan(model.cross_entropy(x, w, [3, -1, 0])[0][:2]).all()
+
+
+def test_cross_entropy_gradient_against_differences():
+    rng = np.random.default_rng(3)
+    x, w, t = rng.standard_normal((5, 4)), rng.standard_normal((7, 4)), [0, 6, -100, 3, 3]
+    g, h = rng.standard_normal(5), 1e-6
+    lse = model.cross_entropy(x, w, t)[1]
+    dx, dw, dz = model.cross_entropy_backward(g, x, w, t, lse)
+    assert (dx[2] == 0).all() and np.allclose(dz.sum(1), 0)
+
+    def value(x, w):
+        return (g * model.cross_entropy(x, w, t)[0]).sum()
+
+    for at in [(0, 0), (1, 3), (2, 1), (4, 2)]:
+        d = np.zeros_like(x)
+        d[at] = h
+        assert abs((value(x + d, w) - value(x - d, w)) / (2 * h) - dx[at]) < 1e-8
+    for at in [(0, 0), (6, 1), (3, 3), (2, 2)]:
+        d = np.zeros_like(w)
+        d[at] = h
+        assert abs((value(x, w + d) - value(x, w - d)) / (2 * h) - dw[at]) < 1e-8
+
+
+def test_cross_entropy_rows_that_take_no_part():
+    x = np.array([[1.0, 2.0], [np.nan, np.inf], [3.0, 1.0]])
+    w = np.ones((3, 2))
+    dx, dw, _ = model.cross_entropy_backward([1.0, 5.0, 0.0], x, w, [1, -100, 2], [3 + np.log(3), 0, 0])
+    assert np.isfinite(dw).all() and (dx[1:] == 0).all() and np.isfinite(dx[0]).all()
