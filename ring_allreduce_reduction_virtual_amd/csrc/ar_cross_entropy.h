@@ -7,6 +7,7 @@
 #include <hip/hip_runtime_api.h>
 
 #include <algorithm>
+#include <cstdlib>
 #include <cstdint>
 
 #include "ar.h"
@@ -18,8 +19,10 @@ constexpr int kCrossRanks = 32;
 
 // Columns of a matrix product's operand are read 16 bytes at a time, so
 // operands that do not start, or whose rows do not lie, on 16 bytes are copied
-// first, each row with zeros up to a whole number of them.
+// first, each row with zeros up to a whole number of them; and so are those
+// whose rows lie too far apart for 32-bit offsets.
 constexpr int kOperandBytes = 16;
+constexpr uint64_t kMostOperandStride = 1u << 23;
 constexpr uint64_t padded_cols(uint64_t cols, uint64_t es) {
     return (cols * es + kOperandBytes - 1) / kOperandBytes * kOperandBytes / es;
 }
@@ -34,14 +37,53 @@ constexpr uint64_t kPieceBytes = 256ull << 20, kLeastPiece = 2048;
 inline uint64_t piece_of(uint64_t rows, uint64_t vocab, uint64_t es, int nranks) {
     const uint64_t tiles = (vocab + kVocabTile - 1) / kVocabTile;
     const uint64_t row_bytes = std::max<uint64_t>(1, rows) * nranks * es;
-    const uint64_t most = std::max<uint64_t>(kLeastPiece, kPieceBytes / row_bytes) / kVocabTile;
+    const uint64_t most = std::min(std::max(kLeastPiece, kPieceBytes / row_bytes), kMostOperandStride / es) / kVocabTile;
     const uint64_t pieces = (tiles + most - 1) / most;
     return (tiles + pieces - 1) / pieces * kVocabTile;
 }
 
-// Large tiles need rows to fill them.
-constexpr uint64_t kFewRows = 128;
-constexpr uint64_t vocab_tile(uint64_t rows) { return rows <= kFewRows ? 128 : 256; }
+// Tiles of the products, m x n: the large one keeps the matrix cores busiest,
+// the smaller ones give few rows or columns more workgroups.
+enum class CrossTile : int { kTiny = 0, kSmall, kMedium, kLarge };
+constexpr uint64_t tile_m(CrossTile t) { return t == CrossTile::kLarge ? 256 : t == CrossTile::kTiny ? 64 : 128; }
+constexpr uint64_t tile_n(CrossTile t) {
+    return t == CrossTile::kLarge ? 256 : t == CrossTile::kMedium ? 128 : t == CrossTile::kSmall ? 64 : 32;
+}
+// The share of the large tile's rate that a tile reaches when it fills the GPU.
+// Measured on MI355X, TFLOP/s, tiny / small / medium / large: bf16, 2 x 4,096
+// rows of 4,096 against 65,536, forward 412 / 747 / 965 / 1,128, backward (6
+// per logit and column) 289 / 698 / 908 / 1,087; float32, 1,024 rows of 1,024
+// against 8,192, forward 73 / 108 / 117 / (128 workgroups) 68.
+inline double tile_rate(CrossTile t, bool wide) {
+    switch (t) {
+        case CrossTile::kLarge: return 1.0;
+        case CrossTile::kMedium: return wide ? 0.97 : 0.84;
+        case CrossTile::kSmall: return wide ? 0.9 : 0.65;
+        default: return wide ? 0.6 : 0.3;
+    }
+}
+inline uint64_t tiles_in(uint64_t m, uint64_t n, CrossTile t) {
+    return (m + tile_m(t) - 1) / tile_m(t) * ((n + tile_n(t) - 1) / tile_n(t));
+}
+constexpr uint64_t kUnits = 256;   // compute units
+// Microseconds of `batch` products of m x n x depth: what the compute unit with
+// the most tiles takes, at the large tile's 4.4 (float32: 0.47) TFLOP/s each.
+inline double tile_time(CrossTile t, uint64_t m, uint64_t n, uint64_t depth, uint64_t batch, bool wide) {
+    const uint64_t turns = (tiles_in(m, n, t) * batch + kUnits - 1) / kUnits;
+    return 2e-6 * turns * tile_m(t) * tile_n(t) * depth / (tile_rate(t, wide) * (wide ? 0.47 : 4.4));
+}
+constexpr CrossTile kCrossTiles[] = {CrossTile::kLarge, CrossTile::kMedium, CrossTile::kSmall, CrossTile::kTiny};
+inline CrossTile pick_tile(uint64_t m, uint64_t n, uint64_t batch, bool wide) {
+    if (const char* e = getenv("AR_TILE")) return static_cast<CrossTile>(atoi(e));  // TEMPORARY
+    CrossTile best = CrossTile::kLarge;
+    for (const CrossTile t : kCrossTiles) {
+        if (tile_time(t, m, n, 1, batch, wide) < tile_time(best, m, n, 1, batch, wide)) best = t;
+    }
+    return best;
+}
+inline CrossTile forward_tile(uint64_t rows, uint64_t vocab, uint64_t es, int nranks) {
+    return pick_tile(vocab, rows, nranks, es == 4);
+}
 
 // A rank's row of a launch, in the order of the rows that take part.
 struct LiveRow {
@@ -83,12 +125,29 @@ struct CrossArgs {
 
 inline uint64_t sum_cols(uint64_t cols) { return (cols + 3) / 4 * 4; }
 
-// How many parts the sum over a piece is cut into so that few rows fill the
-// GPU; at least 1,024 columns each.
-inline uint32_t dx_splits(uint64_t rows, uint64_t cols, uint64_t piece, int nranks) {
-    const uint64_t tiles = nranks * ((rows + 63) / 64) * ((cols + 127) / 128);
-    const uint64_t wanted = tiles >= 256 ? 1 : 512 / std::max<uint64_t>(1, tiles);
-    return static_cast<uint32_t>(std::max<uint64_t>(1, std::min(wanted, piece / 1024)));
+// The tile of dx's sums, and how many parts the sum over a piece is cut into:
+// few rows and columns make few tiles, and parts (at least 256 of the
+// vocabulary each) more, at the cost of writing and reading their sums, 8 bytes
+// each at 4 TB/s.
+struct DxShape {
+    CrossTile tile;
+    uint32_t splits;
+};
+inline DxShape dx_shape(uint64_t rows, uint64_t cols, uint64_t piece, uint64_t es, int nranks) {
+    DxShape best{CrossTile::kLarge, 1};
+    double least = 0;
+    for (const CrossTile t : kCrossTiles) {
+        for (uint64_t s = 1; s <= piece / kVocabTile && s <= 64; s *= 2) {
+            const double time = tile_time(t, cols, rows, (piece + s - 1) / s, s * nranks, es == 4) +
+                                8e-6 / 4 * static_cast<double>(s * nranks * rows * cols);
+            if (least == 0 || time < least) {
+                least = time;
+                best = {t, static_cast<uint32_t>(s)};
+            }
+        }
+    }
+    if (const char* e = getenv("AR_TILE")) best.tile = static_cast<CrossTile>(atoi(e));  // TEMPORARY
+    return best;
 }
 
 // Copies of rows with zeros behind them: rows [first, first + count) of weight.
@@ -100,13 +159,14 @@ struct AlignArgs {
 hipError_t launch_align(const AlignArgs& a, int nranks, ar_dtype_t dtype, hipStream_t stream);
 
 // A piece's maxima and sums, then, after all pieces, the losses.
-hipError_t launch_cross_stats(const CrossArgs& a, int nranks, ar_dtype_t dtype, hipStream_t stream);
+hipError_t launch_cross_stats(const CrossArgs& a, int nranks, CrossTile tile, ar_dtype_t dtype, hipStream_t stream);
 hipError_t launch_cross_loss(const CrossArgs& a, int nranks, hipStream_t stream);
 // The live rows, and their copies of x.
 hipError_t launch_cross_live(const CrossArgs& a, int nranks, ar_dtype_t dtype, hipStream_t stream);
 // A piece's dz, then its part of dx's sums and its rows of dweight.
 hipError_t launch_cross_dz(const CrossArgs& a, int nranks, ar_dtype_t dtype, hipStream_t stream);
-hipError_t launch_cross_dx(const CrossArgs& a, int nranks, bool add, ar_dtype_t dtype, hipStream_t stream);
+hipError_t launch_cross_dx(const CrossArgs& a, int nranks, bool add, CrossTile tile, ar_dtype_t dtype,
+                           hipStream_t stream);
 hipError_t launch_cross_dweight(const CrossArgs& a, int nranks, ar_dtype_t dtype, hipStream_t stream);
 hipError_t launch_cross_finish(const CrossArgs& a, int nranks, ar_dtype_t dtype, hipStream_t stream);
 

@@ -13,7 +13,7 @@ using namespace arimpl;
 
 namespace {
 
-constexpr uint64_t kMaxTokens = (1ull << 31) - 1, kMaxVocab = (1ull << 31) - 1, kMaxWidth = 1ull << 22;
+constexpr uint64_t kMaxTokens = (1ull << 31) - 1, kMaxVocab = (1ull << 31) - 1, kMaxWidth = 1ull << 20;
 // Tiles of one launch: its threads are 32-bit numbers.
 constexpr uint64_t kMaxTiles = 1ull << 22;
 
@@ -36,7 +36,9 @@ struct Layout {
     uint64_t x = 0, weight = 0;                                                    // aligned copies
     uint64_t partials = 0, target_logit = 0;                                       // forward
     uint64_t live_count = 0, place = 0, unscale = 0, live = 0, dz = 0, sums = 0;   // backward
-    uint32_t splits = 1;
+    DxShape dx{};
+    CrossTile tile{};
+    uint64_t tiles = 0;   // forward, of the vocabulary
 
     uint64_t take(uint64_t bytes) {
         const uint64_t at = all;
@@ -50,15 +52,17 @@ struct Layout {
         x = take(n * rows * padded * es);
         weight = take(n * std::min(piece, vocab) * padded * es);
         if (backward) {
-            splits = dx_splits(rows, cols, piece, static_cast<int>(n));
+            dx = dx_shape(rows, cols, piece, es, static_cast<int>(n));
             live_count = take(n * 4);
             unscale = take(n * 4);
             place = take(n * rows * 4);
             live = take(n * rows * sizeof(LiveRow));
             dz = take(n * rows * piece * es);
-            sums = take(n * splits * rows * sum_cols(cols) * 4);
+            sums = take(n * dx.splits * rows * sum_cols(cols) * 4);
         } else {
-            partials = take(n * ((vocab + vocab_tile(rows) - 1) / vocab_tile(rows)) * rows * 8);
+            tile = forward_tile(rows, vocab, es, static_cast<int>(n));
+            tiles = (vocab + tile_m(tile) - 1) / tile_m(tile);
+            partials = take(n * tiles * rows * 8);
             target_logit = take(n * rows * 4);
         }
     }
@@ -67,7 +71,8 @@ struct Layout {
 // Whether an operand's rows can be read 16 bytes at a time, with nothing but
 // the row's own elements in the last ones.
 bool aligned(const void* const* p, int n, uint64_t stride, uint64_t cols, uint64_t es) {
-    if (stride * es % kOperandBytes != 0 || cols * es % kOperandBytes != 0) return false;
+    if (stride * es % kOperandBytes != 0 || cols * es % kOperandBytes != 0 || stride * es > kMostOperandStride)
+        return false;
     for (int r = 0; r < n; ++r) {
         if (reinterpret_cast<uintptr_t>(p[r]) % kOperandBytes != 0) return false;
     }
@@ -155,7 +160,7 @@ ar_result_t ar_cross_entropy(const void* const* x, const void* const* weight, co
             a.wide_index = index_type == AR_INDEX_INT64;
             a.partials = reinterpret_cast<float*>(ws + at.partials);
             a.target_logit = reinterpret_cast<float*>(ws + at.target_logit);
-            a.tiles = static_cast<uint32_t>((vocab + vocab_tile(rows) - 1) / vocab_tile(rows));
+            a.tiles = static_cast<uint32_t>(at.tiles);
             for (int k = 0; k < n; ++k) {
                 a.x[k] = static_cast<const char*>(x[g + k]);
                 a.targets[k] = static_cast<const char*>(targets[g + k]);
@@ -174,7 +179,7 @@ ar_result_t ar_cross_entropy(const void* const* x, const void* const* weight, co
                 const uint64_t count = std::min<uint64_t>(vocab - first, as_is ? vocab : at.piece);
                 rc = set_piece(a, at, ws, weight + g, n, first, count, weight_stride, as_is, dtype, stream);
                 if (rc == AR_SUCCESS)
-                    rc = hip_result(launch_cross_stats(a, n, dtype, stream), "cross_entropy launch");
+                    rc = hip_result(launch_cross_stats(a, n, at.tile, dtype, stream), "cross_entropy launch");
                 if (rc != AR_SUCCESS) return rc;
                 first += count;
             }
@@ -240,7 +245,7 @@ ar_result_t ar_cross_entropy_backward(const float* const* dloss, const void* con
             a.scale = static_cast<float>(scale);
             a.wide_index = index_type == AR_INDEX_INT64;
             a.piece = at.piece;
-            a.splits = at.splits;
+            a.splits = at.dx.splits;
             a.live_count = reinterpret_cast<uint32_t*>(ws + at.live_count);
             a.place = reinterpret_cast<uint32_t*>(ws + at.place);
             a.unscale = reinterpret_cast<float*>(ws + at.unscale);
@@ -264,7 +269,7 @@ ar_result_t ar_cross_entropy_backward(const float* const* dloss, const void* con
                 rc = set_piece(a, at, ws, weight + g, n, first, count, weight_stride, as_is, dtype, stream);
                 if (rc == AR_SUCCESS && rows > 0) rc = hip_result(launch_cross_dz(a, n, dtype, stream), what);
                 if (rc == AR_SUCCESS && rows > 0 && dx != nullptr)
-                    rc = hip_result(launch_cross_dx(a, n, first > 0, dtype, stream), what);
+                    rc = hip_result(launch_cross_dx(a, n, first > 0, at.dx.tile, dtype, stream), what);
                 if (rc == AR_SUCCESS && dweight != nullptr)
                     rc = hip_result(launch_cross_dweight(a, n, dtype, stream), what);
                 if (rc != AR_SUCCESS) return rc;

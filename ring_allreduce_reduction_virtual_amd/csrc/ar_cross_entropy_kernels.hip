@@ -31,9 +31,11 @@ __device__ __forceinline__ int64_t index_at(const char* p, uint64_t i, int wide)
     return wide ? reinterpret_cast<const int64_t*>(p)[i] : reinterpret_cast<const int32_t*>(p)[i];
 }
 
-// Tiles by the number of rows: see start_by_rows.
-typedef TileOf<256, 256, 2, 4> LargeTile;
-typedef TileOf<128, 64, 4, 1> SmallTile;
+// The tiles that pick_tile chooses from.
+typedef TileOf<256, 256, 2, 4, 128, 2> LargeTile;
+typedef TileOf<128, 128, 4, 2, 128, 2> MediumTile;
+typedef TileOf<128, 64, 4, 1, 128, 3> SmallTile;
+typedef TileOf<64, 32, 2, 1, 128, 4> TinyTile;
 
 // ---------------------------------------------------------------------------
 // forward
@@ -42,7 +44,7 @@ typedef TileOf<128, 64, 4, 1> SmallTile;
 template <int DT, class Tile>
 __global__ void __launch_bounds__(Tile::kThreads) k_cross_stats(CrossArgs a, uint32_t tiles_m, uint32_t tiles_n,
                                                                 uint32_t ranks) {
-    __shared__ __attribute__((aligned(1024))) char buffers[2 * Tile::kBytes];
+    __shared__ __attribute__((aligned(1024))) char buffers[Tile::kShared];
     __shared__ float most[Tile::WM][Tile::EN], total[Tile::WM][Tile::EN];
     const TilePlace tile(blockIdx.x, tiles_m, tiles_n, ranks);
     if (!tile.valid) return;
@@ -264,7 +266,7 @@ __global__ void __launch_bounds__(256) k_cross_gather(CrossArgs a, uint64_t padd
 template <int DT, class Tile>
 __global__ void __launch_bounds__(Tile::kThreads) k_cross_dz(CrossArgs a, uint64_t padded, uint32_t tiles_m,
                                                              uint32_t tiles_n, uint32_t ranks) {
-    __shared__ __attribute__((aligned(1024))) char buffers[2 * Tile::kBytes];
+    __shared__ __attribute__((aligned(1024))) char buffers[Tile::kShared];
     const TilePlace tile(blockIdx.x, tiles_m, tiles_n, ranks);
     if (!tile.valid) return;
     constexpr int kEs = elem_size<DT>();
@@ -308,7 +310,7 @@ __global__ void __launch_bounds__(Tile::kThreads) k_cross_dz(CrossArgs a, uint64
 template <int DT, class Tile>
 __global__ void __launch_bounds__(Tile::kThreads) k_cross_dx(CrossArgs a, int add, uint32_t tiles_m, uint32_t tiles_n,
                                                              uint32_t ranks) {
-    __shared__ __attribute__((aligned(1024))) char buffers[2 * Tile::kBytes];
+    __shared__ __attribute__((aligned(1024))) char buffers[Tile::kShared];
     const TilePlace tile(blockIdx.x, tiles_m, tiles_n, ranks * a.splits);
     if (!tile.valid) return;
     constexpr int kEs = elem_size<DT>();
@@ -352,7 +354,7 @@ __global__ void __launch_bounds__(Tile::kThreads) k_cross_dx(CrossArgs a, int ad
 template <int DT, class Tile>
 __global__ void __launch_bounds__(Tile::kThreads) k_cross_dweight(CrossArgs a, uint64_t padded, uint32_t tiles_m,
                                                                   uint32_t tiles_n, uint32_t ranks) {
-    __shared__ __attribute__((aligned(1024))) char buffers[2 * Tile::kBytes];
+    __shared__ __attribute__((aligned(1024))) char buffers[Tile::kShared];
     const TilePlace tile(blockIdx.x, tiles_m, tiles_n, ranks);
     if (!tile.valid) return;
     constexpr int kEs = elem_size<DT>();
@@ -416,8 +418,14 @@ constexpr uint64_t kMostBlocks = 1u << 16;
 
 uint32_t tiles_of(uint64_t n, int tile) { return static_cast<uint32_t>((n + tile - 1) / tile); }
 
-static_assert(LargeTile::EM == vocab_tile(kFewRows + 1) && SmallTile::EM == vocab_tile(kFewRows), "the host's tiles");
-bool few_rows(uint64_t rows) { return rows <= kFewRows; }
+template <class Tile>
+constexpr bool is_tile(CrossTile t) {
+    return static_cast<uint64_t>(Tile::EM) == tile_m(t) && static_cast<uint64_t>(Tile::EN) == tile_n(t);
+}
+static_assert(kMostStride == kMostOperandStride, "the host's operands");
+static_assert(is_tile<LargeTile>(CrossTile::kLarge) && is_tile<MediumTile>(CrossTile::kMedium) &&
+                  is_tile<SmallTile>(CrossTile::kSmall) && is_tile<TinyTile>(CrossTile::kTiny),
+              "the host's tiles");
 
 template <int DT, class Tile>
 hipError_t start_stats(const CrossArgs& a, int nranks, hipStream_t s) {
@@ -481,13 +489,21 @@ hipError_t start_finish(const CrossArgs& a, int nranks, hipStream_t s) {
     return hipGetLastError();
 }
 
-// f<DT>() for a floating dtype
-#define AR_BY_DTYPE(dtype, ...)                                  \
-    switch (dtype) {                                             \
+// an expression with DT, a floating dtype, and Tile
+#define AR_BY_DTYPE(dtype, ...)                                                   \
+    switch (dtype) {                                                              \
         case AR_FLOAT32: { constexpr int DT = AR_FLOAT32; return __VA_ARGS__; }   \
         case AR_BFLOAT16: { constexpr int DT = AR_BFLOAT16; return __VA_ARGS__; } \
         case AR_FLOAT16: { constexpr int DT = AR_FLOAT16; return __VA_ARGS__; }   \
-        default: return hipErrorInvalidValue;                    \
+        default: return hipErrorInvalidValue;                                     \
+    }
+#define AR_BY_TILE(tile, dtype, ...)                                                               \
+    switch (tile) {                                                                                \
+        case CrossTile::kLarge: { typedef LargeTile Tile; AR_BY_DTYPE(dtype, __VA_ARGS__) }        \
+        case CrossTile::kMedium: { typedef MediumTile Tile; AR_BY_DTYPE(dtype, __VA_ARGS__) }      \
+        case CrossTile::kSmall: { typedef SmallTile Tile; AR_BY_DTYPE(dtype, __VA_ARGS__) }        \
+        case CrossTile::kTiny: { typedef TinyTile Tile; AR_BY_DTYPE(dtype, __VA_ARGS__) }          \
+        default: return hipErrorInvalidValue;                                                      \
     }
 
 }  // namespace
@@ -495,9 +511,8 @@ hipError_t start_finish(const CrossArgs& a, int nranks, hipStream_t s) {
 hipError_t launch_align(const AlignArgs& a, int nranks, ar_dtype_t dtype, hipStream_t s) {
     AR_BY_DTYPE(dtype, start_align<DT>(a, nranks, s))
 }
-hipError_t launch_cross_stats(const CrossArgs& a, int nranks, ar_dtype_t dtype, hipStream_t s) {
-    if (few_rows(a.rows)) AR_BY_DTYPE(dtype, start_stats<DT, SmallTile>(a, nranks, s))
-    AR_BY_DTYPE(dtype, start_stats<DT, LargeTile>(a, nranks, s))
+hipError_t launch_cross_stats(const CrossArgs& a, int nranks, CrossTile tile, ar_dtype_t dtype, hipStream_t s) {
+    AR_BY_TILE(tile, dtype, start_stats<DT, Tile>(a, nranks, s))
 }
 hipError_t launch_cross_loss(const CrossArgs& a, int nranks, hipStream_t s) {
     hipLaunchKernelGGL(k_cross_loss, dim3(tiles_of(a.rows, 16), nranks), dim3(256), 0, s, a);
@@ -507,16 +522,13 @@ hipError_t launch_cross_live(const CrossArgs& a, int nranks, ar_dtype_t dtype, h
     AR_BY_DTYPE(dtype, start_live<DT>(a, nranks, s))
 }
 hipError_t launch_cross_dz(const CrossArgs& a, int nranks, ar_dtype_t dtype, hipStream_t s) {
-    if (few_rows(a.rows)) AR_BY_DTYPE(dtype, start_dz<DT, SmallTile>(a, nranks, s))
-    AR_BY_DTYPE(dtype, start_dz<DT, LargeTile>(a, nranks, s))
+    AR_BY_TILE(pick_tile(a.piece, a.rows, nranks, dtype == AR_FLOAT32), dtype, start_dz<DT, Tile>(a, nranks, s))
 }
-hipError_t launch_cross_dx(const CrossArgs& a, int nranks, bool add, ar_dtype_t dtype, hipStream_t s) {
-    if (few_rows(a.rows)) AR_BY_DTYPE(dtype, start_dx<DT, SmallTile>(a, nranks, add, s))
-    AR_BY_DTYPE(dtype, start_dx<DT, LargeTile>(a, nranks, add, s))
+hipError_t launch_cross_dx(const CrossArgs& a, int nranks, bool add, CrossTile tile, ar_dtype_t dtype, hipStream_t s) {
+    AR_BY_TILE(tile, dtype, start_dx<DT, Tile>(a, nranks, add, s))
 }
 hipError_t launch_cross_dweight(const CrossArgs& a, int nranks, ar_dtype_t dtype, hipStream_t s) {
-    if (few_rows(a.rows)) AR_BY_DTYPE(dtype, start_dweight<DT, SmallTile>(a, nranks, s))
-    AR_BY_DTYPE(dtype, start_dweight<DT, LargeTile>(a, nranks, s))
+    AR_BY_TILE(pick_tile(a.cols, a.count, nranks, dtype == AR_FLOAT32), dtype, start_dweight<DT, Tile>(a, nranks, s))
 }
 hipError_t launch_cross_finish(const CrossArgs& a, int nranks, ar_dtype_t dtype, hipStream_t s) {
     AR_BY_DTYPE(dtype, start_finish<DT>(a, nranks, s))

@@ -3,9 +3,9 @@
 // registers for the caller's epilogue.  Inline device code in an unnamed
 // namespace, so each kernel source gets its own copy.
 //
-// A workgroup brings 128 bytes of k of each of its rows of A and B to shared
+// A workgroup brings 64 or 128 bytes of k of each of its rows of A and B to shared
 // memory at a time (global_load_lds: 16 bytes a lane, no registers in between),
-// into one of two buffers while the matrix instructions work on the other.  An
+// into one of several buffers while the matrix instructions work on another.  An
 // operand may lie along k (rows of A or B) or across (rows of k); shared memory
 // holds it as it lies, and 16-bit operands across k are turned on the way to
 // the registers by ds_read_tr16_b64.  Both kinds exchange 16-byte chunks within
@@ -25,17 +25,23 @@ typedef short s16x8 __attribute__((ext_vector_type(8)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
 
-constexpr int kStepBytes = 128;   // of k at a time
 constexpr int kChunk = 16;
 
-// EM x EN outputs by WM x WN wavefronts, each TM x TN squares of 32.
-template <int EM_, int EN_, int WM_, int WN_>
+// EM x EN outputs by WM x WN wavefronts, each TM x TN squares of 32, in steps of
+// STEP bytes of k; BUFFERS steps in shared memory, one worked on, the others on
+// their way.
+template <int EM_, int EN_, int WM_, int WN_, int STEP_, int BUFFERS_>
 struct TileOf {
-    static constexpr int EM = EM_, EN = EN_, WM = WM_, WN = WN_;
+    static constexpr int EM = EM_, EN = EN_, WM = WM_, WN = WN_, kStepBytes = STEP_, kBuffers = BUFFERS_;
     static constexpr int kThreads = WM * WN * 64;
     static constexpr int TM = EM / WM / 32, TN = EN / WN / 32;
     static constexpr int kBytes = (EM + EN) * kStepBytes;   // of one buffer
+    static constexpr int kShared = kBuffers * kBytes;
 };
+
+// Most bytes from one row of an operand to the next: 256 rows' offsets are
+// 32-bit numbers.
+constexpr uint64_t kMostStride = 1u << 23;
 
 // What out-of-range k reads.
 __device__ const u32x4 kZeroChunk = {0, 0, 0, 0};
@@ -43,7 +49,7 @@ __device__ const u32x4 kZeroChunk = {0, 0, 0, 0};
 // One operand: E rows of it (columns, when it lies across k) from `first` on,
 // of which those from `limit` on are not wanted (the last wanted one is read in
 // their place: nothing of it reaches another output).
-template <int DT, int E, int THREADS, bool ALONG>
+template <int DT, int E, int THREADS, int kStepBytes, bool ALONG>
 struct Operand {
     static constexpr int kEs = elem_size<DT>();
     static constexpr int kChunkElems = kChunk / kEs;
@@ -53,56 +59,65 @@ struct Operand {
     static_assert(E * kStepBytes % (kChunk * THREADS) == 0, "whole loads");
     static_assert(THREADS % kRowChunks == 0, "a thread keeps its chunk of a row");
 
-    const char* p[kLoads];
+    const char* base;          // of the step to bring next, the same in all lanes
     uint64_t advance;
-    int k0[kLoads];   // first k of each load within a step
+    uint32_t offset[kLoads];   // from there: operands' rows lie at most kMostStride bytes apart
 
     // which chunk of a row stands at a place, and where a chunk stands
     static __device__ __forceinline__ int swap(int row, int chunk) {
         if constexpr (ALONG) {
-            return chunk ^ ((row >> 1) & 7);
+            return kStepBytes == 128 ? chunk ^ ((row >> 1) & 7) : chunk ^ ((row >> 2) & 3);
         } else if constexpr (kEs == 2) {
             return chunk ^ (((row & 3) << 2) & (kRowChunks - 1));
         } else {
-            return chunk ^ (((row >> 2) & 1) << 3);
+            return chunk ^ ((((row >> 2) & 1) << 3) & (kRowChunks - 1));
         }
     }
 
-    __device__ __forceinline__ void start(const char* base, uint64_t stride, uint64_t first, uint64_t limit) {
+    __device__ __forceinline__ void start(const char* from, uint64_t stride, uint64_t first, uint64_t limit) {
         const int place = threadIdx.x % kRowChunks;
+        // a tile past the limit has the last wanted row for all of its rows
+        if (first >= limit) first = ALONG ? limit - 1 : (limit - 1) / kChunkElems * kChunkElems;
+        base = from + (ALONG ? first * stride : first * kEs);
+        // past the limit: the last wanted row, or the last wanted column's chunk
+        const uint32_t last = static_cast<uint32_t>(std::min<uint64_t>(limit - 1 - first, E - 1));
 #pragma unroll
         for (int j = 0; j < kLoads; ++j) {
-            const int row = (j * THREADS + static_cast<int>(threadIdx.x)) / kRowChunks;
-            const int chunk = swap(row, place);
+            const uint32_t row = (j * THREADS + threadIdx.x) / kRowChunks, chunk = swap(row, place);
             if constexpr (ALONG) {
-                const uint64_t r = std::min<uint64_t>(first + row, limit - 1);
-                p[j] = base + r * stride + chunk * kChunk;
-                k0[j] = chunk * kChunkElems;
+                offset[j] = std::min(row, last) * static_cast<uint32_t>(stride) + chunk * kChunk;
             } else {
-                const uint64_t c = std::min<uint64_t>(first + chunk * kChunkElems,
-                                                      (limit - 1) / kChunkElems * kChunkElems);
-                p[j] = base + row * stride + c * kEs;
-                k0[j] = row;
+                offset[j] = row * static_cast<uint32_t>(stride) + std::min(chunk, last / kChunkElems) * kChunk;
             }
         }
         advance = ALONG ? kStepBytes : kStep * stride;
     }
 
     // Brings the next step of k, of which `left` are in range (ALONG: rounded up
-    // to whole chunks, whose rest must be zeros), to shared memory at `to`.
-    __device__ __forceinline__ void issue(uint32_t to, uint64_t left) {
+    // to whole chunks, whose rest must be zeros), to shared memory at `to`.  m0
+    // says where in shared memory, and needs a wait before the load uses it; the
+    // compiler keeps nothing there in kernels without indexed registers.
+    __device__ __forceinline__ void issue(uint32_t to, int64_t left) {
         to = __builtin_amdgcn_readfirstlane(to + (threadIdx.x & ~63u) * kChunk);
+        if (left >= kStep) {
 #pragma unroll
-        for (int j = 0; j < kLoads; ++j) {
-            const char* q = p[j];
-            if (left < kStep && static_cast<uint64_t>(k0[j]) >= left) q = reinterpret_cast<const char*>(&kZeroChunk);
-            // m0 says where in shared memory, and needs a wait before the load uses it; the
-            // compiler keeps nothing there in kernels without indexed registers
-            asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(to + j * THREADS * kChunk),
-                         "v"(q)
-                         : "memory");
-            p[j] += advance;
+            for (int j = 0; j < kLoads; ++j) {
+                asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(to + j * THREADS * kChunk),
+                             "v"(offset[j]), "s"(base)
+                             : "memory");
+            }
+        } else {
+#pragma unroll
+            for (int j = 0; j < kLoads; ++j) {
+                const int row = (j * THREADS + static_cast<int>(threadIdx.x)) / kRowChunks;
+                const int k = ALONG ? swap(row, threadIdx.x % kRowChunks) * kChunkElems : row;
+                const char* const q = k < left ? base + offset[j] : reinterpret_cast<const char*>(&kZeroChunk);
+                asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(to + j * THREADS * kChunk),
+                             "v"(q)
+                             : "memory");
+            }
         }
+        base += advance;
     }
 
     // Where this lane reads in the operand's part of a buffer: for the T squares
@@ -176,14 +191,22 @@ __device__ __forceinline__ f32x16 multiply(u32x4 a, u32x4 b, f32x16 c) {
 // m = row_of(i) + 4 * (l / 32).
 constexpr int row_of(int i) { return 8 * (i / 4) + i % 4; }
 
-// The sums of one tile, from k = 0 to `depth`.  `buffers`: 2 * Tile::kBytes of
-// shared memory, free again when every wavefront has passed a barrier.
+// Waits until at most N of the wavefront's loads are on their way.
+template <int N>
+__device__ __forceinline__ void wait_loads() {
+    static_assert(N < 64, "the counter's range");
+    asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
+}
+
+// The sums of one tile, from k = 0 to `depth`.  `buffers`: Tile::kShared bytes
+// of shared memory, free again when every wavefront has passed a barrier.
 template <int DT, class Tile, bool A_ALONG, bool B_ALONG>
 __device__ __forceinline__ void product(char* buffers, const char* a, uint64_t a_stride, uint64_t a_first,
                                         uint64_t a_limit, const char* b, uint64_t b_stride, uint64_t b_first,
                                         uint64_t b_limit, uint64_t depth, f32x16 (&sum)[Tile::TM][Tile::TN]) {
-    typedef Operand<DT, Tile::EM, Tile::kThreads, A_ALONG> A;
-    typedef Operand<DT, Tile::EN, Tile::kThreads, B_ALONG> B;
+    typedef Operand<DT, Tile::EM, Tile::kThreads, Tile::kStepBytes, A_ALONG> A;
+    typedef Operand<DT, Tile::EN, Tile::kThreads, Tile::kStepBytes, B_ALONG> B;
+    constexpr int kParts = Tile::kStepBytes / 32;   // of a step, each a square's 16 bytes for both halves
     constexpr int kStep = A::kStep;
 #pragma unroll
     for (int i = 0; i < Tile::TM; ++i) {
@@ -200,37 +223,70 @@ __device__ __forceinline__ void product(char* buffers, const char* a, uint64_t a
     const auto lb = B::template lane<Tile::TN>((wave % Tile::WN) * Tile::TN * 32);
     typedef __attribute__((address_space(3))) char shared_char;
     const uint32_t base = static_cast<uint32_t>(reinterpret_cast<uintptr_t>((shared_char*)buffers));
-    constexpr uint32_t kA = Tile::EM * kStepBytes;
-    oa.issue(base, depth);
-    ob.issue(base + kA, depth);
-    uint32_t now = 0;
-    for (uint64_t k = 0; k < depth; k += kStep) {
-        // this step's loads have come, every wavefront's after the barrier; and every
-        // wavefront has read the other buffer's step
-        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-        __syncthreads();
-        const uint32_t next = now ^ 1u;
-        if (k + kStep < depth) {
-            oa.issue(base + next * Tile::kBytes, depth - k - kStep);
-            ob.issue(base + next * Tile::kBytes + kA, depth - k - kStep);
-        }
-        const char* const pa = buffers + now * Tile::kBytes;
-        const char* const pb = pa + kA;
+    constexpr uint32_t kA = Tile::EM * Tile::kStepBytes;
+    // Steps past the last bring zeros that nothing reads, so that the number of
+    // loads behind a step's is always the same.
+    int64_t left = static_cast<int64_t>(depth);
+    const auto bring_a = [&](uint32_t buffer) { oa.issue(base + buffer * Tile::kBytes, left); };
+    const auto bring_b = [&](uint32_t buffer) {
+        ob.issue(base + buffer * Tile::kBytes + kA, left);
+        left -= kStep;
+    };
+    constexpr int kBehind = (Tile::kBuffers - 2) * (A::kLoads + B::kLoads);
 #pragma unroll
-        for (int kk = 0; kk < 4; ++kk) {
-            u32x4 fa[Tile::TM], fb[Tile::TN];
-#pragma unroll
-            for (int i = 0; i < Tile::TM; ++i) fa[i] = A::template read<Tile::TM>(pa, la, i, kk);
-#pragma unroll
-            for (int j = 0; j < Tile::TN; ++j) fb[j] = B::template read<Tile::TN>(pb, lb, j, kk);
-#pragma unroll
-            for (int i = 0; i < Tile::TM; ++i) {
-#pragma unroll
-                for (int j = 0; j < Tile::TN; ++j) sum[i][j] = multiply<DT>(fa[i], fb[j], sum[i][j]);
-            }
-        }
-        now = next;
+    for (uint32_t k = 0; k + 1 < Tile::kBuffers; ++k) {
+        bring_a(k);
+        bring_b(k);
     }
+    // A part of a step is read while the matrix instructions work on the part
+    // before, the next step's first one while they work on this step's last.
+    u32x4 fa[2][Tile::TM], fb[2][Tile::TN];
+    const auto read = [&](uint32_t buffer, int kk) {
+        const char* const pa = buffers + buffer * Tile::kBytes;
+#pragma unroll
+        for (int i = 0; i < Tile::TM; ++i) fa[kk & 1][i] = A::template read<Tile::TM>(pa, la, i, kk);
+#pragma unroll
+        for (int j = 0; j < Tile::TN; ++j) fb[kk & 1][j] = B::template read<Tile::TN>(pa + kA, lb, j, kk);
+    };
+    const auto work = [&](int kk) {
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int i = 0; i < Tile::TM; ++i) {
+#pragma unroll
+            for (int j = 0; j < Tile::TN; ++j) sum[i][j] = multiply<DT>(fa[kk & 1][i], fb[kk & 1][j], sum[i][j]);
+        }
+        __builtin_amdgcn_sched_barrier(0);
+    };
+    // Loads are issued in two halves, each before a part's matrix instructions: a
+    // wavefront waits for the memory pipe to take them, and all of them at once
+    // would keep the matrix cores waiting too.
+    wait_loads<kBehind>();
+    __syncthreads();
+    uint32_t now = 0, free = Tile::kBuffers - 1;
+    bring_a(free);
+    read(0, 0);
+    for (uint64_t k = kStep;; k += kStep) {
+#pragma unroll
+        for (int kk = 0; kk + 1 < kParts; ++kk) {
+            read(now, kk + 1);
+            if (kk == 0) bring_b(free);
+            work(kk);
+        }
+        if (k < depth) {
+            // the next step's loads have come, every wavefront's after the barrier; and
+            // every wavefront has read all of this step, whose buffer is free
+            wait_loads<kBehind>();
+            __syncthreads();
+            free = now;
+            now = now + 1 == Tile::kBuffers ? 0 : now + 1;
+            read(now, 0);
+            bring_a(free);
+        }
+        work(kParts - 1);
+        if (k >= depth) break;
+    }
+    // nothing may land in shared memory, or in the next workgroup's, after this
+    wait_loads<0>();
 }
 
 // A launch's tiles to workgroups.  Workgroups go to the XCDs in turn; each XCD
