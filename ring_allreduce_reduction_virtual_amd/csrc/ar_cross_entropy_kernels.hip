@@ -50,18 +50,18 @@ __global__ void __launch_bounds__(Tile::kThreads) k_cross_stats(CrossArgs a, uin
     if (!tile.valid) return;
     constexpr int kEs = elem_size<DT>();
     const uint64_t m0 = static_cast<uint64_t>(tile.m) * Tile::EM, n0 = static_cast<uint64_t>(tile.n) * Tile::EN;
-    f32x16 sum[Tile::TM][Tile::TN];
+    f32x4 sum[Tile::TM][Tile::TN];
     product<DT, Tile, true, true>(buffers, a.weight[tile.rank], a.weight_stride * kEs, m0, a.count, a.x[tile.rank],
                                   a.x_stride * kEs, n0, a.rows, a.cols, sum);
     const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
     const int wm = wave / Tile::WN, wn = wave % Tile::WN;
-    const uint64_t first = m0 + wm * Tile::TM * 32 + 4 * (lane >> 5);   // this lane's first row of the piece
+    const uint64_t first = m0 + wm * Tile::TM * kSquare + 4 * (lane >> 4);   // this lane's first row of the piece
     if (m0 + Tile::EM > a.count) {
 #pragma unroll
         for (int i = 0; i < Tile::TM; ++i) {
 #pragma unroll
-            for (int k = 0; k < 16; ++k) {
-                if (first + i * 32 + row_of(k) >= a.count) {
+            for (int k = 0; k < 4; ++k) {
+                if (first + i * kSquare + k >= a.count) {
 #pragma unroll
                     for (int j = 0; j < Tile::TN; ++j) sum[i][j][k] = -INFINITY;
                 }
@@ -70,38 +70,40 @@ __global__ void __launch_bounds__(Tile::kThreads) k_cross_stats(CrossArgs a, uin
     }
 #pragma unroll
     for (int j = 0; j < Tile::TN; ++j) {
-        const int n = wn * Tile::TN * 32 + j * 32 + (lane & 31);
+        const int n = (wn * Tile::TN + j) * kSquare + (lane & 15);
         float top = -INFINITY;
 #pragma unroll
         for (int i = 0; i < Tile::TM; ++i) {
 #pragma unroll
-            for (int k = 0; k < 16; ++k) top = fmaxf(top, sum[i][j][k]);
+            for (int k = 0; k < 4; ++k) top = fmaxf(top, sum[i][j][k]);
         }
-        top = as_f(across32(as_u(top), [](uint32_t p, uint32_t q) { return as_u(fmaxf(as_f(p), as_f(q))); }));
+        const auto higher = [](uint32_t p, uint32_t q) { return as_u(fmaxf(as_f(p), as_f(q))); };
+        top = as_f(across32(across16(as_u(top), higher), higher));
         // a tile of -infinities (a stretch past the vocabulary) adds 0
         const float from = top == -INFINITY ? 0.0f : top;
         float s = 0;
 #pragma unroll
         for (int i = 0; i < Tile::TM; ++i) {
 #pragma unroll
-            for (int k = 0; k < 16; ++k) s += __builtin_amdgcn_exp2f((sum[i][j][k] - from) * kLog2e);
+            for (int k = 0; k < 4; ++k) s += __builtin_amdgcn_exp2f((sum[i][j][k] - from) * kLog2e);
         }
-        s = as_f(across32(as_u(s), [](uint32_t p, uint32_t q) { return as_u(as_f(p) + as_f(q)); }));
-        if (lane < 32) {
+        const auto both = [](uint32_t p, uint32_t q) { return as_u(as_f(p) + as_f(q)); };
+        s = as_f(across32(across16(as_u(s), both), both));
+        if (lane < 16) {
             most[wm][n] = top;
             total[wm][n] = s;
         }
         if (n0 + n < a.rows) {
             const int64_t t = index_at(a.targets[tile.rank], n0 + n, a.wide_index);
-            const int64_t in = t - static_cast<int64_t>(a.first + first);   // this lane's rows: i * 32 + row_of(k)
-            if (in >= 0 && in < Tile::TM * 32 && t < static_cast<int64_t>(a.vocab)) {
+            const int64_t in = t - static_cast<int64_t>(a.first + first);   // this lane's rows: i * kSquare + k
+            if (in >= 0 && in < Tile::TM * kSquare && t < static_cast<int64_t>(a.vocab)) {
                 float z = 0;
                 bool mine = false;
 #pragma unroll
                 for (int i = 0; i < Tile::TM; ++i) {
 #pragma unroll
-                    for (int k = 0; k < 16; ++k) {
-                        if (in == i * 32 + row_of(k)) {
+                    for (int k = 0; k < 4; ++k) {
+                        if (in == i * kSquare + k) {
                             z = sum[i][j][k];
                             mine = true;
                         }
@@ -273,35 +275,32 @@ __global__ void __launch_bounds__(Tile::kThreads) k_cross_dz(CrossArgs a, uint64
     const uint64_t live = a.live_count[tile.rank];
     const uint64_t m0 = static_cast<uint64_t>(tile.m) * Tile::EM, n0 = static_cast<uint64_t>(tile.n) * Tile::EN;
     if (n0 >= live) return;
-    f32x16 sum[Tile::TM][Tile::TN];
+    f32x4 sum[Tile::TM][Tile::TN];
     // a tile past the vocabulary's end (the piece is padded) has its last row for all
     product<DT, Tile, true, true>(buffers, a.weight[tile.rank], a.weight_stride * kEs, m0, a.count,
                                   a.x_live + tile.rank * a.rows * padded * kEs, padded * kEs, n0, live, a.cols, sum);
     const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
-    const uint64_t first = m0 + (wave / Tile::WN) * Tile::TM * 32 + 4 * (lane >> 5);
+    const uint64_t first = m0 + (wave / Tile::WN) * Tile::TM * kSquare + 4 * (lane >> 4);
 #pragma unroll
     for (int j = 0; j < Tile::TN; ++j) {
-        const uint64_t n = n0 + (wave % Tile::WN) * Tile::TN * 32 + j * 32 + (lane & 31);
+        const uint64_t n = n0 + ((wave % Tile::WN) * Tile::TN + j) * kSquare + (lane & 15);
         if (n >= live) continue;
         const LiveRow row = a.live[tile.rank * a.rows + n];
         const int64_t target = row.target - static_cast<int64_t>(a.first + first);
         char* const to = a.dz + ((tile.rank * a.rows + n) * a.piece + first) * kEs;
 #pragma unroll
         for (int i = 0; i < Tile::TM; ++i) {
+            float d[4];
 #pragma unroll
-            for (int k = 0; k < 16; k += 4) {
-                float d[4];
-#pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    const int m = i * 32 + row_of(k + q);
-                    float p = __builtin_amdgcn_exp2f((sum[i][j][k + q] - row.lse) * kLog2e);
-                    if (target == m) p -= 1.0f;
-                    d[q] = first + m < a.count ? row.g * p : 0.0f;
-                }
-                Raw<DT, 4> r;
-                r.set_all(d);
-                r.template store<false>(to + (i * 32 + row_of(k)) * kEs);
+            for (int k = 0; k < 4; ++k) {
+                const int m = i * kSquare + k;
+                float p = __builtin_amdgcn_exp2f((sum[i][j][k] - row.lse) * kLog2e);
+                if (target == m) p -= 1.0f;
+                d[k] = first + m < a.count ? row.g * p : 0.0f;
             }
+            Raw<DT, 4> r;
+            r.set_all(d);
+            r.template store<false>(to + i * kSquare * kEs);
         }
     }
 }
@@ -323,29 +322,23 @@ __global__ void __launch_bounds__(Tile::kThreads) k_cross_dx(CrossArgs a, int ad
     const uint64_t from = blocks * split / a.splits * kVocabTile;
     const uint64_t end = std::min(a.count, blocks * (split + 1) / a.splits * kVocabTile);
     const uint64_t depth = end > from ? end - from : 0;
-    f32x16 sum[Tile::TM][Tile::TN];
+    f32x4 sum[Tile::TM][Tile::TN];
     product<DT, Tile, false, true>(buffers, a.weight[rank] + from * a.weight_stride * kEs, a.weight_stride * kEs, m0,
                                    a.cols, a.dz + (rank * a.rows * a.piece + from) * kEs, a.piece * kEs, n0, live, depth,
                                    sum);
     const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
-    const uint64_t first = m0 + (wave / Tile::WN) * Tile::TM * 32 + 4 * (lane >> 5);
+    const uint64_t first = m0 + (wave / Tile::WN) * Tile::TM * kSquare + 4 * (lane >> 4);
     const uint64_t width = (a.cols + 3) / 4 * 4;
 #pragma unroll
     for (int j = 0; j < Tile::TN; ++j) {
-        const uint64_t n = n0 + (wave % Tile::WN) * Tile::TN * 32 + j * 32 + (lane & 31);
+        const uint64_t n = n0 + ((wave % Tile::WN) * Tile::TN + j) * kSquare + (lane & 15);
         if (n >= live) continue;
         float* const to = a.sums + ((static_cast<uint64_t>(rank) * a.splits + split) * a.rows + n) * width + first;
 #pragma unroll
         for (int i = 0; i < Tile::TM; ++i) {
-#pragma unroll
-            for (int k = 0; k < 16; k += 4) {
-                const int m = i * 32 + row_of(k);
-                if (first + m >= a.cols) continue;
-                f32x4 v = {sum[i][j][k], sum[i][j][k + 1], sum[i][j][k + 2], sum[i][j][k + 3]};
-                f32x4* const p = reinterpret_cast<f32x4*>(to + m);
-                if (add) v += *p;
-                *p = v;
-            }
+            if (first + i * kSquare >= a.cols) continue;
+            f32x4* const p = reinterpret_cast<f32x4*>(to + i * kSquare);
+            *p = add ? sum[i][j] + *p : sum[i][j];
         }
     }
 }
@@ -359,29 +352,26 @@ __global__ void __launch_bounds__(Tile::kThreads) k_cross_dweight(CrossArgs a, u
     if (!tile.valid) return;
     constexpr int kEs = elem_size<DT>();
     const uint64_t m0 = static_cast<uint64_t>(tile.m) * Tile::EM, n0 = static_cast<uint64_t>(tile.n) * Tile::EN;
-    f32x16 sum[Tile::TM][Tile::TN];
+    f32x4 sum[Tile::TM][Tile::TN];
     product<DT, Tile, false, false>(buffers, a.x_live + tile.rank * a.rows * padded * kEs, padded * kEs, m0, a.cols,
                                     a.dz + tile.rank * a.rows * a.piece * kEs, a.piece * kEs, n0, a.count,
                                     a.live_count[tile.rank], sum);
     const float unscale = a.unscale[tile.rank];
     const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
-    const uint64_t first = m0 + (wave / Tile::WN) * Tile::TM * 32 + 4 * (lane >> 5);
+    const uint64_t first = m0 + (wave / Tile::WN) * Tile::TM * kSquare + 4 * (lane >> 4);
 #pragma unroll
     for (int j = 0; j < Tile::TN; ++j) {
-        const uint64_t n = n0 + (wave % Tile::WN) * Tile::TN * 32 + j * 32 + (lane & 31);
+        const uint64_t n = n0 + ((wave % Tile::WN) * Tile::TN + j) * kSquare + (lane & 15);
         if (n >= a.count) continue;
         char* const to = a.dweight[tile.rank] + (a.first + n) * a.dweight_stride * kEs;
 #pragma unroll
         for (int i = 0; i < Tile::TM; ++i) {
+            float d[4];
 #pragma unroll
-            for (int k = 0; k < 16; k += 4) {
-                float d[4];
-#pragma unroll
-                for (int q = 0; q < 4; ++q) d[q] = sum[i][j][k + q] * unscale;
-                Raw<DT, 4> r;
-                r.set_all(d);
-                store_at<false, false>(r, to, first + i * 32 + row_of(k), a.cols);
-            }
+            for (int k = 0; k < 4; ++k) d[k] = sum[i][j][k] * unscale;
+            Raw<DT, 4> r;
+            r.set_all(d);
+            store_at<false, false>(r, to, first + i * kSquare, a.cols);
         }
     }
 }

@@ -18,7 +18,6 @@
 namespace arimpl {
 namespace {
 
-typedef float f32x16 __attribute__((ext_vector_type(16)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 typedef short s16x8 __attribute__((ext_vector_type(8)));
@@ -26,15 +25,16 @@ typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
 
 constexpr int kChunk = 16;
+constexpr int kSquare = 16;   // of outputs, a matrix instruction's
 
-// EM x EN outputs by WM x WN wavefronts, each TM x TN squares of 32, in steps of
+// EM x EN outputs by WM x WN wavefronts, each TM x TN squares of 16, in steps of
 // STEP bytes of k; BUFFERS steps in shared memory, one worked on, the others on
 // their way.
 template <int EM_, int EN_, int WM_, int WN_, int STEP_, int BUFFERS_>
 struct TileOf {
     static constexpr int EM = EM_, EN = EN_, WM = WM_, WN = WN_, kStepBytes = STEP_, kBuffers = BUFFERS_;
     static constexpr int kThreads = WM * WN * 64;
-    static constexpr int TM = EM / WM / 32, TN = EN / WN / 32;
+    static constexpr int TM = EM / WM / kSquare, TN = EN / WN / kSquare;
     static constexpr int kBytes = (EM + EN) * kStepBytes;   // of one buffer
     static constexpr int kShared = kBuffers * kBytes;
 };
@@ -70,7 +70,7 @@ struct Operand {
         } else if constexpr (kEs == 2) {
             return chunk ^ (((row & 3) << 2) & (kRowChunks - 1));
         } else {
-            return chunk ^ ((((row >> 2) & 1) << 3) & (kRowChunks - 1));
+            return chunk ^ (((row >> 2) & 3) << 2 & (kRowChunks - 1));
         }
     }
 
@@ -121,31 +121,31 @@ struct Operand {
     }
 
     // Where this lane reads in the operand's part of a buffer: for the T squares
-    // of 32 from row (column) `first` on.  A lane's part of a square is 16 bytes
-    // along k for each half of the wavefront: chunk 2 kk + lane / 32 of a step.
+    // from row (column) `first` on.  A lane's part of a square is 16 bytes along k,
+    // by its sixteen of the wavefront: chunk 4 kk + lane / 16 of a step.
     template <int T>
     struct Lane {
         uint32_t at[ALONG ? 1 : T];
     };
     template <int T>
     static __device__ __forceinline__ Lane<T> lane(int first) {
-        const int l = threadIdx.x & 63, half = l >> 5;
+        const int l = threadIdx.x & 63, group = l >> 4, j = l & 15;
         Lane<T> r;
         if constexpr (ALONG) {
-            const int row = first + (l & 31);
-            r.at[0] = row * kStepBytes + swap(row, half) * kChunk;
+            const int row = first + j;
+            r.at[0] = row * kStepBytes + swap(row, group) * kChunk;
         } else if constexpr (kEs == 2) {
-            const int j = l & 15, k = half * 8 + j / 4;
+            const int k = group * 8 + j / 4;
 #pragma unroll
             for (int t = 0; t < T; ++t) {
-                const int chunk = (first + t * 32 + ((l >> 4) & 1) * 16) / 8 + (j % 4) / 2;
+                const int chunk = (first + t * kSquare) / 8 + (j % 4) / 2;
                 r.at[t] = k * E * kEs + swap(k, chunk) * kChunk + (j % 2) * 8;
             }
         } else {
 #pragma unroll
             for (int t = 0; t < T; ++t) {
-                const int m = first + t * 32 + (l & 31);
-                r.at[t] = half * 4 * E * kEs + swap(half * 4, m / 4) * kChunk + (m % 4) * 4;
+                const int m = first + t * kSquare + j;
+                r.at[t] = group * 4 * E * kEs + swap(group * 4, m / 4) * kChunk + (m % 4) * 4;
             }
         }
         return r;
@@ -153,16 +153,16 @@ struct Operand {
     template <int T>
     static __device__ __forceinline__ u32x4 read(const char* part, const Lane<T>& r, int t, int kk) {
         if constexpr (ALONG) {
-            // the rows of a square differ from the next one's by 32: the same exchange
-            return *reinterpret_cast<const u32x4*>(part + t * 32 * kStepBytes + (r.at[0] ^ (kk << 5)));
+            // the rows of a square differ from the next one's by 16: the same exchange
+            return *reinterpret_cast<const u32x4*>(part + t * kSquare * kStepBytes + (r.at[0] ^ (kk << 6)));
         } else if constexpr (kEs == 2) {
             typedef __attribute__((address_space(3))) s16x4 shared_s16x4;
-            const char* const q = part + r.at[t] + kk * 16 * E * kEs;
+            const char* const q = part + r.at[t] + kk * 32 * E * kEs;
             const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((shared_s16x4*)(q));
             const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((shared_s16x4*)(q + 4 * E * kEs));
             return __builtin_bit_cast(u32x4, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
         } else {
-            const char* const q = part + r.at[t] + kk * 8 * E * kEs;
+            const char* const q = part + r.at[t] + kk * 16 * E * kEs;
             u32x4 v;
 #pragma unroll
             for (int i = 0; i < 4; ++i) v[i] = *reinterpret_cast<const uint32_t*>(q + i * E * kEs);
@@ -172,24 +172,23 @@ struct Operand {
 };
 
 template <int DT>
-__device__ __forceinline__ f32x16 multiply(u32x4 a, u32x4 b, f32x16 c) {
+__device__ __forceinline__ f32x4 multiply(u32x4 a, u32x4 b, f32x4 c) {
     if constexpr (DT == AR_BFLOAT16) {
-        return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0,
+        return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0,
                                                        0, 0);
     } else if constexpr (DT == AR_FLOAT16) {
-        return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, b), c, 0, 0,
+        return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, b), c, 0, 0,
                                                       0);
     } else {
         // k in another order than in memory, the same for both
 #pragma unroll
-        for (int i = 0; i < 4; ++i) c = __builtin_amdgcn_mfma_f32_32x32x2f32(as_f(a[i]), as_f(b[i]), c, 0, 0, 0);
+        for (int i = 0; i < 4; ++i) c = __builtin_amdgcn_mfma_f32_16x16x4f32(as_f(a[i]), as_f(b[i]), c, 0, 0, 0);
         return c;
     }
 }
 
-// Lane l of a square's sums has column n = l % 32, and in register i the row
-// m = row_of(i) + 4 * (l / 32).
-constexpr int row_of(int i) { return 8 * (i / 4) + i % 4; }
+// Lane l of a square's sums has column n = l % 16 and rows 4 * (l / 16) to
+// 4 * (l / 16) + 3.
 
 // Waits until at most N of the wavefront's loads are on their way.
 template <int N>
@@ -203,15 +202,17 @@ __device__ __forceinline__ void wait_loads() {
 template <int DT, class Tile, bool A_ALONG, bool B_ALONG>
 __device__ __forceinline__ void product(char* buffers, const char* a, uint64_t a_stride, uint64_t a_first,
                                         uint64_t a_limit, const char* b, uint64_t b_stride, uint64_t b_first,
-                                        uint64_t b_limit, uint64_t depth, f32x16 (&sum)[Tile::TM][Tile::TN]) {
+                                        uint64_t b_limit, uint64_t depth, f32x4 (&sum)[Tile::TM][Tile::TN]) {
     typedef Operand<DT, Tile::EM, Tile::kThreads, Tile::kStepBytes, A_ALONG> A;
     typedef Operand<DT, Tile::EN, Tile::kThreads, Tile::kStepBytes, B_ALONG> B;
-    constexpr int kParts = Tile::kStepBytes / 32;   // of a step, each a square's 16 bytes for both halves
+    // A step is worked off in parts: 64 bytes of k, and half of the squares of m.
+    constexpr int kParts = Tile::kStepBytes / 32, kHalf = Tile::TM / 2;
+    static_assert(Tile::TM % 2 == 0, "halves");
     constexpr int kStep = A::kStep;
 #pragma unroll
     for (int i = 0; i < Tile::TM; ++i) {
 #pragma unroll
-        for (int j = 0; j < Tile::TN; ++j) sum[i][j] = f32x16{};
+        for (int j = 0; j < Tile::TN; ++j) sum[i][j] = f32x4{};
     }
     if (depth == 0) return;
     A oa;
@@ -219,8 +220,8 @@ __device__ __forceinline__ void product(char* buffers, const char* a, uint64_t a
     oa.start(a, a_stride, a_first, a_limit);
     ob.start(b, b_stride, b_first, b_limit);
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const auto la = A::template lane<Tile::TM>((wave / Tile::WN) * Tile::TM * 32);
-    const auto lb = B::template lane<Tile::TN>((wave % Tile::WN) * Tile::TN * 32);
+    const auto la = A::template lane<Tile::TM>((wave / Tile::WN) * Tile::TM * kSquare);
+    const auto lb = B::template lane<Tile::TN>((wave % Tile::WN) * Tile::TN * kSquare);
     typedef __attribute__((address_space(3))) char shared_char;
     const uint32_t base = static_cast<uint32_t>(reinterpret_cast<uintptr_t>((shared_char*)buffers));
     constexpr uint32_t kA = Tile::EM * Tile::kStepBytes;
@@ -238,22 +239,25 @@ __device__ __forceinline__ void product(char* buffers, const char* a, uint64_t a
         bring_a(k);
         bring_b(k);
     }
-    // A part of a step is read while the matrix instructions work on the part
-    // before, the next step's first one while they work on this step's last.
-    u32x4 fa[2][Tile::TM], fb[2][Tile::TN];
-    const auto read = [&](uint32_t buffer, int kk) {
+    // A part is read while the matrix instructions work on the part before, the
+    // next step's first one while they work on this step's last.
+    u32x4 fa[2][kHalf], fb[2][Tile::TN];
+    const auto read = [&](uint32_t buffer, int part) {
         const char* const pa = buffers + buffer * Tile::kBytes;
 #pragma unroll
-        for (int i = 0; i < Tile::TM; ++i) fa[kk & 1][i] = A::template read<Tile::TM>(pa, la, i, kk);
+        for (int i = 0; i < kHalf; ++i) fa[part & 1][i] = A::template read<Tile::TM>(pa, la, (part & 1) * kHalf + i, part / 2);
+        if (part % 2 == 0) {
 #pragma unroll
-        for (int j = 0; j < Tile::TN; ++j) fb[kk & 1][j] = B::template read<Tile::TN>(pa + kA, lb, j, kk);
+            for (int j = 0; j < Tile::TN; ++j) fb[part / 2 & 1][j] = B::template read<Tile::TN>(pa + kA, lb, j, part / 2);
+        }
     };
-    const auto work = [&](int kk) {
+    const auto work = [&](int part) {
         __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-        for (int i = 0; i < Tile::TM; ++i) {
+        for (int i = 0; i < kHalf; ++i) {
+            const int m = (part & 1) * kHalf + i;
 #pragma unroll
-            for (int j = 0; j < Tile::TN; ++j) sum[i][j] = multiply<DT>(fa[kk & 1][i], fb[kk & 1][j], sum[i][j]);
+            for (int j = 0; j < Tile::TN; ++j) sum[m][j] = multiply<DT>(fa[part & 1][i], fb[part / 2 & 1][j], sum[m][j]);
         }
         __builtin_amdgcn_sched_barrier(0);
     };
