@@ -7,7 +7,6 @@
 #include <hip/hip_runtime_api.h>
 
 #include <algorithm>
-#include <cstdlib>
 #include <cstdint>
 
 #include "ar.h"
@@ -51,14 +50,17 @@ constexpr uint64_t tile_n(CrossTile t) {
 }
 // The share of the large tile's rate that a tile reaches when it fills the GPU.
 // Measured on MI355X, TFLOP/s, tiny / small / medium / large: bf16, 2 x 4,096
-// rows of 4,096 against 65,536, forward 412 / 747 / 965 / 1,128, backward (6
-// per logit and column) 289 / 698 / 908 / 1,087; float32, 1,024 rows of 1,024
-// against 8,192, forward 73 / 108 / 117 / (128 workgroups) 68.
+// rows of 4,096 against 65,536, forward 445 / 787 / 1,043 / 1,406, backward (6
+// per logit and column) 308 / 739 / 993 / 1,297; float32, 2 x 4,096 rows of
+// 2,048 against 32,768, forward 91 / 131 / 141 / 145, backward 89 / 129 / 138 /
+// 142.  Where the large tile leaves compute units without work the others are
+// ahead: bf16, 512 rows of 1,024 against 8,192, forward 33 / 19 / 16 / 28 us;
+// 16 rows of 4,096 against 65,536 133 / 127 / 146 / 155.
 inline double tile_rate(CrossTile t, bool wide) {
     switch (t) {
         case CrossTile::kLarge: return 1.0;
-        case CrossTile::kMedium: return wide ? 0.97 : 0.84;
-        case CrossTile::kSmall: return wide ? 0.9 : 0.65;
+        case CrossTile::kMedium: return wide ? 0.97 : 0.75;
+        case CrossTile::kSmall: return wide ? 0.9 : 0.56;
         default: return wide ? 0.6 : 0.3;
     }
 }
@@ -67,14 +69,13 @@ inline uint64_t tiles_in(uint64_t m, uint64_t n, CrossTile t) {
 }
 constexpr uint64_t kUnits = 256;   // compute units
 // Microseconds of `batch` products of m x n x depth: what the compute unit with
-// the most tiles takes, at the large tile's 4.4 (float32: 0.47) TFLOP/s each.
+// the most tiles takes, at the large tile's 5.3 (float32: 0.56) TFLOP/s each.
 inline double tile_time(CrossTile t, uint64_t m, uint64_t n, uint64_t depth, uint64_t batch, bool wide) {
     const uint64_t turns = (tiles_in(m, n, t) * batch + kUnits - 1) / kUnits;
-    return 2e-6 * turns * tile_m(t) * tile_n(t) * depth / (tile_rate(t, wide) * (wide ? 0.47 : 4.4));
+    return 2e-6 * turns * tile_m(t) * tile_n(t) * depth / (tile_rate(t, wide) * (wide ? 0.56 : 5.3));
 }
 constexpr CrossTile kCrossTiles[] = {CrossTile::kLarge, CrossTile::kMedium, CrossTile::kSmall, CrossTile::kTiny};
 inline CrossTile pick_tile(uint64_t m, uint64_t n, uint64_t batch, bool wide) {
-    if (const char* e = getenv("AR_TILE")) return static_cast<CrossTile>(atoi(e));  // TEMPORARY
     CrossTile best = CrossTile::kLarge;
     for (const CrossTile t : kCrossTiles) {
         if (tile_time(t, m, n, 1, batch, wide) < tile_time(best, m, n, 1, batch, wide)) best = t;
@@ -146,7 +147,6 @@ inline DxShape dx_shape(uint64_t rows, uint64_t cols, uint64_t piece, uint64_t e
             }
         }
     }
-    if (const char* e = getenv("AR_TILE")) best.tile = static_cast<CrossTile>(atoi(e));  // TEMPORARY
     return best;
 }
 
