@@ -36,8 +36,11 @@ constexpr uint64_t kSortTile = static_cast<uint64_t>(kSortTileThreads) * kSortTi
 constexpr int kDigitBits = 9;            // at most; 18 bits of token take two passes
 constexpr int kDigits = 1 << kDigitBits;
 
-// Places of the sorted order that one group of threads adds up (see the kernel).
-constexpr uint64_t kSumChunk = 32;
+// Places of the sorted order that one group of threads adds up (see the
+// kernel): few, so that few tokens fill the GPU, or more, which leave fewer
+// partial sums.
+constexpr uint64_t kFewPlaces = 16384;
+inline uint64_t sum_chunk(uint64_t rows, int nranks) { return rows * nranks <= kFewPlaces ? 8 : 32; }
 
 struct EmbeddingBackwardArgs {
     const char* dy[kEmbeddingRanks];
@@ -50,7 +53,8 @@ struct EmbeddingBackwardArgs {
     uint64_t rows, vocab, cols;
     uint64_t dy_stride, dtable_stride;
     uint64_t tiles;       // of the sort
-    uint64_t chunks;      // of the sum
+    uint64_t chunk;       // places of a chunk of the sum
+    uint64_t chunks;
     int64_t padding;
     float scale;
     int wide_index, accumulate;
@@ -64,12 +68,15 @@ inline int token_bits(uint64_t vocab) {   // of the values 0 to vocab (vocab: ta
     return bits;
 }
 inline uint64_t sort_tiles(uint64_t rows) { return (rows + kSortTile - 1) / kSortTile; }
-inline uint64_t sum_chunks(uint64_t rows) { return (rows + kSumChunk - 1) / kSumChunk; }
+inline uint64_t sum_chunks(uint64_t rows, int nranks) {
+    const uint64_t chunk = sum_chunk(rows, nranks);
+    return (rows + chunk - 1) / chunk;
+}
 
 // 4-byte words of one rank's part of the workspace, in this order.
 constexpr uint64_t sort_words(uint64_t rows) { return 2 * rows; }   // keys; places
 inline uint64_t count_words(uint64_t rows) { return rows > kSortOne ? sort_tiles(rows) * kDigits : 0; }
-inline uint64_t partial_words(uint64_t rows, uint64_t cols) { return sum_chunks(rows) * 2 * cols; }
+inline uint64_t partial_words(uint64_t rows, uint64_t cols, int nranks) { return sum_chunks(rows, nranks) * 2 * cols; }
 
 hipError_t launch_embedding(const EmbeddingArgs& a, int nranks, ar_dtype_t dtype, ar_dtype_t table, hipStream_t stream);
 hipError_t launch_embedding_backward(const EmbeddingBackwardArgs& a, int nranks, ar_dtype_t dtype, ar_dtype_t table,

@@ -39,7 +39,7 @@ struct Parts {   // of the workspace, in 4-byte words
 };
 Parts workspace_parts(uint64_t rows, uint64_t cols, int nranks) {
     const uint64_t n = static_cast<uint64_t>(nranks);
-    return {n * sort_words(rows), n * sort_words(rows), n * count_words(rows), n * partial_words(rows, cols)};
+    return {n * sort_words(rows), n * sort_words(rows), n * count_words(rows), n * partial_words(rows, cols, nranks)};
 }
 
 }  // namespace
@@ -135,7 +135,7 @@ ar_result_t ar_embedding_backward(const void* const* dy, const void* const* toke
                 a.places = words + parts.keys + f * sort_words(rows);
                 a.counts = words + parts.keys + parts.places + f * count_words(rows);
                 a.partials = reinterpret_cast<float*>(words + parts.keys + parts.places + parts.counts +
-                                                      f * partial_words(rows, cols));
+                                                      f * partial_words(rows, cols, nranks));
             }
             a.rows = rows;
             a.vocab = vocab;
@@ -143,7 +143,8 @@ ar_result_t ar_embedding_backward(const void* const* dy, const void* const* toke
             a.dy_stride = dy_stride;
             a.dtable_stride = dtable_stride;
             a.tiles = sort_tiles(rows);
-            a.chunks = sum_chunks(rows);
+            a.chunk = sum_chunk(rows, nranks);
+            a.chunks = sum_chunks(rows, nranks);
             a.padding = padding_index;
             a.scale = static_cast<float>(scale);
             a.wide_index = index_type == AR_INDEX_INT64;

@@ -6,7 +6,7 @@
 //
 // The gradient is a sum by token whose order must not depend on which
 // workgroup comes first, so no row is added to with atomics.  The places are
-// sorted by token, stably; the sorted order is cut into chunks of kSumChunk
+// sorted by token, stably; the sorted order is cut into chunks of 8 or 32
 // places, and a group of threads adds up each chunk's rows of dy.  A token
 // whose places lie within one chunk is done there.  One that crosses a chunk's
 // end leaves a partial sum in each chunk, and a second launch adds these in
@@ -133,20 +133,22 @@ __device__ __forceinline__ void scan_counts(uint32_t (*count)[kDigits], uint32_t
     }
 }
 
-// One rank's places in one workgroup, up to kSortOne of them, all passes.
+// One rank's places in one workgroup, EACH a thread, all passes (4,096 places
+// of 16-bit tokens on each of 8 ranks: 12 us).
+template <int EACH>
 __global__ void __launch_bounds__(kSortThreads) k_sort_one(EmbeddingBackwardArgs a) {
     constexpr int kWaves = kSortThreads / 64;
     __shared__ uint32_t count[kWaves][kDigits];
     __shared__ uint32_t digits[kDigits], totals[kWaves];
-    __shared__ uint32_t keys[kSortOne];
-    __shared__ uint16_t places[kSortOne];
-    static_assert(kSortOne <= 65536, "places of 16 bits");
+    __shared__ uint32_t keys[kSortThreads * EACH];
+    __shared__ uint16_t places[kSortThreads * EACH];
+    static_assert(kSortThreads * EACH <= 65536, "places of 16 bits");
     const int rank = blockIdx.x, wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
     const uint32_t n = static_cast<uint32_t>(a.rows);
-    uint32_t key[kSortEach], place[kSortEach], at[kSortEach];
+    uint32_t key[EACH], place[EACH], at[EACH];
 #pragma unroll
-    for (int i = 0; i < kSortEach; ++i) {
-        place[i] = (wave * kSortEach + i) * 64 + lane;
+    for (int i = 0; i < EACH; ++i) {
+        place[i] = (wave * EACH + i) * 64 + lane;
         key[i] = place[i] < n ? key_at(a, rank, place[i]) : 0xffffffffu;   // stays behind all others
     }
     const uint32_t mask = (1u << a.digit_bits) - 1;
@@ -155,11 +157,11 @@ __global__ void __launch_bounds__(kSortThreads) k_sort_one(EmbeddingBackwardArgs
         for (int d = threadIdx.x; d < kWaves * kDigits; d += kSortThreads) (&count[0][0])[d] = 0;
         __syncthreads();
 #pragma unroll
-        for (int i = 0; i < kSortEach; ++i) at[i] = take_rank(count[wave], (key[i] >> shift) & mask, a.digit_bits);
+        for (int i = 0; i < EACH; ++i) at[i] = take_rank(count[wave], (key[i] >> shift) & mask, a.digit_bits);
         __syncthreads();
         scan_counts<kSortThreads>(count, digits, totals);
 #pragma unroll
-        for (int i = 0; i < kSortEach; ++i) {
+        for (int i = 0; i < EACH; ++i) {
             const uint32_t d = (key[i] >> shift) & mask;
             const uint32_t to = digits[d] + count[wave][d] + at[i];
             keys[to] = key[i];
@@ -167,8 +169,8 @@ __global__ void __launch_bounds__(kSortThreads) k_sort_one(EmbeddingBackwardArgs
         }
         __syncthreads();
 #pragma unroll
-        for (int i = 0; i < kSortEach; ++i) {
-            const uint32_t from = (wave * kSortEach + i) * 64 + lane;
+        for (int i = 0; i < EACH; ++i) {
+            const uint32_t from = (wave * EACH + i) * 64 + lane;
             key[i] = keys[from];
             place[i] = places[from];
         }
@@ -177,8 +179,8 @@ __global__ void __launch_bounds__(kSortThreads) k_sort_one(EmbeddingBackwardArgs
     uint32_t* const keys_to = a.keys + rank * sort_words(a.rows);
     uint32_t* const places_to = a.places + rank * sort_words(a.rows);
 #pragma unroll
-    for (int i = 0; i < kSortEach; ++i) {
-        const uint32_t to = (wave * kSortEach + i) * 64 + lane;
+    for (int i = 0; i < EACH; ++i) {
+        const uint32_t to = (wave * EACH + i) * 64 + lane;
         if (to < n) {
             keys_to[to] = key[i];
             places_to[to] = place[i];
@@ -291,6 +293,9 @@ __global__ void __launch_bounds__(kSortTileThreads) k_sort_place(EmbeddingBackwa
 // the sums
 // ---------------------------------------------------------------------------
 
+template <int DT>
+constexpr int kSumVec = 16 / elem_size<DT>();
+
 // First place of the sorted keys that is not below v.
 __device__ __forceinline__ uint64_t lower_bound(const uint32_t* keys, uint64_t n, uint32_t v) {
     uint64_t lo = 0;
@@ -303,8 +308,10 @@ __device__ __forceinline__ uint64_t lower_bound(const uint32_t* keys, uint64_t n
     return lo;
 }
 
+// A token's sums of V columns from c on, all but the first `skip` of them, to
+// its row; a row of fewer than V columns up to its end.
 template <int DT, int V>
-__device__ __forceinline__ void write_row(const EmbeddingBackwardArgs& a, int rank, uint32_t token, uint64_t c,
+__device__ __forceinline__ void write_row(const EmbeddingBackwardArgs& a, int rank, uint32_t token, uint64_t c, int skip,
                                           const float (&sum)[V]) {
     char* const to = a.dtable[rank] + token * a.dtable_stride * elem_size<DT>();
     float x[V];
@@ -317,80 +324,125 @@ __device__ __forceinline__ void write_row(const EmbeddingBackwardArgs& a, int ra
         for (int j = 0; j < V; ++j) x[j] += r.get(j);
     }
     r.set_all(x);
-    store_at<false, true>(r, to, c, a.cols);
+    if (skip == 0) {
+        store_at<false, true>(r, to, c, a.cols);
+    } else {
+        r.store_from(to + c * elem_size<DT>(), skip);
+    }
 }
 
 __device__ __forceinline__ float* partial_at(const EmbeddingBackwardArgs& a, int rank, uint64_t chunk, int which) {
     return a.partials + ((rank * a.chunks + chunk) * 2 + which) * a.cols;
 }
 
-constexpr uint64_t kZeroRows = 64;   // rows of the table that a workgroup looks at
+// A wavefront's zeros, `n` elements from p: 16 bytes a lane from the first
+// address that they fit, the elements before and behind one by one.
+template <int DT>
+__device__ __forceinline__ void write_zeros(char* p, uint64_t n) {
+    constexpr int kEs = elem_size<DT>(), V = 16 / kEs;
+    const uint32_t lane = threadIdx.x & 63;
+    const uint32_t head = static_cast<uint32_t>((16 - (reinterpret_cast<uintptr_t>(p) & 15)) % 16 / kEs);
+    if (n < V + head) {
+        if (lane < n) store_elem<kEs, false>(p + lane * kEs, 0);
+        return;
+    }
+    const uint64_t body = (n - head) / V * V;
+    const uint32_t tail = static_cast<uint32_t>(n - head - body);
+    const u32x4 zero = {0, 0, 0, 0};
+    for (uint64_t c = lane * V; c < body; c += 64 * V) store16<false>(p + (head + c) * kEs, zero);
+    if (lane < head) store_elem<kEs, false>(p + lane * kEs, 0);
+    if (lane < tail) store_elem<kEs, false>(p + (head + body + lane) * kEs, 0);
+}
 
-// blockIdx.x below sum_blocks: chunks, one for each group of TPR threads;
-// above: rows of the table without a token.  blockIdx.y: stretches of TPR * V
-// columns.
+// Rows of the table that a workgroup looks at, a quarter of them a wavefront.
+// Measured, a table of 8 x 32,768 rows of 4,096 bf16 for 5 tokens (2.1 GB of
+// zeros, which torch's fill writes in 315 us): 357 us; whole workgroups on a row
+// at a time 371, with 32 rows 391, with 64 420, with nontemporal stores 392.
+constexpr uint64_t kZeroRows = 16;
+
+// Workgroups in turn: the ranks (neighbouring workgroups write different
+// buffers), stretches of TPR * V columns, chunks, one for each group of TPR
+// threads; behind all of these, rows of the table without a token, whole rows
+// for a wavefront.
 template <int DT, int TDT, int TPR>
-__global__ void __launch_bounds__(256) k_embedding_sums(EmbeddingBackwardArgs a, uint32_t sum_blocks,
-                                                        uint32_t zero_blocks) {
-    constexpr int V = 8;
+__global__ void __launch_bounds__(256) k_embedding_sums(EmbeddingBackwardArgs a, uint32_t nranks, uint32_t stretches,
+                                                        uint32_t sum_blocks, uint32_t zero_blocks) {
+    constexpr int V = kSumVec<DT>;
     constexpr int kAhead = 8;   // rows on their way
-    const int rank = blockIdx.z;
+    const uint32_t rank = blockIdx.x % nranks, turn = blockIdx.x / nranks;
     const uint32_t* const keys = a.keys + rank * sort_words(a.rows) + a.sorted * a.rows;
     const uint32_t* const places = a.places + rank * sort_words(a.rows) + a.sorted * a.rows;
     const uint32_t vocab = static_cast<uint32_t>(a.vocab);
-    if (blockIdx.x >= sum_blocks) {
-        const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
-        const uint64_t c_end = std::min<uint64_t>(a.cols, (blockIdx.y + 1ull) * TPR * V);
-        Raw<TDT, V> zero = {};
-        for (uint64_t first = (blockIdx.x - sum_blocks) * kZeroRows + wave * 16; first < a.vocab;
+    if (turn >= sum_blocks * stretches) {
+        constexpr int kWaveRows = kZeroRows / 4;
+        const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
+        for (uint64_t first = (turn - sum_blocks * stretches) * kZeroRows + wave * kWaveRows; first < a.vocab;
              first += zero_blocks * kZeroRows) {
             bool empty = false;
-            if (lane < 16 && first + lane < a.vocab) {
+            if (lane < kWaveRows && first + lane < a.vocab) {
                 const uint32_t v = static_cast<uint32_t>(first + lane);
                 const uint64_t at = lower_bound(keys, a.rows, v);
                 empty = at >= a.rows || keys[at] != v;
             }
             for (uint64_t rows = __ballot(empty); rows != 0; rows &= rows - 1) {
-                char* const to = a.dtable[rank] + (first + __builtin_ctzll(rows)) * a.dtable_stride * elem_size<TDT>();
-                for (uint64_t c = blockIdx.y * static_cast<uint64_t>(TPR) * V + lane * V; c < c_end; c += 64 * V)
-                    store_at<false, true>(zero, to, c, a.cols);
+                const uint64_t row = (first + __builtin_ctzll(rows)) * a.dtable_stride;
+                write_zeros<TDT>(a.dtable[rank] + row * elem_size<TDT>(), a.cols);
             }
         }
         return;
     }
-    const uint64_t c = (blockIdx.y * static_cast<uint64_t>(TPR) + threadIdx.x % TPR) * V;
+    // A vector that would cross the row's end is moved back to end there; its first
+    // `skip` columns are the vector's before.
+    uint64_t c = ((turn % stretches) * static_cast<uint64_t>(TPR) + threadIdx.x % TPR) * V;
     if (c >= a.cols) return;
+    int skip = 0;
+    if (a.cols >= V && c > a.cols - V) {
+        skip = static_cast<int>(c - (a.cols - V));
+        c = a.cols - V;
+    }
     uint32_t group = threadIdx.x / TPR;
     if constexpr (TPR >= 64) group = __builtin_amdgcn_readfirstlane(group);
+    const char* const dy = a.dy[rank] + c * elem_size<DT>();
+    const uint64_t dy_stride = a.dy_stride * elem_size<DT>();
     const uint64_t step = static_cast<uint64_t>(sum_blocks) * kRowsAtOnce<TPR>;
-    for (uint64_t chunk = static_cast<uint64_t>(blockIdx.x) * kRowsAtOnce<TPR> + group; chunk < a.chunks; chunk += step) {
-        const uint64_t first = chunk * kSumChunk;
-        const uint64_t end = std::min(a.rows, first + kSumChunk);
+    for (uint64_t chunk = static_cast<uint64_t>(turn / stretches) * kRowsAtOnce<TPR> + group; chunk < a.chunks;
+         chunk += step) {
+        const uint64_t first = chunk * a.chunk;
+        const uint64_t end = std::min(a.rows, first + a.chunk);
         float sum[V];
 #pragma unroll
         for (int j = 0; j < V; ++j) sum[j] = 0;
         uint32_t token = keys[first];
         bool begins = first == 0 || keys[first - 1] != token;   // in this chunk
+        const bool goes_on = end < a.rows && keys[end] == keys[end - 1];
         const auto leave = [&](bool ends) {
             if (token >= vocab) return;
             if (begins && ends) {
-                write_row<TDT>(a, rank, token, c, sum);
+                write_row<TDT>(a, rank, token, c, skip, sum);
             } else {
-                float* const to = partial_at(a, rank, chunk, begins ? 1 : 0);
+                float* const to = partial_at(a, rank, chunk, begins ? 1 : 0) + c;
 #pragma unroll
                 for (int j = 0; j < V; ++j) {
-                    if (c + j < a.cols) to[c + j] = sum[j];
+                    if (j >= skip && c + j < a.cols) to[j] = sum[j];
                 }
             }
         };
         for (uint64_t at = first; at < end; at += kAhead) {
-            uint32_t key[kAhead];
+            uint32_t key[kAhead], place[kAhead];
             Raw<DT, V> r[kAhead];
+            // places past the end read the last one's row, which is not added
 #pragma unroll
             for (int k = 0; k < kAhead; ++k) {
-                key[k] = at + k < end ? keys[at + k] : 0xffffffffu;
-                if (key[k] < vocab)
-                    load_at<false, true>(r[k], a.dy[rank] + places[at + k] * a.dy_stride * elem_size<DT>(), c, a.cols);
+                const uint64_t from = std::min(at + k, end - 1);
+                key[k] = keys[from];
+                place[k] = places[from];
+            }
+            if (a.cols >= V) {
+#pragma unroll
+                for (int k = 0; k < kAhead; ++k) r[k].template load<true>(dy + place[k] * dy_stride);
+            } else {
+#pragma unroll
+                for (int k = 0; k < kAhead; ++k) r[k].load_some(dy + place[k] * dy_stride, static_cast<int>(a.cols));
             }
 #pragma unroll
             for (int k = 0; k < kAhead; ++k) {
@@ -402,50 +454,56 @@ __global__ void __launch_bounds__(256) k_embedding_sums(EmbeddingBackwardArgs a,
 #pragma unroll
                     for (int j = 0; j < V; ++j) sum[j] = 0;
                 }
-                if (token < vocab) {
 #pragma unroll
-                    for (int j = 0; j < V; ++j) sum[j] += r[k].get(j);
-                }
+                for (int j = 0; j < V; ++j) sum[j] += r[k].get(j);
             }
         }
-        leave(end == a.rows || keys[end] != token);
+        leave(!goes_on);
     }
 }
 
-// The tokens that cross the end of a chunk: from the chunk where one begins, the
-// partial sums up to the one where it ends.  A wavefront takes 64 columns, and
-// one chunk after another of those that its workgroup looks at.
-constexpr uint64_t kJoinChunks = 16;
-
+// The tokens that cross the end of a chunk: a wavefront looks at one chunk's
+// end and 256 columns; where a token begins in that chunk and goes on, it adds
+// the partial sums up to the chunk where the token ends.
 template <int TDT>
 __global__ void __launch_bounds__(256) k_embedding_join(EmbeddingBackwardArgs a) {
-    const int rank = blockIdx.z;
+    const int rank = blockIdx.z, lane = threadIdx.x & 63;
     const uint32_t* const keys = a.keys + rank * sort_words(a.rows) + a.sorted * a.rows;
-    const uint64_t c = blockIdx.y * 64ull + (threadIdx.x & 63);
-    if (c >= a.cols) return;
-    const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    for (uint64_t k = wave; k < kJoinChunks; k += 4) {
-        const uint64_t chunk = blockIdx.x * kJoinChunks + k;
-        const uint64_t first = chunk * kSumChunk, end = first + kSumChunk;
-        if (end >= a.rows) return;
-        const uint32_t token = keys[end - 1];
-        if (token >= a.vocab || keys[end] != token || (first > 0 && keys[first - 1] == token)) continue;
-        const uint64_t last = (lower_bound(keys, a.rows, token + 1) - 1) / kSumChunk;
-        float sum = partial_at(a, rank, chunk, 1)[c];
-#pragma unroll 8
-        for (uint64_t j = chunk + 1; j <= last; ++j) sum += partial_at(a, rank, j, 0)[c];
-        char* const to = a.dtable[rank] + (token * a.dtable_stride + c) * elem_size<TDT>();
-        float x = sum * a.scale;
-        if (a.accumulate) x += widen<TDT>(load_elem<elem_size<TDT>()>(to));
-        store_elem<elem_size<TDT>(), false>(to, narrow<TDT>(x));
+    const uint64_t chunk = blockIdx.x * 4ull + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const uint64_t first = chunk * a.chunk, end = first + a.chunk;
+    if (end >= a.rows) return;
+    const uint32_t token = keys[end - 1];
+    if (token >= a.vocab || keys[end] != token || (first > 0 && keys[first - 1] == token)) return;
+    // chunks behind this one that the token reaches past: 64 ends looked at at a time
+    uint64_t whole = 0;
+    for (;;) {
+        const uint64_t at = end + (whole + lane + 1) * a.chunk;   // the first place behind that chunk
+        const uint64_t past = __ballot(at < a.rows && keys[at] == token);
+        if (past != ~0ull) {
+            whole += __builtin_ctzll(~past);
+            break;
+        }
+        whole += 64;
     }
+    const uint64_t last = chunk + 1 + whole;
+    const uint64_t c = blockIdx.y * 256ull + lane * 4;
+    float sum[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) sum[j] = c + j < a.cols ? partial_at(a, rank, chunk, 1)[c + j] : 0.0f;
+#pragma unroll 4
+    for (uint64_t k = chunk + 1; k <= last; ++k) {
+        const float* const from = partial_at(a, rank, k, 0);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) sum[j] += c + j < a.cols ? from[c + j] : 0.0f;
+    }
+    if (c < a.cols) write_row<TDT>(a, rank, token, c, 0, sum);
 }
 
 // Vectors of a row to threads of a row: all of one wavefront's or workgroup's
 // threads work on rows as short as 8 vectors.
 int row_threads(uint64_t cols, int vector) {
     const uint64_t need = (cols + vector - 1) / vector;
-    return need <= 8 ? 8 : need <= 16 ? 16 : need <= 32 ? 32 : need <= 64 ? 64 : 256;
+    return need <= 8 ? 8 : need <= 16 ? 16 : need <= 32 ? 32 : need <= 64 ? 64 : need <= 128 ? 128 : 256;
 }
 
 constexpr uint64_t kMostBlocks = 1u << 16;
@@ -465,13 +523,21 @@ hipError_t embedding_by_width(const EmbeddingArgs& a, int nranks, hipStream_t s)
         case 16: return start_embedding<DT, TDT, 16>(a, nranks, s);
         case 32: return start_embedding<DT, TDT, 32>(a, nranks, s);
         case 64: return start_embedding<DT, TDT, 64>(a, nranks, s);
+        case 128: return start_embedding<DT, TDT, 128>(a, nranks, s);
         default: return start_embedding<DT, TDT, 256>(a, nranks, s);
     }
 }
 
 hipError_t start_sort(const EmbeddingBackwardArgs& a, int nranks, hipStream_t s) {
     if (a.rows <= kSortOne) {
-        hipLaunchKernelGGL(k_sort_one, dim3(nranks), dim3(kSortThreads), 0, s, a);
+        const dim3 grid(nranks), block(kSortThreads);
+        if (a.rows <= kSortThreads) {
+            hipLaunchKernelGGL((k_sort_one<1>), grid, block, 0, s, a);
+        } else if (a.rows <= kSortThreads * 4) {
+            hipLaunchKernelGGL((k_sort_one<4>), grid, block, 0, s, a);
+        } else {
+            hipLaunchKernelGGL((k_sort_one<kSortEach>), grid, block, 0, s, a);
+        }
         return hipGetLastError();
     }
     const dim3 tiles(static_cast<unsigned>(a.tiles), nranks);
@@ -489,15 +555,16 @@ template <int DT, int TDT, int TPR>
 hipError_t start_sums(const EmbeddingBackwardArgs& a, int nranks, hipStream_t s) {
     const uint64_t sums = (a.chunks + kRowsAtOnce<TPR> - 1) / kRowsAtOnce<TPR>;
     const uint64_t zeros = a.accumulate ? 0 : (a.vocab + kZeroRows - 1) / kZeroRows;
-    const uint32_t sum_blocks = static_cast<uint32_t>(std::min(sums, kMostBlocks));
+    const uint32_t stretches = static_cast<uint32_t>((a.cols + TPR * kSumVec<DT> - 1) / (TPR * kSumVec<DT>));
+    const uint32_t sum_blocks = static_cast<uint32_t>(std::min(sums, std::max<uint64_t>(1, 4 * kMostBlocks / stretches)));
     const uint32_t zero_blocks = static_cast<uint32_t>(std::min(zeros, kMostBlocks));
     if (sum_blocks + zero_blocks == 0) return hipSuccess;
-    const dim3 grid(sum_blocks + zero_blocks, static_cast<unsigned>((a.cols + TPR * 8 - 1) / (TPR * 8)), nranks);
-    hipLaunchKernelGGL((k_embedding_sums<DT, TDT, TPR>), grid, dim3(256), 0, s, a, sum_blocks, zero_blocks);
-    hipError_t e = hipGetLastError();
+    const dim3 grid(nranks * (sum_blocks * stretches + zero_blocks));
+    hipLaunchKernelGGL((k_embedding_sums<DT, TDT, TPR>), grid, dim3(256), 0, s, a, static_cast<uint32_t>(nranks),
+                       stretches, sum_blocks, zero_blocks);
+    const hipError_t e = hipGetLastError();
     if (e != hipSuccess || a.chunks < 2) return e;
-    const dim3 joins(static_cast<unsigned>((a.chunks + kJoinChunks - 1) / kJoinChunks),
-                     static_cast<unsigned>((a.cols + 63) / 64), nranks);
+    const dim3 joins(static_cast<unsigned>((a.chunks + 3) / 4), static_cast<unsigned>((a.cols + 255) / 256), nranks);
     hipLaunchKernelGGL((k_embedding_join<TDT>), joins, dim3(256), 0, s, a);
     return hipGetLastError();
 }
@@ -508,11 +575,12 @@ hipError_t backward_by_width(const EmbeddingBackwardArgs& a, int nranks, hipStre
         const hipError_t e = start_sort(a, nranks, s);
         if (e != hipSuccess) return e;
     }
-    switch (row_threads(a.cols, 8)) {
+    switch (row_threads(a.cols, kSumVec<DT>)) {
         case 8: return start_sums<DT, TDT, 8>(a, nranks, s);
         case 16: return start_sums<DT, TDT, 16>(a, nranks, s);
         case 32: return start_sums<DT, TDT, 32>(a, nranks, s);
         case 64: return start_sums<DT, TDT, 64>(a, nranks, s);
+        case 128: return start_sums<DT, TDT, 128>(a, nranks, s);
         default: return start_sums<DT, TDT, 256>(a, nranks, s);
     }
 }

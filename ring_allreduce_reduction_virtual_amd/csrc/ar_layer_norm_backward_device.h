@@ -32,33 +32,45 @@ __device__ __forceinline__ void store_floats(float* to, const float* x) {
     }
 }
 
-// V elements of the forward pass's input: as they were, or from their codes.
-template <int DT, int V, bool PACKED>
-struct Input : Raw<DT, V> {};
+// How the forward pass's input is kept: as it was; in 8 bits, rows of whole
+// vectors (which lie within blocks); in 8 bits, rows of any width, whose last
+// vector is moved back to end with the row and may cross a block's end.
+enum Kept { kAsItWas, kPackedWhole, kPackedAny };
 
-template <int DT, int V>
-struct Input<DT, V, true> {
+// V elements of it.
+template <int DT, int V, int KEPT>
+struct Input : Raw<DT, V> {
+    __device__ __forceinline__ void ready() {}
+};
+
+template <int V, int KEPT>
+struct PackedInput {
     static constexpr int kWords = V / 4;
     uint32_t w[kWords];
-    // the scales of the block that the first element is in and of the next, and
-    // how many elements are in the first: a vector moved back to end with its row
-    // may cross a block's end
+    // the scale of the block that the first element is in and of the last one's,
+    // bytes until ready(), which comes when they are needed: a use waits for the
+    // load; and how many elements are in the first block
+    uint32_t e[2];
     float scale[2];
     int edge;
+    __device__ __forceinline__ void ready() {
+        scale[0] = activation_scale_value(e[0]);
+        if constexpr (KEPT == kPackedAny) scale[1] = activation_scale_value(e[1]);
+    }
     __device__ __forceinline__ float get(int j) const {
-        return activation_value(w[j / 4], j % 4, j < edge ? scale[0] : scale[1]);
+        return activation_value(w[j / 4], j % 4, KEPT == kPackedWhole || j < edge ? scale[0] : scale[1]);
     }
     // from element `at` of a row; WHOLE: all V elements are in it
     template <bool WHOLE>
     __device__ __forceinline__ void load(const uint8_t* codes, const uint8_t* scales, uint64_t at, uint64_t cols) {
 #pragma unroll
         for (int k = 0; k < kWords; ++k) w[k] = 0;
-        scale[0] = scale[1] = 0;
+        e[0] = e[1] = 0;
         edge = AR_ACTIVATION_BLOCK - static_cast<int>(at % AR_ACTIVATION_BLOCK);
         if (!WHOLE && at >= cols) return;
         const uint64_t last = (WHOLE || at + V <= cols ? at + V : cols) - 1;
-        scale[0] = activation_scale_value(scales[at / AR_ACTIVATION_BLOCK]);
-        scale[1] = activation_scale_value(scales[last / AR_ACTIVATION_BLOCK]);
+        e[0] = scales[at / AR_ACTIVATION_BLOCK];
+        if constexpr (KEPT == kPackedAny) e[1] = scales[last / AR_ACTIVATION_BLOCK];
         const char* const p = reinterpret_cast<const char*>(codes + at);
         if (WHOLE || at + V <= cols) {
             if constexpr (kWords == 2) {
@@ -77,14 +89,18 @@ struct Input<DT, V, true> {
         }
     }
 };
+template <int DT, int V>
+struct Input<DT, V, kPackedWhole> : PackedInput<V, kPackedWhole> {};
+template <int DT, int V>
+struct Input<DT, V, kPackedAny> : PackedInput<V, kPackedAny> {};
 
 // A row of the forward pass's input.
-template <int DT, bool PACKED>
+template <int DT, int KEPT>
 struct InputRow {
     const char* x;
     const uint8_t* scales;   // of a packed row
     __device__ __forceinline__ InputRow(const NormBackwardArgs& a, int rank, uint64_t row) {
-        if constexpr (PACKED) {
+        if constexpr (KEPT != kAsItWas) {
             x = a.x[rank] + row * a.cols;
             scales = a.scales[rank] + row * ((a.cols + AR_ACTIVATION_BLOCK - 1) / AR_ACTIVATION_BLOCK);
         } else {
@@ -94,8 +110,8 @@ struct InputRow {
     }
     // a thread's vector of a row in registers
     template <int THREADS, int V>
-    __device__ __forceinline__ void load(Input<DT, V, PACKED>& r, const RowPart<THREADS, V>& at, int cols) const {
-        if constexpr (PACKED) {
+    __device__ __forceinline__ void load(Input<DT, V, KEPT>& r, const RowPart<THREADS, V>& at, int cols) const {
+        if constexpr (KEPT != kAsItWas) {
             r.template load<(THREADS > 8)>(reinterpret_cast<const uint8_t*>(x), scales, at.at, cols);
         } else {
             at.template load<true, DT>(r, x, cols);
@@ -103,8 +119,8 @@ struct InputRow {
     }
     // V elements at c, or up to the row's end
     template <int V>
-    __device__ __forceinline__ void load(Input<DT, V, PACKED>& r, uint64_t c, uint64_t cols) const {
-        if constexpr (PACKED) {
+    __device__ __forceinline__ void load(Input<DT, V, KEPT>& r, uint64_t c, uint64_t cols) const {
+        if constexpr (KEPT != kAsItWas) {
             r.template load<false>(reinterpret_cast<const uint8_t*>(x), scales, c, cols);
         } else {
             load_at<false, false, DT, V>(r, x, c, cols);
@@ -112,7 +128,7 @@ struct InputRow {
     }
 };
 
-template <int DT, int WDT, bool PACKED, int THREADS, int NV>
+template <int DT, int WDT, int KEPT, int THREADS, int NV>
 __global__ void __launch_bounds__(block_threads(THREADS)) k_layer_norm_backward(NormBackwardArgs a, int weights) {
     constexpr int V = kRowVec<DT>;
     constexpr int EACH = NV * V;
@@ -131,7 +147,7 @@ __global__ void __launch_bounds__(block_threads(THREADS)) k_layer_norm_backward(
     const float *const mean0 = a.mean[rank], *const rstd0 = a.rstd[rank];
     // DEPTH rows on their way: the one worked on and those whose loads run beside it
     Raw<DT, V> rd[DEPTH][NV];
-    Input<DT, V, PACKED> rx[DEPTH][NV];
+    Input<DT, V, KEPT> rx[DEPTH][NV];
     float mean[DEPTH], rstd[DEPTH];
     // The ranks start at different rows: their buffers often lie a power of two
     // apart, and equal rows would meet in the same memory channels (8 ranks x
@@ -142,7 +158,7 @@ __global__ void __launch_bounds__(block_threads(THREADS)) k_layer_norm_backward(
     const auto fetch = [&](int k, uint64_t r) {
         r = real_row(r);
         const char* const dy = dy0 + r * a.dy_stride * elem_size<DT>();
-        const InputRow<DT, PACKED> x(a, rank, r);
+        const InputRow<DT, KEPT> x(a, rank, r);
 #pragma unroll
         for (int u = 0; u < NV; ++u) {
             RowPart<THREADS, V>(u, cols).template load<true>(rd[k][u], dy, cols);
@@ -177,6 +193,7 @@ __global__ void __launch_bounds__(block_threads(THREADS)) k_layer_norm_backward(
             for (int u = 0; u < NV; ++u) {
                 // no gradient, no part in any sum: only dy is cleared
                 RowPart<THREADS, V>(u, cols).clear(rd[k][u]);
+                rx[k][u].ready();
 #pragma unroll
                 for (int j = 0; j < V; ++j) {
                     const float d = rd[k][u].get(j);
@@ -199,7 +216,7 @@ __global__ void __launch_bounds__(block_threads(THREADS)) k_layer_norm_backward(
 #pragma unroll
                     for (int w = 0; w < Raw<DT, V>::kWords; ++w) asm volatile("" : "+v"(rd[k][u].w[w]));
 #pragma unroll
-                    for (int w = 0; w < Input<DT, V, PACKED>::kWords; ++w) asm volatile("" : "+v"(rx[k][u].w[w]));
+                    for (int w = 0; w < Input<DT, V, KEPT>::kWords; ++w) asm volatile("" : "+v"(rx[k][u].w[w]));
 #pragma unroll
                     for (int w = 0; w < Raw<WDT, V>::kWords; ++w) asm volatile("" : "+v"(g[u].w[w]));
                 }
@@ -280,7 +297,7 @@ __global__ void __launch_bounds__(block_threads(THREADS)) k_layer_norm_backward(
 // Rows past what registers hold: dx alone, in two passes over the row; with the
 // columns' sums below, 2^26 bf16 elements take 149 us (rows of 16,640) where rows
 // in registers take 100 (16,384).
-template <int DT, int WDT, bool PACKED>
+template <int DT, int WDT, int KEPT>
 __global__ void __launch_bounds__(1024) k_layer_norm_backward_wide(NormBackwardArgs a) {
     constexpr int V = kRowVec<DT>;
     constexpr uint64_t kStep = 1024 * V;
@@ -290,16 +307,17 @@ __global__ void __launch_bounds__(1024) k_layer_norm_backward_wide(NormBackwardA
     int turn = 0;
     for (uint64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
         const char* const dy = a.dy[rank] + row * a.dy_stride * elem_size<DT>();
-        const InputRow<DT, PACKED> x(a, rank, row);
+        const InputRow<DT, KEPT> x(a, rank, row);
         char* const dx = a.dx[rank] + row * a.dx_stride * elem_size<DT>();
         const float mean = a.mean[rank][row], rstd = a.rstd[rank][row];
         float s[2] = {0, 0};
         for (uint64_t c = threadIdx.x * V; c < a.cols; c += kStep) {
             Raw<DT, V> rd;
-            Input<DT, V, PACKED> rx;
+            Input<DT, V, KEPT> rx;
             Raw<WDT, V> g;
             load_at<false, false>(rd, dy, c, a.cols);
             x.load(rx, c, a.cols);
+            rx.ready();
             if (gamma != nullptr) load_at<false, false>(g, gamma, c, a.cols);
 #pragma unroll
             for (int j = 0; j < V; ++j) {
@@ -315,10 +333,11 @@ __global__ void __launch_bounds__(1024) k_layer_norm_backward_wide(NormBackwardA
         const float a0 = s[0] / static_cast<float>(a.cols), a1 = s[1] / static_cast<float>(a.cols);
         for (uint64_t c = threadIdx.x * V; c < a.cols; c += kStep) {
             Raw<DT, V> rd;
-            Input<DT, V, PACKED> rx;
+            Input<DT, V, KEPT> rx;
             Raw<WDT, V> g;
             load_at<false, false>(rd, dy, c, a.cols);
             x.load(rx, c, a.cols);
+            rx.ready();
             if (gamma != nullptr) load_at<false, false>(g, gamma, c, a.cols);
             float out[V];
 #pragma unroll
@@ -335,7 +354,7 @@ __global__ void __launch_bounds__(1024) k_layer_norm_backward_wide(NormBackwardA
 
 // The partial sums of such rows, before dx is written (dx may be dy): a
 // workgroup takes one vector of columns a thread and every a.blocks-th row.
-template <int DT, bool PACKED>
+template <int DT, int KEPT>
 __global__ void __launch_bounds__(kColumnThreads) k_layer_norm_columns(NormBackwardArgs a) {
     constexpr int V = kRowVec<DT>;
     const int rank = blockIdx.z;
@@ -346,9 +365,10 @@ __global__ void __launch_bounds__(kColumnThreads) k_layer_norm_columns(NormBackw
     for (int j = 0; j < V; ++j) dg[j] = db[j] = 0;
     for (uint64_t row = blockIdx.y; row < a.rows; row += a.blocks) {
         Raw<DT, V> rd;
-        Input<DT, V, PACKED> rx;
+        Input<DT, V, KEPT> rx;
         load_at<false, false>(rd, a.dy[rank] + row * a.dy_stride * elem_size<DT>(), c, a.cols);
-        InputRow<DT, PACKED>(a, rank, row).load(rx, c, a.cols);
+        InputRow<DT, KEPT>(a, rank, row).load(rx, c, a.cols);
+        rx.ready();
         const float mean = a.mean[rank][row], rstd = a.rstd[rank][row];
 #pragma unroll
         for (int j = 0; j < V; ++j) {
@@ -394,50 +414,50 @@ __global__ void __launch_bounds__(1024) k_layer_norm_weight_sums(NormBackwardArg
 
 constexpr uint64_t kMostBlocks = 1u << 18;
 
-template <int DT, int WDT, bool PACKED, int THREADS, int NV>
+template <int DT, int WDT, int KEPT, int THREADS, int NV>
 hipError_t start(const NormBackwardArgs& a, int nranks, bool weights, hipStream_t s) {
     const dim3 block(block_threads(THREADS));
     if constexpr (NV == 0) {
         if (weights) {
             const dim3 columns(static_cast<unsigned>(column_stretches(a.cols, kRowVec<DT>)), a.blocks, nranks);
-            hipLaunchKernelGGL((k_layer_norm_columns<DT, PACKED>), columns, dim3(kColumnThreads), 0, s, a);
+            hipLaunchKernelGGL((k_layer_norm_columns<DT, KEPT>), columns, dim3(kColumnThreads), 0, s, a);
             const hipError_t e = hipGetLastError();
             if (e != hipSuccess) return e;
         }
         const dim3 grid(static_cast<unsigned>(std::min<uint64_t>(a.rows, kMostBlocks)), nranks);
-        hipLaunchKernelGGL((k_layer_norm_backward_wide<DT, WDT, PACKED>), grid, block, 0, s, a);
+        hipLaunchKernelGGL((k_layer_norm_backward_wide<DT, WDT, KEPT>), grid, block, 0, s, a);
     } else {
         const dim3 grid(a.blocks, nranks);
-        hipLaunchKernelGGL((k_layer_norm_backward<DT, WDT, PACKED, THREADS, NV>), grid, block, 0, s, a, weights ? 1 : 0);
+        hipLaunchKernelGGL((k_layer_norm_backward<DT, WDT, KEPT, THREADS, NV>), grid, block, 0, s, a, weights ? 1 : 0);
     }
     return hipGetLastError();
 }
 
-template <int DT, int WDT, bool PACKED>
+template <int DT, int WDT, int KEPT>
 hipError_t rows_by_shape(const NormBackwardArgs& a, int nranks, bool weights, hipStream_t s) {
     const RowShape w = backward_shape(a.cols, kRowVec<DT>);
     switch (w.threads * 16 + w.vectors) {
-        case 8 * 16 + 1: return start<DT, WDT, PACKED, 8, 1>(a, nranks, weights, s);
-        case 16 * 16 + 1: return start<DT, WDT, PACKED, 16, 1>(a, nranks, weights, s);
-        case 32 * 16 + 1: return start<DT, WDT, PACKED, 32, 1>(a, nranks, weights, s);
-        case 64 * 16 + 1: return start<DT, WDT, PACKED, 64, 1>(a, nranks, weights, s);
-        case 128 * 16 + 1: return start<DT, WDT, PACKED, 128, 1>(a, nranks, weights, s);
-        case 256 * 16 + 1: return start<DT, WDT, PACKED, 256, 1>(a, nranks, weights, s);
-        case 256 * 16 + 2: return start<DT, WDT, PACKED, 256, 2>(a, nranks, weights, s);
-        case 512 * 16 + 2: return start<DT, WDT, PACKED, 512, 2>(a, nranks, weights, s);
-        case 512 * 16 + 4: return start<DT, WDT, PACKED, 512, 4>(a, nranks, weights, s);
+        case 8 * 16 + 1: return start<DT, WDT, KEPT, 8, 1>(a, nranks, weights, s);
+        case 16 * 16 + 1: return start<DT, WDT, KEPT, 16, 1>(a, nranks, weights, s);
+        case 32 * 16 + 1: return start<DT, WDT, KEPT, 32, 1>(a, nranks, weights, s);
+        case 64 * 16 + 1: return start<DT, WDT, KEPT, 64, 1>(a, nranks, weights, s);
+        case 128 * 16 + 1: return start<DT, WDT, KEPT, 128, 1>(a, nranks, weights, s);
+        case 256 * 16 + 1: return start<DT, WDT, KEPT, 256, 1>(a, nranks, weights, s);
+        case 256 * 16 + 2: return start<DT, WDT, KEPT, 256, 2>(a, nranks, weights, s);
+        case 512 * 16 + 2: return start<DT, WDT, KEPT, 512, 2>(a, nranks, weights, s);
+        case 512 * 16 + 4: return start<DT, WDT, KEPT, 512, 4>(a, nranks, weights, s);
         case 512 * 16 + 8:
-            if constexpr (DT == AR_FLOAT32) return start<DT, WDT, PACKED, 512, 8>(a, nranks, weights, s);
+            if constexpr (DT == AR_FLOAT32) return start<DT, WDT, KEPT, 512, 8>(a, nranks, weights, s);
             return hipErrorInvalidValue;
-        case 1024 * 16: return start<DT, WDT, PACKED, 1024, 0>(a, nranks, weights, s);
+        case 1024 * 16: return start<DT, WDT, KEPT, 1024, 0>(a, nranks, weights, s);
         default: return hipErrorInvalidValue;
     }
 }
 
-template <int DT, int WDT, bool PACKED>
+template <int DT, int WDT, int KEPT>
 hipError_t by_shape(const NormBackwardArgs& a, int nranks, bool weights, hipStream_t s) {
     if (a.rows > 0) {   // else nothing but zeros to write below
-        const hipError_t e = rows_by_shape<DT, WDT, PACKED>(a, nranks, weights, s);
+        const hipError_t e = rows_by_shape<DT, WDT, KEPT>(a, nranks, weights, s);
         if (e != hipSuccess) return e;
     }
     if (!weights) return hipSuccess;
@@ -446,17 +466,17 @@ hipError_t by_shape(const NormBackwardArgs& a, int nranks, bool weights, hipStre
     return hipGetLastError();
 }
 
-template <bool PACKED>
+template <int KEPT>
 hipError_t launch_backward(const NormBackwardArgs& a, int nranks, bool weights, ar_dtype_t dtype, ar_dtype_t weight,
                            hipStream_t s) {
     switch (dtype) {
-        case AR_FLOAT32: return by_shape<AR_FLOAT32, AR_FLOAT32, PACKED>(a, nranks, weights, s);
+        case AR_FLOAT32: return by_shape<AR_FLOAT32, AR_FLOAT32, KEPT>(a, nranks, weights, s);
         case AR_BFLOAT16:
-            return weight == AR_FLOAT32 ? by_shape<AR_BFLOAT16, AR_FLOAT32, PACKED>(a, nranks, weights, s)
-                                        : by_shape<AR_BFLOAT16, AR_BFLOAT16, PACKED>(a, nranks, weights, s);
+            return weight == AR_FLOAT32 ? by_shape<AR_BFLOAT16, AR_FLOAT32, KEPT>(a, nranks, weights, s)
+                                        : by_shape<AR_BFLOAT16, AR_BFLOAT16, KEPT>(a, nranks, weights, s);
         case AR_FLOAT16:
-            return weight == AR_FLOAT32 ? by_shape<AR_FLOAT16, AR_FLOAT32, PACKED>(a, nranks, weights, s)
-                                        : by_shape<AR_FLOAT16, AR_FLOAT16, PACKED>(a, nranks, weights, s);
+            return weight == AR_FLOAT32 ? by_shape<AR_FLOAT16, AR_FLOAT32, KEPT>(a, nranks, weights, s)
+                                        : by_shape<AR_FLOAT16, AR_FLOAT16, KEPT>(a, nranks, weights, s);
         default: return hipErrorInvalidValue;
     }
 }

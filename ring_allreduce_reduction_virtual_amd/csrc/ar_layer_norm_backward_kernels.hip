@@ -7,7 +7,7 @@ namespace arimpl {
 
 hipError_t launch_norm_backward(const NormBackwardArgs& a, int nranks, bool weights, ar_dtype_t dtype,
                                 ar_dtype_t weight, hipStream_t s) {
-    return launch_backward<false>(a, nranks, weights, dtype, weight, s);
+    return launch_backward<kAsItWas>(a, nranks, weights, dtype, weight, s);
 }
 
 }  // namespace arimpl

@@ -7,7 +7,10 @@ namespace arimpl {
 
 hipError_t launch_norm_backward_packed(const NormBackwardArgs& a, int nranks, bool weights, ar_dtype_t dtype,
                                        ar_dtype_t weight, hipStream_t s) {
-    return launch_backward<true>(a, nranks, weights, dtype, weight, s);
+    // whole vectors: 16 bytes of dy and dx
+    return a.cols % (dtype == AR_FLOAT32 ? 4 : 8) == 0
+               ? launch_backward<kPackedWhole>(a, nranks, weights, dtype, weight, s)
+               : launch_backward<kPackedAny>(a, nranks, weights, dtype, weight, s);
 }
 
 }  // namespace arimpl
