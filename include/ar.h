@@ -759,8 +759,9 @@ ar_result_t ar_cross_entropy(const void* const* x, const void* const* weight, co
  *   dx = dz W,  dweight = dz^T x.
  * dx[r] has rows dx_stride apart, dweight[r] dweight_stride; either array may
  * be NULL.  dz is rounded to dtype before the two products, as their operands
- * have to be (binary16: after scaling by a power of two that brings the
- * largest |g| near 2^14, so that small gradients do not underflow), and the
+ * have to be: a 16-bit one relative to the largest |g| of the rank's rows, so
+ * that rows that count alike lose nothing by the rounding of g, and binary16
+ * (which then has 2^13 for the largest) keeps the small ones.  The
  * sums are float32, rounded once.  Rows that are ignored, or whose g is 0,
  * take no part whatever x holds there: their dx is 0.  A target outside
  * [0, vocab) that is not ignored makes its row of dx, and dweight, NaN.

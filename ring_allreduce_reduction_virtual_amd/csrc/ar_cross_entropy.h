@@ -116,7 +116,7 @@ struct CrossArgs {
     uint32_t tiles;       // of the vocabulary
     uint32_t* live_count; // backward: [1]
     uint32_t* place;      // backward: [row]: its place among the live rows, or ~0
-    float* unscale;       // backward: [1]: undoes binary16's scaling
+    float* unscale;       // backward: [1]: undoes the scaling of 16-bit dz
     LiveRow* live;        // backward: [row]
     char* x_live;         // backward: [row][padded cols]: the live rows of x
     char* dz;             // backward: [row][piece]

@@ -14,16 +14,22 @@ using namespace arimpl;
 namespace {
 
 constexpr uint64_t kMaxTokens = (1ull << 31) - 1, kMaxVocab = (1ull << 31) - 1, kMaxWidth = 1ull << 20;
-// Tiles of one launch: its threads are 32-bit numbers.
-constexpr uint64_t kMaxTiles = 1ull << 22;
+// Large tiles of one launch, whose threads are counted with 32 bits.
+constexpr uint64_t kMaxTiles = 1ull << 21;
+uint64_t large_tiles(uint64_t m, uint64_t n, uint64_t batch) { return tiles_in(m, n, CrossTile::kLarge) * batch; }
 
 ar_result_t check_sizes(size_t rows, size_t vocab, size_t cols, ar_dtype_t dtype, int nranks) {
     const ar_result_t rc = check_types(dtype, dtype, "same", nranks);
     if (rc != AR_SUCCESS) return rc;
     if (vocab == 0) return fail_with(AR_ERR_INVALID_ARGUMENT, "a vocabulary of 0");
-    if (rows > kMaxTokens || vocab > kMaxVocab || cols > kMaxWidth ||
-        (rows + 255) / 256 * ((std::max(vocab, cols) + 127) / 128) * std::min(nranks, kCrossRanks) > kMaxTiles ||
-        (vocab + 255) / 256 * ((cols + 127) / 128) * std::min(nranks, kCrossRanks) > kMaxTiles)
+    bool fits = rows <= kMaxTokens && vocab <= kMaxVocab && cols <= kMaxWidth;
+    if (fits) {   // the backward pass's launches; the forward pass's are cut to fit
+        const int n = std::min(nranks, kCrossRanks);
+        const uint64_t es = float_size(dtype), piece = piece_of(rows, vocab, es, n);
+        fits = large_tiles(piece, rows, n) <= kMaxTiles && large_tiles(piece, cols, n) <= kMaxTiles &&
+               large_tiles(cols, rows, n * dx_shape(rows, cols, piece, es, n).splits) <= kMaxTiles;
+    }
+    if (!fits)
         return fail_with(AR_ERR_INVALID_ARGUMENT, "%llu rows of %llu columns against a vocabulary of %llu are too large",
                          static_cast<unsigned long long>(rows), static_cast<unsigned long long>(cols),
                          static_cast<unsigned long long>(vocab));
@@ -173,10 +179,11 @@ ar_result_t ar_cross_entropy(const void* const* x, const void* const* weight, co
                 rc = align(x + g, n, 0, rows, cols, x_stride, at.padded, dtype, ws + at.x, a.x, stream);
                 if (rc != AR_SUCCESS) return rc;
             }
-            // a weight that needs no copy is one piece
+            // a weight that needs no copy is one piece, as far as one launch goes
             const bool as_is = aligned(weight + g, n, weight_stride, cols, es);
+            const uint64_t most = kMaxTiles / large_tiles(1, rows, n) * kVocabTile;
             for (uint64_t first = 0; first < vocab;) {
-                const uint64_t count = std::min<uint64_t>(vocab - first, as_is ? vocab : at.piece);
+                const uint64_t count = std::min<uint64_t>(vocab - first, as_is ? most : at.piece);
                 rc = set_piece(a, at, ws, weight + g, n, first, count, weight_stride, as_is, dtype, stream);
                 if (rc == AR_SUCCESS)
                     rc = hip_result(launch_cross_stats(a, n, at.tile, dtype, stream), "cross_entropy launch");

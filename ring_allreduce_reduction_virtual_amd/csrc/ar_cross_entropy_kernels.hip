@@ -139,8 +139,10 @@ __global__ void __launch_bounds__(256) k_cross_loss(CrossArgs a) {
     float top = -INFINITY, s = 0;
     if (row < a.rows) {
         const float* const from = a.partials + (static_cast<uint64_t>(rank) * a.tiles * a.rows + row) * 2;
+#pragma unroll 8
         for (uint32_t t = part; t < a.tiles; t += 16) {
-            const float x = from[t * a.rows * 2], y = from[t * a.rows * 2 + 1];
+            const float2 each = *reinterpret_cast<const float2*>(from + t * a.rows * 2);
+            const float x = each.x, y = each.y;
             const float higher = fmaxf(top, x), base = higher == -INFINITY ? 0.0f : higher;
             s = s * __builtin_amdgcn_exp2f((top - base) * kLog2e) + y * __builtin_amdgcn_exp2f((x - base) * kLog2e);
             top = higher;
@@ -177,7 +179,9 @@ __global__ void __launch_bounds__(256) k_align(AlignArgs a) {
     const uint64_t each = a.to_stride / V, all = a.count * each;
     char* const to = a.to + static_cast<uint64_t>(blockIdx.y) * a.count * a.to_stride * elem_size<DT>();
     for (uint64_t i = blockIdx.x * 256ull + threadIdx.x; i < all; i += gridDim.x * 256ull) {
-        const uint64_t row = i / each, c = i % each * V;
+        // 32-bit division where it will do: it takes a fraction of the 64-bit one
+        const uint64_t row = all >> 32 ? i / each : static_cast<uint32_t>(i) / static_cast<uint32_t>(each);
+        const uint64_t c = (i - row * each) * V;
         Raw<DT, V> r;
         load_at<false, false>(r, a.from[blockIdx.y] + row * a.from_stride * elem_size<DT>(), c, a.cols);
         r.template store<false>(to + (row * a.to_stride + c) * elem_size<DT>());
@@ -189,16 +193,18 @@ __global__ void __launch_bounds__(256) k_align(AlignArgs a) {
 // ---------------------------------------------------------------------------
 
 // The rows that take part, in order, with their g: one workgroup a rank.
-__global__ void __launch_bounds__(1024) k_cross_live(CrossArgs a, int scaled) {
+__global__ void __launch_bounds__(1024) k_cross_live(CrossArgs a, float span) {
     __shared__ uint32_t counts[2][16];
     __shared__ float tops[16];
     const int rank = blockIdx.x, wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
     const auto weight = [&](uint64_t row) {
         return a.dloss[rank] != nullptr ? a.scale * a.dloss[rank][row] : a.scale;
     };
-    float up = 1.0f;
-    if (scaled) {
-        // the largest finite |g| of all rows goes to [2^13, 2^14)
+    // The g of a 16-bit dz are relative to the largest finite |g|, which becomes
+    // `span`: rows that count alike lose nothing by g's own rounding, and binary16
+    // keeps small ones.  span 0 (float32): g as it is.
+    float largest = 1.0f;
+    if (span > 0) {
         float top = 0;
         for (uint64_t row = threadIdx.x; row < a.rows; row += 1024) {
             const float g = fabsf(weight(row));
@@ -208,14 +214,9 @@ __global__ void __launch_bounds__(1024) k_cross_live(CrossArgs a, int scaled) {
         if (lane == 0) tops[wave] = top;
         __syncthreads();
         for (int w = 0; w < 16; ++w) top = fmaxf(top, tops[w]);
-        int e = 0;
-        if (top > 0) {
-            (void)frexpf(top, &e);
-            e = std::max(-126, std::min(126, 14 - e));
-        }
-        up = __builtin_amdgcn_ldexpf(1.0f, e);
+        if (top > 0) largest = top;
     }
-    if (threadIdx.x == 0) a.unscale[rank] = 1.0f / up;
+    if (threadIdx.x == 0) a.unscale[rank] = span > 0 ? largest / span : 1.0f;
     uint32_t before = 0;
     int turn = 0;
     for (uint64_t first = 0; first < a.rows; first += 1024) {
@@ -228,7 +229,8 @@ __global__ void __launch_bounds__(1024) k_cross_live(CrossArgs a, int scaled) {
             live = t != a.ignore && r.g != 0;
             const bool known = t >= 0 && static_cast<uint64_t>(t) < a.vocab;
             r.target = known ? t : -1;
-            r.g = known ? r.g * up : as_f(0x7fc00000u);
+            if (span > 0) r.g = r.g / largest * span;
+            if (!known) r.g = as_f(0x7fc00000u);
             r.lse = a.lse_in[rank][row];
         }
         const uint64_t mask = __ballot(live);
@@ -406,6 +408,10 @@ __global__ void __launch_bounds__(256) k_cross_finish(CrossArgs a) {
 
 constexpr uint64_t kMostBlocks = 1u << 16;
 
+// A launch's threads are counted with 32 bits (the host has checked sizes for
+// large tiles, which these sizes get).
+bool fits_launch(uint64_t blocks, int threads) { return blocks * threads <= 0xffffffffull; }
+
 uint32_t tiles_of(uint64_t n, int tile) { return static_cast<uint32_t>((n + tile - 1) / tile); }
 
 template <class Tile>
@@ -421,6 +427,7 @@ template <int DT, class Tile>
 hipError_t start_stats(const CrossArgs& a, int nranks, hipStream_t s) {
     const uint32_t tiles_m = tiles_of(a.count, Tile::EM), tiles_n = tiles_of(a.rows, Tile::EN);
     const uint64_t blocks = tile_blocks(static_cast<uint64_t>(tiles_m) * tiles_n * nranks);
+    if (!fits_launch(blocks, Tile::kThreads)) return hipErrorInvalidValue;
     hipLaunchKernelGGL((k_cross_stats<DT, Tile>), dim3(static_cast<unsigned>(blocks)), dim3(Tile::kThreads), 0, s, a,
                        tiles_m, tiles_n, static_cast<uint32_t>(nranks));
     return hipGetLastError();
@@ -428,7 +435,8 @@ hipError_t start_stats(const CrossArgs& a, int nranks, hipStream_t s) {
 
 template <int DT>
 hipError_t start_live(const CrossArgs& a, int nranks, hipStream_t s) {
-    hipLaunchKernelGGL(k_cross_live, dim3(nranks), dim3(1024), 0, s, a, DT == AR_FLOAT16 ? 1 : 0);
+    hipLaunchKernelGGL(k_cross_live, dim3(nranks), dim3(1024), 0, s, a,
+                       DT == AR_FLOAT16 ? 8192.0f : DT == AR_BFLOAT16 ? 1.0f : 0.0f);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess || a.rows == 0) return e;
     const dim3 grid(static_cast<unsigned>(std::min(a.rows, kMostBlocks)), nranks);
@@ -440,6 +448,7 @@ template <int DT, class Tile>
 hipError_t start_dz(const CrossArgs& a, int nranks, hipStream_t s) {
     const uint32_t tiles_m = tiles_of(a.piece, Tile::EM), tiles_n = tiles_of(a.rows, Tile::EN);
     const uint64_t blocks = tile_blocks(static_cast<uint64_t>(tiles_m) * tiles_n * nranks);
+    if (!fits_launch(blocks, Tile::kThreads)) return hipErrorInvalidValue;
     hipLaunchKernelGGL((k_cross_dz<DT, Tile>), dim3(static_cast<unsigned>(blocks)), dim3(Tile::kThreads), 0, s, a,
                        padded_cols(a.cols, elem_size<DT>()), tiles_m, tiles_n, static_cast<uint32_t>(nranks));
     return hipGetLastError();
@@ -449,6 +458,7 @@ template <int DT, class Tile>
 hipError_t start_dx(const CrossArgs& a, int nranks, bool add, hipStream_t s) {
     const uint32_t tiles_m = tiles_of(a.cols, Tile::EM), tiles_n = tiles_of(a.rows, Tile::EN);
     const uint64_t blocks = tile_blocks(static_cast<uint64_t>(tiles_m) * tiles_n * nranks * a.splits);
+    if (!fits_launch(blocks, Tile::kThreads)) return hipErrorInvalidValue;
     hipLaunchKernelGGL((k_cross_dx<DT, Tile>), dim3(static_cast<unsigned>(blocks)), dim3(Tile::kThreads), 0, s, a,
                        add ? 1 : 0, tiles_m, tiles_n, static_cast<uint32_t>(nranks));
     return hipGetLastError();
@@ -458,6 +468,7 @@ template <int DT, class Tile>
 hipError_t start_dweight(const CrossArgs& a, int nranks, hipStream_t s) {
     const uint32_t tiles_m = tiles_of(a.cols, Tile::EM), tiles_n = tiles_of(a.count, Tile::EN);
     const uint64_t blocks = tile_blocks(static_cast<uint64_t>(tiles_m) * tiles_n * nranks);
+    if (!fits_launch(blocks, Tile::kThreads)) return hipErrorInvalidValue;
     hipLaunchKernelGGL((k_cross_dweight<DT, Tile>), dim3(static_cast<unsigned>(blocks)), dim3(Tile::kThreads), 0, s, a,
                        padded_cols(a.cols, elem_size<DT>()), tiles_m, tiles_n, static_cast<uint32_t>(nranks));
     return hipGetLastError();

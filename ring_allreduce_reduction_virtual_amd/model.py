@@ -16,7 +16,7 @@ import torch
 
 from . import _lib
 from .binding import _on_device, _stream_handle, _ws
-from .step import (_dtype_of, _empty, _first, _FLOATS, _new_parts, _norm_backward, _pointers, _rank_list,
+from .step import (_array, _dtype_of, _fast, _first, _FLOATS, _new_parts, _norm_backward, _pointers, _rank_list,
                    _row_pointers, _scratch, _written)
 
 _INDICES = {torch.int32: "i32", torch.int64: "i64"}
@@ -255,6 +255,10 @@ def _packed_rows(packed, n, dev, index, rows, cols, what):
     got = []
     for k, (part, dt, width) in enumerate((("codes", torch.int8, cols), ("scales", torch.uint8, blocks))):
         tensors = [p[k] for p in packed]
+        fast = _fast and _fast.rows(tensors, dt, index, rows, width)
+        if fast is not None and fast[1] == width:
+            got.append(_array(fast[0]))
+            continue
         got.append(_pointers(tensors, dev, index, dt, [rows * width] * n, f"the {part} of {what}"))
         if any(t.shape != (rows, width) for t in tensors):
             raise ValueError(f"the {part} of {what} must be [{rows}, {width}] tensors")

@@ -92,8 +92,9 @@ def check_forward(ar, xs, weights, targets, **k):
 
 def check_backward(ar, xs, weights, targets, lses, dlosses, dtype, scale=1.0, pad=0, offset=0, **k):
     """dz: p's relative error is that of its exponent (the logit's error, lse is given; the difference's roundings)
-    and 3 roundings, then the rounding to the type; dx and dweight: sums of at most k terms of float32 products,
-    twice (pieces and splits are added up), the power of two is exact, one rounding."""
+    and 4 roundings (g relative to the largest is a quotient), then the rounding to the type; dx and dweight: sums of
+    at most k terms of float32 products, twice (pieces and splits are added up), the product with the largest g, one
+    rounding."""
     torch = _torch()
     n, (rows, cols), vocab = len(xs), xs[0].shape, weights[0].shape[0]
     dxs = rows_of(np.random.default_rng(0), n, rows, cols, dtype, pad, offset=offset)
@@ -112,13 +113,13 @@ def check_backward(ar, xs, weights, targets, lses, dlosses, dtype, scale=1.0, pa
         p = np.where(live[:, None], np.exp(z - lse[:, None]), 0)
         arg = np.abs(z - lse[:, None])
         p_off = p * 1.01 * (logit_error(x, w) + 3 * U32 * arg + 2 * U32 + EXP) + 2.0 ** -126
-        # binary16's dz is scaled to below 2^14: its subnormals' step relative to the largest |g|
+        # binary16's dz has 2^13 for the largest |g|: its subnormals' step relative to that
         floor = np.abs(g[live]).max(initial=0) * 2.0 ** -13 * TINY["f16"] if dtype == "f16" else TINY[dtype]
-        dz_off = np.abs(g)[:, None] * (p_off + 3 * U32 * (p + 1)) + 2 * U32 * np.abs(dz)
+        dz_off = np.abs(g)[:, None] * (p_off + 3 * U32 * (p + 1)) + 4 * U32 * np.abs(dz)
         dz_off = np.where(live[:, None], dz_off + (0 if dtype == "f32" else UNIT[dtype] * (np.abs(dz) + dz_off) + floor), 0)
         for got, want, left, right, depth in ((dxs[r], want_dx, (np.abs(dz), dz_off), np.abs(w), vocab),
                                               (dws[r], want_dw, (np.abs(dz).T, dz_off.T), np.abs(x), rows)):
-            off = left[1] @ right * 1.01 + 2 * (depth + 2) * U32 * ((left[0] + left[1]) @ right)
+            off = left[1] @ right * 1.01 + (2 * (depth + 2) + 2) * U32 * ((left[0] + left[1]) @ right)
             away = np.abs(f64(got) - want)
             bad = away - off - rounded(np.abs(want) + off, dtype)
             assert (bad <= 0).all(), (got.shape, float(bad.max()), np.argwhere(~(bad <= 0))[:5])
