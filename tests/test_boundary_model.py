@@ -227,14 +227,14 @@ def test_cross_entropy_errors(lib):
 @pytest.mark.parametrize("rows,vocab,cols", [(1, 1, 1), (16, 8192, 1024), (129, 5003, 515), (8192, 65536, 4096),
                                              (4096, 131072, 8192), (131072, 50257, 768), (3, 1 << 22, 64)])
 def test_cross_entropy_workspaces(lib, dt, rows, vocab, cols):
-    """The backward pass never needs memory for the logits: a piece of them, at most a quarter of a GiB or 2,048
+    """The backward pass never needs memory for the logits: a piece of them, at most half a GiB or 2,048
     columns, beside copies and float32 sums of x's size."""
     es = 4 if dt == F32 else 2
     for n in (1, 4, 33):
         ranks = min(n, 32)
         forward = lib.ar_cross_entropy_workspace_bytes(rows, vocab, cols, dt, n, 0)
         back = lib.ar_cross_entropy_workspace_bytes(rows, vocab, cols, dt, n, 1)
-        piece = max(256 << 20, ranks * rows * 2048 * es)
+        piece = max(512 << 20, ranks * rows * 2048 * es)
         width = cols + 8
         # x's copy, a piece of the weight's (no wider than the vocabulary or dz's bound), and 64 splits of dx at most
         copies = ranks * (rows + min(vocab + 256, piece // (ranks * rows * es) + 256)) * width * es
