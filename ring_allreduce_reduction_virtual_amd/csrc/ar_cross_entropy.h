@@ -54,16 +54,18 @@ constexpr uint64_t tile_n(CrossTile t) {
 // Measured on MI355X, TFLOP/s, tiny / small / medium / large: bf16, 2 x 4,096
 // rows of 4,096 against 65,536, forward 445 / 787 / 1,043 / 1,406, backward (6
 // per logit and column) 308 / 739 / 993 / 1,297; float32, 2 x 4,096 rows of
-// 2,048 against 32,768, forward 91 / 131 / 141 / 145, backward 89 / 129 / 138 /
-// 142.  Where the large tile leaves compute units without work the others are
-// ahead: bf16, 512 rows of 1,024 against 8,192, forward 33 / 19 / 16 / 28 us;
-// 16 rows of 4,096 against 65,536 133 / 127 / 146 / 155.
+// 2,048 against 32,768, forward (91 with two wavefronts) / 131 / 141 / 145.
+// Where the large tile leaves compute units without work the others are ahead:
+// bf16, 512 rows of 1,024 against 8,192, forward 33 / 19 / 16 / 28 us; 16 rows
+// of 4,096 against 65,536 133 / 127 / 146 / 155; float32, 3 x 129 rows of 515
+// against 5,003, forward and backward 56 + 142 (tiny and small), 62 + 165 with
+// the tiny tile rated at 0.6, 152 + 337 with the large tile alone.
 inline double tile_rate(CrossTile t, bool wide) {
     switch (t) {
         case CrossTile::kLarge: return 1.0;
         case CrossTile::kMedium: return wide ? 0.97 : 0.75;
         case CrossTile::kSmall: return wide ? 0.9 : 0.56;
-        default: return wide ? 0.6 : 0.3;
+        default: return wide ? 0.8 : 0.3;
     }
 }
 inline uint64_t tiles_in(uint64_t m, uint64_t n, CrossTile t) {

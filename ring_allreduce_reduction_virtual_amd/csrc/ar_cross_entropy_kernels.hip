@@ -35,7 +35,7 @@ __device__ __forceinline__ int64_t index_at(const char* p, uint64_t i, int wide)
 typedef TileOf<256, 256, 2, 4, 128, 2> LargeTile;
 typedef TileOf<128, 128, 4, 2, 128, 2> MediumTile;
 typedef TileOf<128, 64, 4, 1, 128, 3> SmallTile;
-typedef TileOf<64, 32, 2, 1, 128, 4> TinyTile;
+typedef TileOf<64, 32, 2, 2, 128, 4> TinyTile;
 
 // ---------------------------------------------------------------------------
 // forward

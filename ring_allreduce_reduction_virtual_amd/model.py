@@ -17,7 +17,7 @@ import torch
 from . import _lib
 from .binding import _on_device, _stream_handle, _ws
 from .step import (_array, _dtype_of, _fast, _first, _FLOATS, _new_parts, _norm_backward, _pointers, _rank_list,
-                   _row_pointers, _scratch, _written)
+                   _row_pointers, _scratch, _second_half, _written)
 
 _INDICES = {torch.int32: "i32", torch.int64: "i64"}
 
@@ -144,6 +144,12 @@ def ar_cross_entropy_workspace_bytes(rows: int, vocab: int, cols: int, dtype: st
     return v
 
 
+def _flat_floats(tensors, n, dev, index, rows, what):
+    """Addresses of one float32 tensor of `rows` elements per rank."""
+    _per_rank(tensors, n, what)
+    return _pointers(tensors, dev, index, torch.float32, [rows] * n, what)
+
+
 def _cross_inputs(xs, weights, targets):
     """What both passes read: (first x, dev, index, (rows, vocab, cols), addresses, strides, index type)."""
     x0 = _rank_list(xs, "xs")
@@ -174,14 +180,13 @@ def ar_cross_entropy(xs, weights, targets, losses=None, lses=None, ignore_index:
     rows = shape[0]
     name = _FLOATS[x0.dtype]
     given = (losses, lses)
-    got = []
-    for outs, what in ((losses, "losses"), (lses, "lses")):
-        if outs is None:
-            got.append(_new_parts((n, rows), torch.float32, dev, stream))
-        else:
-            _per_rank(outs, n, what)
-            got.append((outs, _pointers(outs, dev, index, torch.float32, [rows] * n, what)))
-    (losses, lp), (lses, sp) = got
+    if losses is None and lses is None:
+        both, lp = _new_parts((2 * n, rows), torch.float32, dev, stream)
+        losses, lses, sp = both[:n], both[n:], _second_half(lp, n)
+    else:
+        made = [None, None] if all(g is not None for g in given) else _new_parts((n, rows), torch.float32, dev, stream)
+        losses, lp = made if losses is None else (losses, _flat_floats(losses, n, dev, index, rows, "losses"))
+        lses, sp = made if lses is None else (lses, _flat_floats(lses, n, dev, index, rows, "lses"))
     with _on_device(dev):
         workspace = _scratch(ar_cross_entropy_workspace_bytes(*shape, name, n), workspace, dev, stream)
         wp, wb = _ws(workspace, dev)
@@ -205,12 +210,8 @@ def ar_cross_entropy_backward(dlosses, xs, weights, targets, lses, dxs=None, dwe
     x0, n, dev, index, shape, inputs, strides, index_type = _cross_inputs(xs, weights, targets)
     rows, vocab, cols = shape
     dt, name = x0.dtype, _FLOATS[x0.dtype]
-    _per_rank(lses, n, "lses")
-    sp = _pointers(lses, dev, index, torch.float32, [rows] * n, "lses")
-    dp = None
-    if dlosses is not None:
-        _per_rank(dlosses, n, "dlosses")
-        dp = _pointers(dlosses, dev, index, torch.float32, [rows] * n, "dlosses")
+    sp = _flat_floats(lses, n, dev, index, rows, "lses")
+    dp = None if dlosses is None else _flat_floats(dlosses, n, dev, index, rows, "dlosses")
     given = (dxs, dweights)
     gx = gw = None
     x_stride = w_stride = cols
