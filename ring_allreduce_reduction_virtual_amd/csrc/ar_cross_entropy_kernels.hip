@@ -269,14 +269,13 @@ __global__ void __launch_bounds__(256) k_cross_gather(CrossArgs a, uint64_t padd
 // dz of a piece's columns: [live row][piece], zeros behind the vocabulary's end.
 template <int DT, class Tile>
 __global__ void __launch_bounds__(Tile::kThreads) k_cross_dz(CrossArgs a, uint64_t padded, uint32_t tiles_m,
-                                                             uint32_t tiles_n, uint32_t ranks) {
+                                                             uint32_t ranks) {
     __shared__ __attribute__((aligned(1024))) char buffers[Tile::kShared];
-    const TilePlace tile(blockIdx.x, tiles_m, tiles_n, ranks);
+    const TilePlace tile(blockIdx.x, tiles_m, a.live_count, Tile::EN, 1, ranks);
     if (!tile.valid) return;
     constexpr int kEs = elem_size<DT>();
     const uint64_t live = a.live_count[tile.rank];
     const uint64_t m0 = static_cast<uint64_t>(tile.m) * Tile::EM, n0 = static_cast<uint64_t>(tile.n) * Tile::EN;
-    if (n0 >= live) return;
     f32x4 sum[Tile::TM][Tile::TN];
     // a tile past the vocabulary's end (the piece is padded) has its last row for all
     product<DT, Tile, true, true>(buffers, a.weight[tile.rank], a.weight_stride * kEs, m0, a.count,
@@ -309,16 +308,14 @@ __global__ void __launch_bounds__(Tile::kThreads) k_cross_dz(CrossArgs a, uint64
 
 // A piece's part of dx's sums: [split][live row][column].
 template <int DT, class Tile>
-__global__ void __launch_bounds__(Tile::kThreads) k_cross_dx(CrossArgs a, int add, uint32_t tiles_m, uint32_t tiles_n,
-                                                             uint32_t ranks) {
+__global__ void __launch_bounds__(Tile::kThreads) k_cross_dx(CrossArgs a, int add, uint32_t tiles_m, uint32_t ranks) {
     __shared__ __attribute__((aligned(1024))) char buffers[Tile::kShared];
-    const TilePlace tile(blockIdx.x, tiles_m, tiles_n, ranks * a.splits);
+    const TilePlace tile(blockIdx.x, tiles_m, a.live_count, Tile::EN, a.splits, ranks);
     if (!tile.valid) return;
     constexpr int kEs = elem_size<DT>();
-    const uint32_t rank = tile.rank / a.splits, split = tile.rank % a.splits;
+    const uint32_t rank = tile.rank, split = tile.part;
     const uint64_t live = a.live_count[rank];
     const uint64_t m0 = static_cast<uint64_t>(tile.m) * Tile::EM, n0 = static_cast<uint64_t>(tile.n) * Tile::EN;
-    if (n0 >= live) return;
     // this split's columns of the piece, whole tiles of the vocabulary
     const uint64_t blocks = a.piece / kVocabTile;
     const uint64_t from = blocks * split / a.splits * kVocabTile;
@@ -418,7 +415,7 @@ template <class Tile>
 constexpr bool is_tile(CrossTile t) {
     return static_cast<uint64_t>(Tile::EM) == tile_m(t) && static_cast<uint64_t>(Tile::EN) == tile_n(t);
 }
-static_assert(kMostStride == kMostOperandStride, "the host's operands");
+static_assert(kMostStride == kMostOperandStride && kCrossRanks <= 64, "the host's operands");
 static_assert(is_tile<LargeTile>(CrossTile::kLarge) && is_tile<MediumTile>(CrossTile::kMedium) &&
                   is_tile<SmallTile>(CrossTile::kSmall) && is_tile<TinyTile>(CrossTile::kTiny),
               "the host's tiles");
@@ -450,7 +447,7 @@ hipError_t start_dz(const CrossArgs& a, int nranks, hipStream_t s) {
     const uint64_t blocks = tile_blocks(static_cast<uint64_t>(tiles_m) * tiles_n * nranks);
     if (!fits_launch(blocks, Tile::kThreads)) return hipErrorInvalidValue;
     hipLaunchKernelGGL((k_cross_dz<DT, Tile>), dim3(static_cast<unsigned>(blocks)), dim3(Tile::kThreads), 0, s, a,
-                       padded_cols(a.cols, elem_size<DT>()), tiles_m, tiles_n, static_cast<uint32_t>(nranks));
+                       padded_cols(a.cols, elem_size<DT>()), tiles_m, static_cast<uint32_t>(nranks));
     return hipGetLastError();
 }
 
@@ -460,7 +457,7 @@ hipError_t start_dx(const CrossArgs& a, int nranks, bool add, hipStream_t s) {
     const uint64_t blocks = tile_blocks(static_cast<uint64_t>(tiles_m) * tiles_n * nranks * a.splits);
     if (!fits_launch(blocks, Tile::kThreads)) return hipErrorInvalidValue;
     hipLaunchKernelGGL((k_cross_dx<DT, Tile>), dim3(static_cast<unsigned>(blocks)), dim3(Tile::kThreads), 0, s, a,
-                       add ? 1 : 0, tiles_m, tiles_n, static_cast<uint32_t>(nranks));
+                       add ? 1 : 0, tiles_m, static_cast<uint32_t>(nranks));
     return hipGetLastError();
 }
 

@@ -298,14 +298,43 @@ __device__ __forceinline__ void product(char* buffers, const char* a, uint64_t a
 // the tiles that it works on at a time share their operands in its L2.
 constexpr uint32_t kAcross = 4;
 struct TilePlace {
-    uint32_t rank, m, n;
+    uint32_t rank, part, m, n;
     bool valid;
-    __device__ __forceinline__ TilePlace(uint32_t block, uint32_t tiles_m, uint32_t tiles_n, uint32_t ranks) {
-        const uint32_t all = tiles_m * tiles_n * ranks, each = (all + 7) / 8;
-        const uint32_t t = (block & 7) * each + (block >> 3);
-        valid = (block >> 3) < each && t < all;
+    __device__ __forceinline__ TilePlace(uint32_t block, uint32_t tiles_m, uint32_t tiles_n, uint32_t ranks) : part(0) {
+        uint32_t t = 0;
+        valid = stretch(block, tiles_m * tiles_n * ranks, t);
         rank = t / (tiles_m * tiles_n);
-        const uint32_t in = t % (tiles_m * tiles_n);
+        across(t % (tiles_m * tiles_n), tiles_m, tiles_n);
+    }
+    // The same when each rank (at most 64) has its own n side, of live[rank], in
+    // tiles of `en`, and each of its tiles is made in `parts`.  The workgroups past
+    // the last tile are then the launch's last, in every XCD alike: a batch half of
+    // which is ignored leaves no XCD without work.
+    __device__ __forceinline__ TilePlace(uint32_t block, uint32_t tiles_m, const uint32_t* live, uint32_t en,
+                                         uint32_t parts, uint32_t ranks) {
+        const uint32_t lane = threadIdx.x & 63, mine = lane < ranks ? (live[lane] + en - 1) / en : 0;
+        const auto tiles_n = [&](uint32_t r) -> uint32_t { return __builtin_amdgcn_readlane(mine, r); };
+        uint32_t all = 0, t = 0;
+        for (uint32_t r = 0; r < ranks; ++r) all += tiles_n(r);
+        valid = stretch(block, all * tiles_m * parts, t);
+        if (!valid) return;
+        for (rank = 0; rank + 1 < ranks; ++rank) {
+            const uint32_t here = tiles_n(rank) * tiles_m * parts;
+            if (t < here) break;
+            t -= here;
+        }
+        const uint32_t each = tiles_n(rank) * tiles_m;
+        part = t / each;
+        across(t % each, tiles_m, tiles_n(rank));
+    }
+
+private:
+    static __device__ __forceinline__ bool stretch(uint32_t block, uint32_t all, uint32_t& t) {
+        const uint32_t each = (all + 7) / 8;
+        t = (block & 7) * each + (block >> 3);
+        return (block >> 3) < each && t < all;
+    }
+    __device__ __forceinline__ void across(uint32_t in, uint32_t tiles_m, uint32_t tiles_n) {
         const uint32_t group = in / (kAcross * tiles_m), rest = in % (kAcross * tiles_m);
         const uint32_t width = std::min(kAcross, tiles_n - group * kAcross);
         m = rest / width;
