@@ -31,11 +31,16 @@ __device__ __forceinline__ int64_t index_at(const char* p, uint64_t i, int wide)
     return wide ? reinterpret_cast<const int64_t*>(p)[i] : reinterpret_cast<const int32_t*>(p)[i];
 }
 
-// The tiles that pick_tile chooses from.
+// The tiles that pick_tile chooses from.  The smallest one of float32 has a
+// buffer less, for a fourth workgroup on a compute unit beside three: 3 x 129
+// rows of 515 against 5,003, backward, 143 -> 134 us; 16 bits lose by it (16
+// rows of 4,096 against 65,536 112 + 444 -> 116 + 459 us), and two buffers cost
+// float32 there 832 -> 978 us.
 typedef TileOf<256, 256, 2, 4, 128, 2> LargeTile;
 typedef TileOf<128, 128, 4, 2, 128, 2> MediumTile;
 typedef TileOf<128, 64, 4, 1, 128, 3> SmallTile;
-typedef TileOf<64, 32, 2, 2, 128, 4> TinyTile;
+template <int DT>
+using TinyTile = TileOf<64, 32, 2, 2, 128, DT == AR_FLOAT32 ? 3 : 4>;
 
 // ---------------------------------------------------------------------------
 // forward
@@ -417,7 +422,7 @@ constexpr bool is_tile(CrossTile t) {
 }
 static_assert(kMostStride == kMostOperandStride && kCrossRanks <= 64, "the host's operands");
 static_assert(is_tile<LargeTile>(CrossTile::kLarge) && is_tile<MediumTile>(CrossTile::kMedium) &&
-                  is_tile<SmallTile>(CrossTile::kSmall) && is_tile<TinyTile>(CrossTile::kTiny),
+                  is_tile<SmallTile>(CrossTile::kSmall) && is_tile<TinyTile<AR_FLOAT32>>(CrossTile::kTiny),
               "the host's tiles");
 
 template <int DT, class Tile>
@@ -487,7 +492,7 @@ hipError_t start_finish(const CrossArgs& a, int nranks, hipStream_t s) {
     return hipGetLastError();
 }
 
-// an expression with DT, a floating dtype, and Tile
+// an expression with DT, a floating dtype
 #define AR_BY_DTYPE(dtype, ...)                                                   \
     switch (dtype) {                                                              \
         case AR_FLOAT32: { constexpr int DT = AR_FLOAT32; return __VA_ARGS__; }   \
@@ -495,14 +500,16 @@ hipError_t start_finish(const CrossArgs& a, int nranks, hipStream_t s) {
         case AR_FLOAT16: { constexpr int DT = AR_FLOAT16; return __VA_ARGS__; }   \
         default: return hipErrorInvalidValue;                                     \
     }
-#define AR_BY_TILE(tile, dtype, ...)                                                               \
-    switch (tile) {                                                                                \
-        case CrossTile::kLarge: { typedef LargeTile Tile; AR_BY_DTYPE(dtype, __VA_ARGS__) }        \
-        case CrossTile::kMedium: { typedef MediumTile Tile; AR_BY_DTYPE(dtype, __VA_ARGS__) }      \
-        case CrossTile::kSmall: { typedef SmallTile Tile; AR_BY_DTYPE(dtype, __VA_ARGS__) }        \
-        case CrossTile::kTiny: { typedef TinyTile Tile; AR_BY_DTYPE(dtype, __VA_ARGS__) }          \
-        default: return hipErrorInvalidValue;                                                      \
+template <int DT, class F>
+hipError_t by_tile(CrossTile tile, const F& start) {
+    switch (tile) {
+        case CrossTile::kLarge: return start(LargeTile{});
+        case CrossTile::kMedium: return start(MediumTile{});
+        case CrossTile::kSmall: return start(SmallTile{});
+        case CrossTile::kTiny: return start(TinyTile<DT>{});
     }
+    return hipErrorInvalidValue;
+}
 
 }  // namespace
 
@@ -510,7 +517,9 @@ hipError_t launch_align(const AlignArgs& a, int nranks, ar_dtype_t dtype, hipStr
     AR_BY_DTYPE(dtype, start_align<DT>(a, nranks, s))
 }
 hipError_t launch_cross_stats(const CrossArgs& a, int nranks, CrossTile tile, ar_dtype_t dtype, hipStream_t s) {
-    AR_BY_TILE(tile, dtype, start_stats<DT, Tile>(a, nranks, s))
+    AR_BY_DTYPE(dtype, by_tile<DT>(tile, [&](auto t) {
+                    return start_stats<DT, decltype(t)>(a, nranks, s);
+                }))
 }
 hipError_t launch_cross_loss(const CrossArgs& a, int nranks, hipStream_t s) {
     hipLaunchKernelGGL(k_cross_loss, dim3(tiles_of(a.rows, 16), nranks), dim3(256), 0, s, a);
@@ -520,13 +529,19 @@ hipError_t launch_cross_live(const CrossArgs& a, int nranks, ar_dtype_t dtype, h
     AR_BY_DTYPE(dtype, start_live<DT>(a, nranks, s))
 }
 hipError_t launch_cross_dz(const CrossArgs& a, int nranks, ar_dtype_t dtype, hipStream_t s) {
-    AR_BY_TILE(pick_tile(a.piece, a.rows, nranks, dtype == AR_FLOAT32), dtype, start_dz<DT, Tile>(a, nranks, s))
+    AR_BY_DTYPE(dtype, by_tile<DT>(pick_tile(a.piece, a.rows, nranks, dtype == AR_FLOAT32), [&](auto t) {
+                    return start_dz<DT, decltype(t)>(a, nranks, s);
+                }))
 }
 hipError_t launch_cross_dx(const CrossArgs& a, int nranks, bool add, CrossTile tile, ar_dtype_t dtype, hipStream_t s) {
-    AR_BY_TILE(tile, dtype, start_dx<DT, Tile>(a, nranks, add, s))
+    AR_BY_DTYPE(dtype, by_tile<DT>(tile, [&](auto t) {
+                    return start_dx<DT, decltype(t)>(a, nranks, add, s);
+                }))
 }
 hipError_t launch_cross_dweight(const CrossArgs& a, int nranks, ar_dtype_t dtype, hipStream_t s) {
-    AR_BY_TILE(pick_tile(a.cols, a.count, nranks, dtype == AR_FLOAT32), dtype, start_dweight<DT, Tile>(a, nranks, s))
+    AR_BY_DTYPE(dtype, by_tile<DT>(pick_tile(a.cols, a.count, nranks, dtype == AR_FLOAT32), [&](auto t) {
+                    return start_dweight<DT, decltype(t)>(a, nranks, s);
+                }))
 }
 hipError_t launch_cross_finish(const CrossArgs& a, int nranks, ar_dtype_t dtype, hipStream_t s) {
     AR_BY_DTYPE(dtype, start_finish<DT>(a, nranks, s))
