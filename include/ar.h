@@ -707,10 +707,10 @@ typedef enum {
  * out_stride elements apart) receives scale * row tokens[r][i] of table[r]
  * (`vocab` rows of `cols` elements of table_dtype, which is dtype or
  * AR_FLOAT32, table_stride apart): a float32 product, rounded to dtype (to
- * binary16 in the same step).  A token outside [0, vocab) reads nothing; its row becomes NaN.  Outputs
- * overlap nothing else; several ranks may read one table.  scale is any number
- * in float32's range but one that it rounds to 0.  rows == 0 or cols == 0 is a
- * successful no-op. */
+ * binary16 in the same step).  A token outside [0, vocab) reads nothing; its
+ * row becomes NaN.  Outputs overlap nothing else; several ranks may read one
+ * table.  scale is any number in float32's range but one that it rounds to 0.
+ * rows == 0 or cols == 0 is a successful no-op. */
 ar_result_t ar_embedding(const void* const* tokens, const void* const* table, void* const* out, size_t rows,
                          size_t vocab, size_t cols, size_t table_stride, size_t out_stride, ar_index_t index_type,
                          ar_dtype_t dtype, ar_dtype_t table_dtype, double scale, int nranks, hipStream_t stream);
@@ -746,7 +746,9 @@ size_t ar_embedding_workspace_bytes(size_t rows, size_t vocab, size_t cols, int 
  * joined in order.  Outputs overlap nothing else; ranks may share one weight.
  * rows == 0 is a successful no-op; cols == 0 means logits of 0.
  * `workspace`: at least ar_cross_entropy_workspace_bytes(...) bytes of device
- * memory, 16-byte aligned.  vocab of 1 to 2^31 - 1, rows < 2^31. */
+ * memory, 16-byte aligned.  vocab of 1 to 2^31 - 1.  More than a launch can
+ * count is refused; up to 2^25 rows, 2^36 rows x cols and 2^36 vocab x cols,
+ * each of all ranks together, always fit. */
 ar_result_t ar_cross_entropy(const void* const* x, const void* const* weight, const void* const* targets,
                              float* const* loss, float* const* lse, size_t rows, size_t vocab, size_t cols,
                              size_t x_stride, size_t weight_stride, ar_index_t index_type, long long ignore_index,

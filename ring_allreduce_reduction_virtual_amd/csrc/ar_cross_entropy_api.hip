@@ -14,8 +14,9 @@ using namespace arimpl;
 namespace {
 
 constexpr uint64_t kMaxTokens = (1ull << 31) - 1, kMaxVocab = (1ull << 31) - 1, kMaxWidth = 1ull << 20;
-// Large tiles of one launch, whose threads are counted with 32 bits.
-constexpr uint64_t kMaxTiles = 1ull << 21;
+// Large tiles of one launch, whose threads are counted with 32 bits; few rows or
+// columns get up to eight small ones of 256 threads instead of each.
+constexpr uint64_t kMaxTiles = 1ull << 20;
 uint64_t large_tiles(uint64_t m, uint64_t n, uint64_t batch) { return tiles_in(m, n, CrossTile::kLarge) * batch; }
 
 ar_result_t check_sizes(size_t rows, size_t vocab, size_t cols, ar_dtype_t dtype, int nranks) {

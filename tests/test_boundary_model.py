@@ -242,3 +242,11 @@ def test_cross_entropy_workspaces(lib, dt, rows, vocab, cols):
         assert back <= piece + ranks * 256 * rows * es + copies + ranks * rows * (64 * width * 4 + 64) + 16384
     assert lib.ar_cross_entropy_workspace_bytes(rows, vocab, cols, I32, 1, 0) == NONE
     assert lib.ar_cross_entropy_workspace_bytes(rows, 0, cols, dt, 1, 1) == NONE
+
+
+def test_cross_entropy_launches_fit(lib):
+    """More rows than one launch's threads can be counted for are refused before anything is launched."""
+    for backward in (0, 1):
+        assert lib.ar_cross_entropy_workspace_bytes(1 << 28, 64, 8, BF16, 1, backward) not in (0, NONE)
+        assert lib.ar_cross_entropy_workspace_bytes((1 << 28) + 1, 64, 8, BF16, 1, backward) == NONE
+        assert lib.ar_cross_entropy_workspace_bytes(1 << 29, 64, 8, BF16, 1, backward) == NONE

@@ -338,3 +338,14 @@ def test_refusals(ar):
     odd = torch.zeros(need + 8, dtype=torch.uint8, device="cuda")[1:need + 1]
     with pytest.raises(ar.ArError, match="aligned"):
         ar.ar_embedding_backward(dy, t, 5, workspace=odd)
+
+
+def test_most_tokens(ar):
+    """2^31 - 1 places, the most: the sort's counts and every grid at their largest."""
+    torch = _torch()
+    rows, vocab = (1 << 31) - 1, 1024
+    tokens = torch.arange(rows, dtype=torch.int32, device="cuda").remainder_(vocab)
+    got = ar.ar_embedding_backward([torch.ones(rows, 1, device="cuda")], [tokens], vocab)[0]
+    want = torch.full((vocab, 1), float(1 << 21), device="cuda")   # whole numbers below 2^24 throughout
+    want[-1] -= 1
+    assert torch.equal(got, want)
