@@ -16,6 +16,13 @@
 // sums gain dz W of the piece (the order of pieces is fixed); the piece's rows
 // of dweight = dz^T x are complete.  The rows that take part are gathered
 // first, so that ignored rows cost nothing and reach nothing.
+//
+// The matrix cores bound the large sizes: 2 x 4,096 rows of 4,096 against
+// 65,536 in bf16 take 3.3 ms forward (1,340 TFLOP/s; operands of zeros, which
+// draw less power, 1,615) and 10.3 backward (1,280), each of the three products
+// the same 1.75 ms for half of the vocabulary; float32, 2 x 4,096 of 2,048 against
+// 32,768, 7.6 ms (146) and 23.1.  With few rows reading the weight does: 16 rows
+// of 4,096 against 65,536 112 us (4.8 TB/s).
 
 #include <hip/hip_runtime.h>
 
@@ -177,7 +184,8 @@ __global__ void __launch_bounds__(256) k_cross_loss(CrossArgs a) {
 // aligned copies
 // ---------------------------------------------------------------------------
 
-// Rows with zeros behind them, a vector of 16 bytes of the copy a thread.
+// Rows with zeros behind them, a vector of 16 bytes of the copy a thread: 3 x
+// 5,003 rows of 515 float32, 11 us (5.6 TB/s).
 template <int DT>
 __global__ void __launch_bounds__(256) k_align(AlignArgs a) {
     constexpr int V = kOperandBytes / elem_size<DT>();
@@ -253,7 +261,8 @@ __global__ void __launch_bounds__(1024) k_cross_live(CrossArgs a, float span) {
     if (threadIdx.x == 0) a.live_count[rank] = before;
 }
 
-// The live rows of x, one after another with zeros behind each.
+// The live rows of x, one after another with zeros behind each: a copy, 24 us
+// for 2 x 4,096 rows of 4,096 bf16 (5.3 TB/s).
 template <int DT>
 __global__ void __launch_bounds__(256) k_cross_gather(CrossArgs a, uint64_t padded) {
     constexpr int V = kOperandBytes / elem_size<DT>();
