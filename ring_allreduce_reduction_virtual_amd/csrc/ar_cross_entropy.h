@@ -26,6 +26,18 @@ constexpr uint64_t padded_cols(uint64_t cols, uint64_t es) {
     return (cols * es + kOperandBytes - 1) / kOperandBytes * kOperandBytes / es;
 }
 
+// With few rows, reading the weight is the time, and its copy three times that:
+// float32 operands are then read 4 bytes at a time where they lie.  Copied / in
+// place, us: forward, 2 x 2 rows of 817 against 34,928 152 / 77, 55 of 490
+// against 122,842 181 / 115, 59 of 3,110 against 1,611 65 / 70, 3 x 129 of 515
+// against 5,003 56 / 55, 4 x 424 of 1,223 against 55,858 2,374 / 2,820;
+// backward, whose one copy serves two products, the same 298 / 239, 397 / 371,
+// 97 / 116, 131 / 154, 6,435 / 7,596.
+constexpr uint64_t kWordRows = 64, kWordRowsBackward = 32;
+constexpr bool in_words(uint64_t rows, uint64_t es, bool backward) {
+    return es == 4 && rows <= (backward ? kWordRowsBackward : kWordRows);
+}
+
 // The backward pass works the vocabulary off in pieces of whole tiles, so that
 // what it keeps of dz is bounded whatever the vocabulary is: kPieceBytes in all,
 // or kLeastPiece columns.  Every piece more reads and writes dx's float32 sums
@@ -109,6 +121,7 @@ struct CrossArgs {
     char* dweight[kCrossRanks];
     uint64_t rows, vocab, cols;
     uint64_t x_stride, weight_stride, dx_stride, dweight_stride;   // elements
+    int whole;   // 0: float32 x (forward) and weight are read 4 bytes at a time
     int64_t ignore;
     float scale;
     int wide_index;

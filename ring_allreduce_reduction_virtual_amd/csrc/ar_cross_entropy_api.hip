@@ -40,7 +40,7 @@ ar_result_t check_sizes(size_t rows, size_t vocab, size_t cols, ar_dtype_t dtype
 // The parts of the workspace, in bytes from its start.
 struct Layout {
     uint64_t piece = 0, padded = 0, all = 0;
-    uint64_t x = 0, weight = 0;                                                    // aligned copies
+    uint64_t x = 0, weight = 0;                                                    // aligned copies, or live rows
     uint64_t partials = 0, target_logit = 0;                                       // forward
     uint64_t live_count = 0, place = 0, unscale = 0, live = 0, dz = 0, sums = 0;   // backward
     DxShape dx{};
@@ -56,8 +56,9 @@ struct Layout {
         const uint64_t n = static_cast<uint64_t>(std::min(nranks, kCrossRanks)), es = float_size(dtype);
         piece = piece_of(rows, vocab, es, static_cast<int>(n));
         padded = padded_cols(cols, es);
-        x = take(n * rows * padded * es);
-        weight = take(n * std::min(piece, vocab) * padded * es);
+        const bool copies = !in_words(rows, es, backward);
+        if (backward || copies) x = take(n * rows * padded * es);
+        if (copies) weight = take(n * std::min(piece, vocab) * padded * es);
         if (backward) {
             dx = dx_shape(rows, cols, piece, es, static_cast<int>(n));
             live_count = take(n * 4);
@@ -175,13 +176,17 @@ ar_result_t ar_cross_entropy(const void* const* x, const void* const* weight, co
                 a.lse[k] = lse[g + k];
             }
             a.x_stride = x_stride;
-            if (!aligned(x + g, n, x_stride, cols, es)) {
+            const bool x_aligned = aligned(x + g, n, x_stride, cols, es);
+            const bool weight_aligned = aligned(weight + g, n, weight_stride, cols, es);
+            const bool words = in_words(rows, es, false) && !(x_aligned && weight_aligned);
+            a.whole = !words;
+            if (!x_aligned && !words) {
                 a.x_stride = at.padded;
                 rc = align(x + g, n, 0, rows, cols, x_stride, at.padded, dtype, ws + at.x, a.x, stream);
                 if (rc != AR_SUCCESS) return rc;
             }
             // a weight that needs no copy is one piece, as far as one launch goes
-            const bool as_is = aligned(weight + g, n, weight_stride, cols, es);
+            const bool as_is = weight_aligned || words;
             const uint64_t most = kMaxTiles / large_tiles(1, rows, n) * kVocabTile;
             for (uint64_t first = 0; first < vocab;) {
                 const uint64_t count = std::min<uint64_t>(vocab - first, as_is ? most : at.piece);
@@ -271,7 +276,9 @@ ar_result_t ar_cross_entropy_backward(const float* const* dloss, const void* con
             }
             const char* const what = "cross_entropy_backward launch";
             if ((rc = hip_result(launch_cross_live(a, n, dtype, stream), what)) != AR_SUCCESS) return rc;
-            const bool as_is = aligned(weight + g, n, weight_stride, cols, es);
+            const bool weight_aligned = aligned(weight + g, n, weight_stride, cols, es);
+            a.whole = weight_aligned || !in_words(rows, es, true);
+            const bool as_is = weight_aligned || !a.whole;
             for (uint64_t first = 0; first < vocab; first += at.piece) {
                 const uint64_t count = std::min<uint64_t>(vocab - first, at.piece);
                 rc = set_piece(a, at, ws, weight + g, n, first, count, weight_stride, as_is, dtype, stream);

@@ -53,7 +53,7 @@ using TinyTile = TileOf<64, 32, 2, 2, 128, DT == AR_FLOAT32 ? 3 : 4>;
 // forward
 // ---------------------------------------------------------------------------
 
-template <int DT, class Tile>
+template <int DT, class Tile, bool WHOLE>
 __global__ void __launch_bounds__(Tile::kThreads) k_cross_stats(CrossArgs a, uint32_t tiles_m, uint32_t tiles_n,
                                                                 uint32_t ranks) {
     __shared__ __attribute__((aligned(1024))) char buffers[Tile::kShared];
@@ -63,7 +63,7 @@ __global__ void __launch_bounds__(Tile::kThreads) k_cross_stats(CrossArgs a, uin
     constexpr int kEs = elem_size<DT>();
     const uint64_t m0 = static_cast<uint64_t>(tile.m) * Tile::EM, n0 = static_cast<uint64_t>(tile.n) * Tile::EN;
     f32x4 sum[Tile::TM][Tile::TN];
-    product<DT, Tile, true, true>(buffers, a.weight[tile.rank], a.weight_stride * kEs, m0, a.count, a.x[tile.rank],
+    product<DT, Tile, WHOLE, true, true>(buffers, a.weight[tile.rank], a.weight_stride * kEs, m0, a.count, a.x[tile.rank],
                                   a.x_stride * kEs, n0, a.rows, a.cols, sum);
     const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
     const int wm = wave / Tile::WN, wn = wave % Tile::WN;
@@ -281,7 +281,7 @@ __global__ void __launch_bounds__(256) k_cross_gather(CrossArgs a, uint64_t padd
 }
 
 // dz of a piece's columns: [live row][piece], zeros behind the vocabulary's end.
-template <int DT, class Tile>
+template <int DT, class Tile, bool WHOLE>
 __global__ void __launch_bounds__(Tile::kThreads) k_cross_dz(CrossArgs a, uint64_t padded, uint32_t tiles_m,
                                                              uint32_t ranks) {
     __shared__ __attribute__((aligned(1024))) char buffers[Tile::kShared];
@@ -292,7 +292,7 @@ __global__ void __launch_bounds__(Tile::kThreads) k_cross_dz(CrossArgs a, uint64
     const uint64_t m0 = static_cast<uint64_t>(tile.m) * Tile::EM, n0 = static_cast<uint64_t>(tile.n) * Tile::EN;
     f32x4 sum[Tile::TM][Tile::TN];
     // a tile past the vocabulary's end (the piece is padded) has its last row for all
-    product<DT, Tile, true, true>(buffers, a.weight[tile.rank], a.weight_stride * kEs, m0, a.count,
+    product<DT, Tile, WHOLE, true, true>(buffers, a.weight[tile.rank], a.weight_stride * kEs, m0, a.count,
                                   a.x_live + tile.rank * a.rows * padded * kEs, padded * kEs, n0, live, a.cols, sum);
     const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
     const uint64_t first = m0 + (wave / Tile::WN) * Tile::TM * kSquare + 4 * (lane >> 4);
@@ -321,7 +321,7 @@ __global__ void __launch_bounds__(Tile::kThreads) k_cross_dz(CrossArgs a, uint64
 }
 
 // A piece's part of dx's sums: [split][live row][column].
-template <int DT, class Tile>
+template <int DT, class Tile, bool WHOLE>
 __global__ void __launch_bounds__(Tile::kThreads) k_cross_dx(CrossArgs a, int add, uint32_t tiles_m, uint32_t ranks) {
     __shared__ __attribute__((aligned(1024))) char buffers[Tile::kShared];
     const TilePlace tile(blockIdx.x, tiles_m, a.live_count, Tile::EN, a.splits, ranks);
@@ -336,7 +336,7 @@ __global__ void __launch_bounds__(Tile::kThreads) k_cross_dx(CrossArgs a, int ad
     const uint64_t end = std::min(a.count, blocks * (split + 1) / a.splits * kVocabTile);
     const uint64_t depth = end > from ? end - from : 0;
     f32x4 sum[Tile::TM][Tile::TN];
-    product<DT, Tile, false, true>(buffers, a.weight[rank] + from * a.weight_stride * kEs, a.weight_stride * kEs, m0,
+    product<DT, Tile, WHOLE, false, true>(buffers, a.weight[rank] + from * a.weight_stride * kEs, a.weight_stride * kEs, m0,
                                    a.cols, a.dz + (rank * a.rows * a.piece + from) * kEs, a.piece * kEs, n0, live, depth,
                                    sum);
     const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
@@ -366,7 +366,7 @@ __global__ void __launch_bounds__(Tile::kThreads) k_cross_dweight(CrossArgs a, u
     constexpr int kEs = elem_size<DT>();
     const uint64_t m0 = static_cast<uint64_t>(tile.m) * Tile::EM, n0 = static_cast<uint64_t>(tile.n) * Tile::EN;
     f32x4 sum[Tile::TM][Tile::TN];
-    product<DT, Tile, false, false>(buffers, a.x_live + tile.rank * a.rows * padded * kEs, padded * kEs, m0, a.cols,
+    product<DT, Tile, true, false, false>(buffers, a.x_live + tile.rank * a.rows * padded * kEs, padded * kEs, m0, a.cols,
                                     a.dz + tile.rank * a.rows * a.piece * kEs, a.piece * kEs, n0, a.count,
                                     a.live_count[tile.rank], sum);
     const float unscale = a.unscale[tile.rank];
@@ -434,14 +434,31 @@ static_assert(is_tile<LargeTile>(CrossTile::kLarge) && is_tile<MediumTile>(Cross
                   is_tile<SmallTile>(CrossTile::kSmall) && is_tile<TinyTile<AR_FLOAT32>>(CrossTile::kTiny),
               "the host's tiles");
 
+// f(WHOLE), and what the launch says.  Few rows (in_words) never get a tile wider
+// than they are: one that is costs more in any number of tiles.
+template <int DT, class Tile, class F>
+hipError_t by_rows(const CrossArgs& a, const F& f) {
+    constexpr bool kWords = DT == AR_FLOAT32 && Tile::EN <= static_cast<int>(kWordRows);
+    if constexpr (kWords) {
+        if (!a.whole) {
+            f(std::false_type{});
+            return hipGetLastError();
+        }
+    }
+    if (!a.whole) return hipErrorInvalidValue;
+    f(std::true_type{});
+    return hipGetLastError();
+}
+
 template <int DT, class Tile>
 hipError_t start_stats(const CrossArgs& a, int nranks, hipStream_t s) {
     const uint32_t tiles_m = tiles_of(a.count, Tile::EM), tiles_n = tiles_of(a.rows, Tile::EN);
     const uint64_t blocks = tile_blocks(static_cast<uint64_t>(tiles_m) * tiles_n * nranks);
     if (!fits_launch(blocks, Tile::kThreads)) return hipErrorInvalidValue;
-    hipLaunchKernelGGL((k_cross_stats<DT, Tile>), dim3(static_cast<unsigned>(blocks)), dim3(Tile::kThreads), 0, s, a,
-                       tiles_m, tiles_n, static_cast<uint32_t>(nranks));
-    return hipGetLastError();
+    return by_rows<DT, Tile>(a, [&](auto whole) {
+        hipLaunchKernelGGL((k_cross_stats<DT, Tile, whole.value>), dim3(static_cast<unsigned>(blocks)),
+                           dim3(Tile::kThreads), 0, s, a, tiles_m, tiles_n, static_cast<uint32_t>(nranks));
+    });
 }
 
 template <int DT>
@@ -460,9 +477,11 @@ hipError_t start_dz(const CrossArgs& a, int nranks, hipStream_t s) {
     const uint32_t tiles_m = tiles_of(a.piece, Tile::EM), tiles_n = tiles_of(a.rows, Tile::EN);
     const uint64_t blocks = tile_blocks(static_cast<uint64_t>(tiles_m) * tiles_n * nranks);
     if (!fits_launch(blocks, Tile::kThreads)) return hipErrorInvalidValue;
-    hipLaunchKernelGGL((k_cross_dz<DT, Tile>), dim3(static_cast<unsigned>(blocks)), dim3(Tile::kThreads), 0, s, a,
-                       padded_cols(a.cols, elem_size<DT>()), tiles_m, static_cast<uint32_t>(nranks));
-    return hipGetLastError();
+    return by_rows<DT, Tile>(a, [&](auto whole) {
+        hipLaunchKernelGGL((k_cross_dz<DT, Tile, whole.value>), dim3(static_cast<unsigned>(blocks)),
+                           dim3(Tile::kThreads), 0, s, a, padded_cols(a.cols, elem_size<DT>()), tiles_m,
+                           static_cast<uint32_t>(nranks));
+    });
 }
 
 template <int DT, class Tile>
@@ -470,9 +489,10 @@ hipError_t start_dx(const CrossArgs& a, int nranks, bool add, hipStream_t s) {
     const uint32_t tiles_m = tiles_of(a.cols, Tile::EM), tiles_n = tiles_of(a.rows, Tile::EN);
     const uint64_t blocks = tile_blocks(static_cast<uint64_t>(tiles_m) * tiles_n * nranks * a.splits);
     if (!fits_launch(blocks, Tile::kThreads)) return hipErrorInvalidValue;
-    hipLaunchKernelGGL((k_cross_dx<DT, Tile>), dim3(static_cast<unsigned>(blocks)), dim3(Tile::kThreads), 0, s, a,
-                       add ? 1 : 0, tiles_m, static_cast<uint32_t>(nranks));
-    return hipGetLastError();
+    return by_rows<DT, Tile>(a, [&](auto whole) {
+        hipLaunchKernelGGL((k_cross_dx<DT, Tile, whole.value>), dim3(static_cast<unsigned>(blocks)),
+                           dim3(Tile::kThreads), 0, s, a, add ? 1 : 0, tiles_m, static_cast<uint32_t>(nranks));
+    });
 }
 
 template <int DT, class Tile>

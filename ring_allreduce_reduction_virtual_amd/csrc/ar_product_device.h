@@ -10,8 +10,11 @@
 // holds it as it lies, and 16-bit operands across k are turned on the way to
 // the registers by ds_read_tr16_b64.  Both kinds exchange 16-byte chunks within
 // a row by its number, so that the lanes that read at a time meet different
-// banks.
+// banks.  Float32 operands whose rows do not lie on 16 bytes can be brought 4
+// bytes a lane.
 #pragma once
+
+#include <type_traits>
 
 #include "ar_step_device.h"
 
@@ -46,22 +49,13 @@ constexpr uint64_t kMostStride = 1u << 23;
 // What out-of-range k reads.
 __device__ const u32x4 kZeroChunk = {0, 0, 0, 0};
 
-// One operand: E rows of it (columns, when it lies across k) from `first` on,
-// of which those from `limit` on are not wanted (the last wanted one is read in
-// their place: nothing of it reaches another output).
-template <int DT, int E, int THREADS, int kStepBytes, bool ALONG>
-struct Operand {
+// An operand's part of a buffer: E rows of it (columns, when it lies across k).
+template <int DT, int E, int kStepBytes, bool ALONG>
+struct InShared {
     static constexpr int kEs = elem_size<DT>();
     static constexpr int kChunkElems = kChunk / kEs;
     static constexpr int kStep = kStepBytes / kEs;             // k at a time
-    static constexpr int kLoads = E * kStepBytes / kChunk / THREADS;
     static constexpr int kRowChunks = ALONG ? kStepBytes / kChunk : E * kEs / kChunk;
-    static_assert(E * kStepBytes % (kChunk * THREADS) == 0, "whole loads");
-    static_assert(THREADS % kRowChunks == 0, "a thread keeps its chunk of a row");
-
-    const char* base;          // of the step to bring next, the same in all lanes
-    uint64_t advance;
-    uint32_t offset[kLoads];   // from there: operands' rows lie at most kMostStride bytes apart
 
     // which chunk of a row stands at a place, and where a chunk stands
     static __device__ __forceinline__ int swap(int row, int chunk) {
@@ -72,52 +66,6 @@ struct Operand {
         } else {
             return chunk ^ (((row >> 2) & 3) << 2 & (kRowChunks - 1));
         }
-    }
-
-    __device__ __forceinline__ void start(const char* from, uint64_t stride, uint64_t first, uint64_t limit) {
-        const int place = threadIdx.x % kRowChunks;
-        // a tile past the limit has the last wanted row for all of its rows
-        if (first >= limit) first = ALONG ? limit - 1 : (limit - 1) / kChunkElems * kChunkElems;
-        base = from + (ALONG ? first * stride : first * kEs);
-        // past the limit: the last wanted row, or the last wanted column's chunk
-        const uint32_t last = static_cast<uint32_t>(std::min<uint64_t>(limit - 1 - first, E - 1));
-#pragma unroll
-        for (int j = 0; j < kLoads; ++j) {
-            const uint32_t row = (j * THREADS + threadIdx.x) / kRowChunks, chunk = swap(row, place);
-            if constexpr (ALONG) {
-                offset[j] = std::min(row, last) * static_cast<uint32_t>(stride) + chunk * kChunk;
-            } else {
-                offset[j] = row * static_cast<uint32_t>(stride) + std::min(chunk, last / kChunkElems) * kChunk;
-            }
-        }
-        advance = ALONG ? kStepBytes : kStep * stride;
-    }
-
-    // Brings the next step of k, of which `left` are in range (ALONG: rounded up
-    // to whole chunks, whose rest must be zeros), to shared memory at `to`.  m0
-    // says where in shared memory, and needs a wait before the load uses it; the
-    // compiler keeps nothing there in kernels without indexed registers.
-    __device__ __forceinline__ void issue(uint32_t to, int64_t left) {
-        to = __builtin_amdgcn_readfirstlane(to + (threadIdx.x & ~63u) * kChunk);
-        if (left >= kStep) {
-#pragma unroll
-            for (int j = 0; j < kLoads; ++j) {
-                asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(to + j * THREADS * kChunk),
-                             "v"(offset[j]), "s"(base)
-                             : "memory");
-            }
-        } else {
-#pragma unroll
-            for (int j = 0; j < kLoads; ++j) {
-                const int row = (j * THREADS + static_cast<int>(threadIdx.x)) / kRowChunks;
-                const int k = ALONG ? swap(row, threadIdx.x % kRowChunks) * kChunkElems : row;
-                const char* const q = k < left ? base + offset[j] : reinterpret_cast<const char*>(&kZeroChunk);
-                asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(to + j * THREADS * kChunk),
-                             "v"(q)
-                             : "memory");
-            }
-        }
-        base += advance;
     }
 
     // Where this lane reads in the operand's part of a buffer: for the T squares
@@ -171,6 +119,115 @@ struct Operand {
     }
 };
 
+// One operand: E rows of it (columns, when it lies across k) from `first` on,
+// of which those from `limit` on are not wanted (the last wanted one is read in
+// their place: nothing of it reaches another output).  Its rows lie on 16 bytes,
+// at most kMostStride apart.
+template <int DT, int E, int THREADS, int kStepBytes, bool ALONG>
+struct ChunkOperand : InShared<DT, E, kStepBytes, ALONG> {
+    typedef InShared<DT, E, kStepBytes, ALONG> Shared;
+    using Shared::kChunkElems, Shared::kEs, Shared::kRowChunks, Shared::kStep, Shared::swap;
+    static constexpr int kLoads = E * kStepBytes / kChunk / THREADS;
+    static_assert(E * kStepBytes % (kChunk * THREADS) == 0, "whole loads");
+    static_assert(THREADS % kRowChunks == 0, "a thread keeps its chunk of a row");
+
+    const char* base;          // of the step to bring next, the same in all lanes
+    uint64_t advance;
+    uint32_t offset[kLoads];   // from there: operands' rows lie at most kMostStride bytes apart
+
+    __device__ __forceinline__ void start(const char* from, uint64_t stride, uint64_t first, uint64_t limit) {
+        const int place = threadIdx.x % kRowChunks;
+        // a tile past the limit has the last wanted row for all of its rows
+        if (first >= limit) first = ALONG ? limit - 1 : (limit - 1) / kChunkElems * kChunkElems;
+        base = from + (ALONG ? first * stride : first * kEs);
+        // past the limit: the last wanted row, or the last wanted column's chunk
+        const uint32_t last = static_cast<uint32_t>(std::min<uint64_t>(limit - 1 - first, E - 1));
+#pragma unroll
+        for (int j = 0; j < kLoads; ++j) {
+            const uint32_t row = (j * THREADS + threadIdx.x) / kRowChunks, chunk = swap(row, place);
+            if constexpr (ALONG) {
+                offset[j] = std::min(row, last) * static_cast<uint32_t>(stride) + chunk * kChunk;
+            } else {
+                offset[j] = row * static_cast<uint32_t>(stride) + std::min(chunk, last / kChunkElems) * kChunk;
+            }
+        }
+        advance = ALONG ? kStepBytes : kStep * stride;
+    }
+
+    // Brings the next step of k, of which `left` are in range (ALONG: rounded up
+    // to whole chunks, whose rest must be zeros), to shared memory at `to`.  m0
+    // says where in shared memory, and needs a wait before the load uses it; the
+    // compiler keeps nothing there in kernels without indexed registers.
+    __device__ __forceinline__ void issue(uint32_t to, int64_t left) {
+        to = __builtin_amdgcn_readfirstlane(to + (threadIdx.x & ~63u) * kChunk);
+        if (left >= kStep) {
+#pragma unroll
+            for (int j = 0; j < kLoads; ++j) {
+                asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(to + j * THREADS * kChunk),
+                             "v"(offset[j]), "s"(base)
+                             : "memory");
+            }
+        } else {
+#pragma unroll
+            for (int j = 0; j < kLoads; ++j) {
+                const int row = (j * THREADS + static_cast<int>(threadIdx.x)) / kRowChunks;
+                const int k = ALONG ? swap(row, threadIdx.x % kRowChunks) * kChunkElems : row;
+                const char* const q = k < left ? base + offset[j] : reinterpret_cast<const char*>(&kZeroChunk);
+                asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(to + j * THREADS * kChunk),
+                             "v"(q)
+                             : "memory");
+            }
+        }
+        base += advance;
+    }
+};
+
+// The same of float32 operands in any place and any distance apart: 4 bytes a
+// lane, whose addresses are made anew for each load.  Four times the load
+// instructions: for products that reading the operands bounds.
+template <int DT, int E, int THREADS, int kStepBytes, bool ALONG>
+struct WordOperand : InShared<DT, E, kStepBytes, ALONG> {
+    typedef InShared<DT, E, kStepBytes, ALONG> Shared;
+    using Shared::kChunkElems, Shared::kEs, Shared::kRowChunks, Shared::kStep, Shared::swap;
+    static constexpr int kWord = 4, kRowWords = kRowChunks * kChunk / kWord;
+    static constexpr int kLoads = E * kStepBytes / kWord / THREADS;
+    static_assert(kEs == kWord && E * kStepBytes % (kWord * THREADS) == 0, "whole loads");
+    static_assert(THREADS % kRowWords == 0, "a thread keeps its word of a row");
+
+    const char* base;   // of the step to bring next
+    uint64_t stride, advance;
+    uint32_t last;      // wanted row (column)
+
+    __device__ __forceinline__ void start(const char* from, uint64_t stride_, uint64_t first, uint64_t limit) {
+        if (first >= limit) first = limit - 1;
+        stride = stride_;
+        base = from + (ALONG ? first * stride : first * kEs);
+        last = static_cast<uint32_t>(std::min<uint64_t>(limit - 1 - first, E - 1));
+        advance = ALONG ? kStepBytes : kStep * stride;
+    }
+
+    // As above; k past `left` is 0 whatever lies there.
+    __device__ __forceinline__ void issue(uint32_t to, int64_t left) {
+        to = __builtin_amdgcn_readfirstlane(to + (threadIdx.x & ~63u) * kWord);
+        const uint32_t word = threadIdx.x % kRowWords;
+#pragma unroll
+        for (int j = 0; j < kLoads; ++j) {
+            const uint32_t row = (j * THREADS + threadIdx.x) / kRowWords;
+            const uint32_t in = swap(row, word / kChunkElems) * kChunkElems + word % kChunkElems;   // its place in the row
+            const uint32_t k = ALONG ? in : row, which = std::min(ALONG ? row : in, last);
+            const char* q = base + (ALONG ? which : k) * stride + (ALONG ? k : which) * kWord;
+            if (k >= left) q = reinterpret_cast<const char*>(&kZeroChunk);
+            asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, off" ::"s"(to + j * THREADS * kWord), "v"(q)
+                         : "memory");
+        }
+        base += advance;
+    }
+};
+
+template <int DT, int E, int THREADS, int kStepBytes, bool WHOLE, bool ALONG>
+using Operand = std::conditional_t<WHOLE, ChunkOperand<DT, E, THREADS, kStepBytes, ALONG>,
+                                   WordOperand<DT, E, THREADS, kStepBytes, ALONG>>;
+
 template <int DT>
 __device__ __forceinline__ f32x4 multiply(u32x4 a, u32x4 b, f32x4 c) {
     if constexpr (DT == AR_BFLOAT16) {
@@ -199,12 +256,13 @@ __device__ __forceinline__ void wait_loads() {
 
 // The sums of one tile, from k = 0 to `depth`.  `buffers`: Tile::kShared bytes
 // of shared memory, free again when every wavefront has passed a barrier.
-template <int DT, class Tile, bool A_ALONG, bool B_ALONG>
+// WHOLE: the operands' rows lie on 16 bytes.
+template <int DT, class Tile, bool WHOLE, bool A_ALONG, bool B_ALONG>
 __device__ __forceinline__ void product(char* buffers, const char* a, uint64_t a_stride, uint64_t a_first,
                                         uint64_t a_limit, const char* b, uint64_t b_stride, uint64_t b_first,
                                         uint64_t b_limit, uint64_t depth, f32x4 (&sum)[Tile::TM][Tile::TN]) {
-    typedef Operand<DT, Tile::EM, Tile::kThreads, Tile::kStepBytes, A_ALONG> A;
-    typedef Operand<DT, Tile::EN, Tile::kThreads, Tile::kStepBytes, B_ALONG> B;
+    typedef Operand<DT, Tile::EM, Tile::kThreads, Tile::kStepBytes, WHOLE, A_ALONG> A;
+    typedef Operand<DT, Tile::EN, Tile::kThreads, Tile::kStepBytes, WHOLE, B_ALONG> B;
     // A step is worked off in parts: 64 bytes of k, and half of the squares of m.
     constexpr int kParts = Tile::kStepBytes / 32, kHalf = Tile::TM / 2;
     static_assert(Tile::TM % 2 == 0, "halves");

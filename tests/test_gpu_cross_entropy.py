@@ -170,8 +170,33 @@ def test_long_sums(ar, dtype, rows, cols, vocab):
 @pytest.mark.parametrize("pad,offset", [(1, 0), (0, 1), (3, 5), (8, 0), (0, 8), (8, 3)])
 @pytest.mark.parametrize("rows,cols", [(37, 64), (200, 40), (37, 61)])
 def test_strides_and_alignments(ar, dtype, rows, cols, pad, offset):
-    """Rows and starts off 16 bytes are copied, NaN beside the rows reaches nothing."""
+    """Rows and starts off 16 bytes; NaN beside the rows reaches nothing."""
     check(ar, np.random.default_rng(pad + offset), 2, rows, cols, 333, dtype, pad, offset)
+
+
+@pytest.mark.parametrize("rows,cols,vocab", [(50, 61, 40000), (64, 515, 9000), (32, 1003, 3000), (1, 2047, 500)])
+@pytest.mark.parametrize("pad,offset", [(0, 0), (2, 1)])
+def test_few_float32_rows_anywhere(ar, rows, cols, vocab, pad, offset):
+    """Few rows of float32 are read where they lie, in every tile that they get."""
+    check(ar, np.random.default_rng(rows), 2, rows, cols, vocab, "f32", pad, offset)
+
+
+@pytest.mark.parametrize("dtype,stride", [("f32", (1 << 21) + 1), ("f32", (1 << 21) + 4), ("bf16", (1 << 22) + 8)])
+@pytest.mark.parametrize("rows", [5, 40, 70])
+def test_rows_far_apart(ar, dtype, stride, rows):
+    """Rows of the weight too far apart for 32-bit offsets: the same bits as from rows without gaps."""
+    torch = _torch()
+    rng = np.random.default_rng(rows)
+    xs, weights = rows_of(rng, 1, rows, 64, dtype), rows_of(rng, 1, 70, 64, dtype)
+    targets = targets_of(rng, 1, rows, 70)
+    room = torch.full((69 * stride + 64,), math.nan, dtype=weights[0].dtype, device="cuda")
+    far = [torch.as_strided(room, (70, 64), (stride, 1)).copy_(weights[0])]
+    losses, lses = ar.ar_cross_entropy(xs, weights, targets)
+    far_losses, far_lses = ar.ar_cross_entropy(xs, far, targets)
+    assert torch.equal(losses[0], far_losses[0]) and torch.equal(lses[0], far_lses[0])
+    dxs, dws = ar.ar_cross_entropy_backward(None, xs, weights, targets, lses)
+    far_dxs, far_dws = ar.ar_cross_entropy_backward(None, xs, far, targets, lses)
+    assert torch.equal(dxs[0], far_dxs[0]) and torch.equal(dws[0], far_dws[0])
 
 
 @pytest.mark.parametrize("dtype,rows,vocab", [("bf16", 8200, 33000), ("f32", 4100, 18000), ("bf16", 20, 140000)])
