@@ -38,16 +38,17 @@ __device__ __forceinline__ int64_t index_at(const char* p, uint64_t i, int wide)
     return wide ? reinterpret_cast<const int64_t*>(p)[i] : reinterpret_cast<const int32_t*>(p)[i];
 }
 
-// The tiles that pick_tile chooses from.  The smallest one of float32 has a
-// buffer less, for a fourth workgroup on a compute unit beside three: 3 x 129
-// rows of 515 against 5,003, backward, 143 -> 134 us; 16 bits lose by it (16
-// rows of 4,096 against 65,536 112 + 444 -> 116 + 459 us), and two buffers cost
-// float32 there 832 -> 978 us.
+// The tiles that pick_tile chooses from.  The smallest one waits for memory most:
+// 16 bits have twice the k a step (16 rows of 1,024 against 8,192 10.5 -> 9.2 us,
+// 32 of 768 against 50,257, backward, 84 -> 81, the same elsewhere); float32 has
+// three short steps, so that four workgroups share a compute unit (3 x 129 rows
+// of 515 against 5,003, backward, 143 us with four -> 134; two cost 16 rows of
+// 4,096 against 65,536 832 -> 978).
 typedef TileOf<256, 256, 2, 4, 128, 2> LargeTile;
 typedef TileOf<128, 128, 4, 2, 128, 2> MediumTile;
 typedef TileOf<128, 64, 4, 1, 128, 3> SmallTile;
 template <int DT>
-using TinyTile = TileOf<64, 32, 2, 2, 128, DT == AR_FLOAT32 ? 3 : 4>;
+using TinyTile = TileOf<64, 32, 2, 2, DT == AR_FLOAT32 ? 128 : 256, 3>;
 
 // ---------------------------------------------------------------------------
 // forward

@@ -3,7 +3,7 @@
 // registers for the caller's epilogue.  Inline device code in an unnamed
 // namespace, so each kernel source gets its own copy.
 //
-// A workgroup brings 64 or 128 bytes of k of each of its rows of A and B to shared
+// A workgroup brings 128 or 256 bytes of k of each of its rows of A and B to shared
 // memory at a time (global_load_lds: 16 bytes a lane, no registers in between),
 // into one of several buffers while the matrix instructions work on another.  An
 // operand may lie along k (rows of A or B) or across (rows of k); shared memory
@@ -55,12 +55,13 @@ struct InShared {
     static constexpr int kEs = elem_size<DT>();
     static constexpr int kChunkElems = kChunk / kEs;
     static constexpr int kStep = kStepBytes / kEs;             // k at a time
+    static_assert(kStepBytes == 128 || kStepBytes == 256, "the exchange of chunks");
     static constexpr int kRowChunks = ALONG ? kStepBytes / kChunk : E * kEs / kChunk;
 
     // which chunk of a row stands at a place, and where a chunk stands
     static __device__ __forceinline__ int swap(int row, int chunk) {
         if constexpr (ALONG) {
-            return kStepBytes == 128 ? chunk ^ ((row >> 1) & 7) : chunk ^ ((row >> 2) & 3);
+            return kStepBytes == 256 ? chunk ^ (row & 15) : chunk ^ ((row >> 1) & 7);
         } else if constexpr (kEs == 2) {
             return chunk ^ (((row & 3) << 2) & (kRowChunks - 1));
         } else {
