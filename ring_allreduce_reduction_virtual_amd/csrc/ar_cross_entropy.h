@@ -64,14 +64,15 @@ constexpr uint64_t tile_n(CrossTile t) {
 }
 // The share of the large tile's rate that a tile reaches when it fills the GPU.
 // Measured on MI355X, TFLOP/s, tiny / small / medium / large: bf16, 2 x 4,096
-// rows of 4,096 against 65,536, forward 445 / 787 / 1,043 / 1,406, backward (6
-// per logit and column) 308 / 739 / 993 / 1,297; float32, 2 x 4,096 rows of
-// 2,048 against 32,768, forward (91 with two wavefronts) / 131 / 141 / 145.
-// Where the large tile leaves compute units without work the others are ahead:
-// bf16, 512 rows of 1,024 against 8,192, forward 33 / 19 / 16 / 28 us; 16 rows
-// of 4,096 against 65,536 133 / 127 / 146 / 155; float32, 3 x 129 rows of 515
-// against 5,003, forward and backward 56 + 142 (tiny and small), 62 + 165 with
-// the tiny tile rated at 0.6, 152 + 337 with the large tile alone.
+// rows of 4,096 against 65,536, forward 409 / 767 / 994 / 1,319, backward (6
+// per logit and column) 346 / 702 / 970 / 1,269; float32, 2 x 4,096 rows of
+// 2,048 against 32,768, forward 120 / 131 / 141 / 145, backward 117 / 130 / 139 /
+// 143.  Where the large tile leaves compute units without work the others are
+// ahead, us, forward and backward: bf16, 512 rows of 1,024 against 8,192 31 + 105 /
+// 20 + 70 / 17 + 64 / 28 + 93 (picked: 17 + 65); 16 rows of 4,096 against 65,536
+// 111 + 876 / 118 + 529 / 136 + 513 / 150 + 517 (picked: 110 + 447); float32, 3 x
+// 129 rows of 515 against 5,003 56 + 132 / 62 + 167 / 61 + 158 / 154 + 337
+// (picked: 56 + 132).
 inline double tile_rate(CrossTile t, bool wide) {
     switch (t) {
         case CrossTile::kLarge: return 1.0;
