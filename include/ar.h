@@ -738,9 +738,11 @@ size_t ar_embedding_workspace_bytes(size_t rows, size_t vocab, size_t cols, int 
  * `vocab` x `cols` (weight_stride apart), both of dtype, and
  *   lse[i] = log(sum over v of exp(z[i][v])),  loss[i] = lse[i] - z[i][t]
  * for the target t = targets[r][i].  loss[r] and lse[r] are `rows` float32
- * each; the backward pass needs lse.  A target equal to ignore_index gives
- * loss 0; any other outside [0, vocab) gives NaN.  A NaN or +infinity among a
- * row's logits makes its lse and loss NaN.  The vocabulary is worked off in
+ * each; the backward pass needs lse.  A loss is summed from the logits'
+ * difference, not from the rounded lse: beside large logits a small one stays.
+ * A target equal to ignore_index gives loss 0; any other outside [0, vocab)
+ * gives NaN.  A NaN or +infinity among a row's logits makes its lse and loss
+ * NaN.  The vocabulary is worked off in
  * pieces: products of 16-bit elements are summed in float32 by the matrix
  * cores (float32 ones too), maxima and sums of exponentials kept per piece and
  * joined in order.  Outputs overlap nothing else; ranks may share one weight.

@@ -169,14 +169,15 @@ __global__ void __launch_bounds__(256) k_cross_loss(CrossArgs a) {
     const float base = top == -INFINITY ? 0.0f : top;
     s = 0;
     for (int p = 0; p < 16; ++p) s += total[p][r] * __builtin_amdgcn_exp2f((most[p][r] - base) * kLog2e);
-    const float lse = base + __builtin_amdgcn_logf(s) * kLn2;
-    a.lse[rank][row] = lse;
+    const float rest = __builtin_amdgcn_logf(s) * kLn2;
+    a.lse[rank][row] = base + rest;
     const int64_t t = index_at(a.targets[rank], row, a.wide_index);
     float loss = as_f(0x7fc00000u);
     if (t == a.ignore) {
         loss = 0;
     } else if (t >= 0 && static_cast<uint64_t>(t) < a.vocab) {
-        loss = lse - a.target_logit[rank * a.rows + row];
+        // not lse - z: where the logits are large, lse has rounded a small loss away
+        loss = (base - a.target_logit[rank * a.rows + row]) + rest;
     }
     a.loss[rank][row] = loss;
 }

@@ -494,3 +494,32 @@ def test_refusals(ar):
         b(None, x, w, t, s, workspace=torch.zeros(need + 32, dtype=torch.uint8, device="cuda")[4:need + 4])
     with pytest.raises(ar.ArError, match="workspace"):
         b(None, x, w, t, s, workspace=torch.zeros(need - 1, dtype=torch.uint8, device="cuda"))
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("rows,vocab", [(8, 300), (8, 5000), (200, 5000)])
+def test_small_losses_of_large_logits(ar, dtype, rows, vocab):
+    """Logits of up to 8,192 whose differences every type holds: the loss keeps what lse, a large number, rounds away.
+
+    z = c (of the row) for the target and c - 12 for the others, exact in float32, so that the loss is
+    log(1 + (V - 1) e^-12) for every c.  Its exponentials' sum is off by U32 for every addition to a sum that holds the
+    target's 1 (32 of a lane, 4 across lanes and wavefronts, a tile in 16 and 16 joined: below V / 16 / 32 + 60) and as
+    much for the small ones' own (relative: V / 128 + 300, EXP and the argument's rounding, 2 * 12 U32); the logarithm
+    has EXP, and the last sum U32.
+    """
+    torch = _torch()
+    c = torch.tensor([2.0 ** (k % 8 - 7) for k in range(rows)])          # 1/128 to 1
+    x = torch.zeros(rows, 8)
+    x[:, 0], x[:, 1] = c, 1.0
+    w = torch.zeros(vocab, 8)
+    w[:, 0], w[:, 1] = 8192.0, -12.0
+    w[7, 1] = 0.0
+    t = torch.full((rows,), 7, device="cuda")
+    dt = torch_dtype(dtype)
+    (loss,), (lse,) = ar.ar_cross_entropy([x.to("cuda", dt)], [w.to("cuda", dt)], [t])
+    rest = (vocab - 1) * math.exp(-12)
+    want = math.log1p(rest)
+    off = (vocab / 512 + 60) * U32 + rest * ((vocab / 128 + 300 + 24) * U32 + EXP) + (EXP + U32) * want
+    assert (np.abs(f64(loss) - want) <= off).all(), (f64(loss) - want, off)
+    large = 8192 * f64(c) + want
+    assert (np.abs(f64(lse) - large) <= off + 2 * U32 * large).all()
