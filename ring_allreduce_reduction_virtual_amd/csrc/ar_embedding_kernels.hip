@@ -10,9 +10,11 @@
 // sorted by token, stably; the sorted order is cut into chunks of 8 or 32
 // places, and a group of threads adds up each chunk's rows of dy.  A token
 // whose places lie within one chunk is done there.  One that crosses a chunk's
-// end leaves a partial sum in each chunk, and a second launch adds these in
-// order: a frequent token is spread over as many groups as it has chunks, and
-// no token makes one group longer than another.  The launch that sums also
+// end leaves a partial sum in each chunk, so that in this launch a frequent
+// token is spread over as many groups as it has chunks; a second launch joins
+// the partial sums in order, one wavefront for a token's 256 columns, whose
+// chain grows with the token's places (a rank's 32,768 places under a 1/k law
+// 169 us for the whole gradient, all of one token 468).  The launch that sums also
 // writes the zeros of rows that no token names.  Writing the table bounds it: 8 x
 // 4,096 tokens into 8 x 32,768 rows of 4,096 bf16, 424 us for 2.4 GB (5.7 TB/s),
 // the sort 12.6 and the join 14.8.
@@ -467,6 +469,8 @@ __global__ void __launch_bounds__(256) k_embedding_sums(EmbeddingBackwardArgs a,
     }
 }
 
+constexpr uint32_t kJoinGroup = 256;   // partial sums
+
 // The tokens that cross the end of a chunk: a wavefront looks at one chunk's
 // end and 256 columns; where a token begins in that chunk and goes on, it adds
 // the partial sums up to the chunk where the token ends.
@@ -513,9 +517,32 @@ __global__ void __launch_bounds__(256) k_embedding_join(EmbeddingBackwardArgs a)
             }
             k += many.value;
         };
-        while (k + 16 <= last + 1) add(std::integral_constant<int, 16>{});
-        while (k + 4 <= last + 1) add(std::integral_constant<int, 4>{});
-        while (k <= last) add(std::integral_constant<int, 1>{});
+        // Added in groups, the groups' sums in groups again, and what those give: one
+        // chain would be off by as many roundings as there are partial sums, and after
+        // some 2^24 alike would no longer grow.
+        float groups[4] = {}, more[4] = {};
+        uint32_t count = 0;
+        for (uint64_t group = chunk;; group += kJoinGroup) {
+            const uint64_t end_of_group = std::min(last + 1, group + kJoinGroup);
+            while (k + 16 <= end_of_group) add(std::integral_constant<int, 16>{});
+            while (k + 4 <= end_of_group) add(std::integral_constant<int, 4>{});
+            while (k < end_of_group) add(std::integral_constant<int, 1>{});
+            if (k > last) break;
+            const bool full = ++count % kJoinGroup == 0;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                groups[j] += sum[j];
+                sum[j] = 0;
+                if (full) {
+                    more[j] += groups[j];
+                    groups[j] = 0;
+                }
+            }
+        }
+        if (count > 0) {   // else the sum as it is, the sign of a 0 with it
+#pragma unroll
+            for (int j = 0; j < 4; ++j) sum[j] = (more[j] + groups[j]) + sum[j];
+        }
         if (c < a.cols) write_row<TDT>(a, rank, token, c, 0, sum);
     }
 }

@@ -349,3 +349,22 @@ def test_most_tokens(ar):
     want = torch.full((vocab, 1), float(1 << 21), device="cuda")   # whole numbers below 2^24 throughout
     want[-1] -= 1
     assert torch.equal(got, want)
+
+
+@pytest.mark.parametrize("rows", [1 << 20, (1 << 22) + 8193 * 5 + 7])
+def test_one_token_of_a_million_places(ar, rows):
+    """All places of one token, with values whose partial sums are no whole numbers.
+
+    The sums are of 32 places, 256 of those, 256 of those again and the rest: as many roundings one after another, of
+    at most the whole sum (all terms are positive) each; the scale's product and the last sums add 4.  One chain of
+    all of a million places' partial sums is off by thousands.
+    """
+    torch = _torch()
+    values = torch.tensor([1 / (c + 3) for c in range(8)], device="cuda")
+    dy = values.expand(rows, 8).contiguous()
+    tokens = torch.full((rows,), 3, device="cuda")
+    (got,) = ar.ar_embedding_backward([dy], [tokens], 5)
+    want = values.double() * rows
+    off = (32 + 256 + 256 + rows / 32 / 65536 + 4) * U32 * want
+    assert ((got[3].double() - want).abs() <= off).all(), ((got[3].double() - want) / want / U32).tolist()
+    assert (got[[0, 1, 2, 4]] == 0).all()
