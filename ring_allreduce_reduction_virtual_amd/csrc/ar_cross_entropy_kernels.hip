@@ -143,43 +143,47 @@ __global__ void __launch_bounds__(Tile::kThreads) k_cross_stats(CrossArgs a, uin
     }
 }
 
-// lse and loss of 16 rows a workgroup: 16 threads a row, each over every 16th
-// tile of the vocabulary, then the 16 in order.
+// lse and loss of 16 rows a workgroup at a time: 16 threads a row, each over
+// every 16th tile of the vocabulary, then the 16 in order.
 __global__ void __launch_bounds__(256) k_cross_loss(CrossArgs a) {
     __shared__ float most[16][17], total[16][17];
     const int rank = blockIdx.y, r = threadIdx.x % 16, part = threadIdx.x / 16;
-    const uint64_t row = blockIdx.x * 16ull + r;
-    float top = -INFINITY, s = 0;
-    if (row < a.rows) {
-        const float* const from = a.partials + (static_cast<uint64_t>(rank) * a.tiles * a.rows + row) * 2;
+    for (uint64_t first = blockIdx.x * 16ull; first < a.rows; first += gridDim.x * 16ull) {
+        const uint64_t row = first + r;
+        float top = -INFINITY, s = 0;
+        if (row < a.rows) {
+            const float* const from = a.partials + (static_cast<uint64_t>(rank) * a.tiles * a.rows + row) * 2;
 #pragma unroll 8
-        for (uint32_t t = part; t < a.tiles; t += 16) {
-            const float2 each = *reinterpret_cast<const float2*>(from + t * a.rows * 2);
-            const float x = each.x, y = each.y;
-            const float higher = fmaxf(top, x), base = higher == -INFINITY ? 0.0f : higher;
-            s = s * __builtin_amdgcn_exp2f((top - base) * kLog2e) + y * __builtin_amdgcn_exp2f((x - base) * kLog2e);
-            top = higher;
+            for (uint32_t t = part; t < a.tiles; t += 16) {
+                const float2 each = *reinterpret_cast<const float2*>(from + t * a.rows * 2);
+                const float x = each.x, y = each.y;
+                const float higher = fmaxf(top, x), base = higher == -INFINITY ? 0.0f : higher;
+                s = s * __builtin_amdgcn_exp2f((top - base) * kLog2e) + y * __builtin_amdgcn_exp2f((x - base) * kLog2e);
+                top = higher;
+            }
         }
+        most[part][r] = top;
+        total[part][r] = s;
+        __syncthreads();
+        if (part == 0 && row < a.rows) {
+            for (int p = 1; p < 16; ++p) top = fmaxf(top, most[p][r]);
+            const float base = top == -INFINITY ? 0.0f : top;
+            s = 0;
+            for (int p = 0; p < 16; ++p) s += total[p][r] * __builtin_amdgcn_exp2f((most[p][r] - base) * kLog2e);
+            const float rest = __builtin_amdgcn_logf(s) * kLn2;
+            a.lse[rank][row] = base + rest;
+            const int64_t t = index_at(a.targets[rank], row, a.wide_index);
+            float loss = as_f(0x7fc00000u);
+            if (t == a.ignore) {
+                loss = 0;
+            } else if (t >= 0 && static_cast<uint64_t>(t) < a.vocab) {
+                // not lse - z: where the logits are large, lse has rounded a small loss away
+                loss = (base - a.target_logit[rank * a.rows + row]) + rest;
+            }
+            a.loss[rank][row] = loss;
+        }
+        __syncthreads();   // the next rows' maxima go to the same place
     }
-    most[part][r] = top;
-    total[part][r] = s;
-    __syncthreads();
-    if (part != 0 || row >= a.rows) return;
-    for (int p = 1; p < 16; ++p) top = fmaxf(top, most[p][r]);
-    const float base = top == -INFINITY ? 0.0f : top;
-    s = 0;
-    for (int p = 0; p < 16; ++p) s += total[p][r] * __builtin_amdgcn_exp2f((most[p][r] - base) * kLog2e);
-    const float rest = __builtin_amdgcn_logf(s) * kLn2;
-    a.lse[rank][row] = base + rest;
-    const int64_t t = index_at(a.targets[rank], row, a.wide_index);
-    float loss = as_f(0x7fc00000u);
-    if (t == a.ignore) {
-        loss = 0;
-    } else if (t >= 0 && static_cast<uint64_t>(t) < a.vocab) {
-        // not lse - z: where the logits are large, lse has rounded a small loss away
-        loss = (base - a.target_logit[rank * a.rows + row]) + rest;
-    }
-    a.loss[rank][row] = loss;
 }
 
 // ---------------------------------------------------------------------------
@@ -553,7 +557,8 @@ hipError_t launch_cross_stats(const CrossArgs& a, int nranks, CrossTile tile, ar
                 }))
 }
 hipError_t launch_cross_loss(const CrossArgs& a, int nranks, hipStream_t s) {
-    hipLaunchKernelGGL(k_cross_loss, dim3(tiles_of(a.rows, 16), nranks), dim3(256), 0, s, a);
+    const uint64_t blocks = std::min<uint64_t>(tiles_of(a.rows, 16), 16 * kMostBlocks);
+    hipLaunchKernelGGL(k_cross_loss, dim3(static_cast<unsigned>(blocks), nranks), dim3(256), 0, s, a);
     return hipGetLastError();
 }
 hipError_t launch_cross_live(const CrossArgs& a, int nranks, ar_dtype_t dtype, hipStream_t s) {

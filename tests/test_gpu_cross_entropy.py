@@ -523,3 +523,25 @@ def test_small_losses_of_large_logits(ar, dtype, rows, vocab):
     assert (np.abs(f64(loss) - want) <= off).all(), (f64(loss) - want, off)
     large = 8192 * f64(c) + want
     assert (np.abs(f64(lse) - large) <= off + 2 * U32 * large).all()
+
+
+def test_most_rows(ar):
+    """2^28 rows, the most: every grid at its largest.
+
+    Two logits, 0 and k / 4 for k of 0 to 4 by the row: exact; the loss of a sum of two terms is off by the
+    exponential's, the logarithm's and some 8 more roundings of numbers up to 2.
+    """
+    torch = _torch()
+    rows = 1 << 28
+    k = torch.arange(rows, dtype=torch.int32, device="cuda").remainder_(5)
+    x = torch.zeros(rows, 8, dtype=torch.bfloat16, device="cuda")
+    x[:, 0] = k
+    w = torch.zeros(2, 8, dtype=torch.bfloat16, device="cuda")
+    w[1, 0] = 0.25
+    t = (k % 2).int()
+    (loss,), (lse,) = ar.ar_cross_entropy([x], [w], [t])
+    want = torch.log1p(torch.exp(torch.arange(5, dtype=torch.float64, device="cuda") / 4))
+    for at in range(5):
+        mine = k == at
+        assert ((lse[mine] - want[at]).abs() <= 2 * (2 * EXP + 8 * U32)).all()
+        assert ((loss[mine] - (want[at] - (at % 2) * at / 4)).abs() <= 2 * (2 * EXP + 8 * U32)).all()
