@@ -748,9 +748,9 @@ size_t ar_embedding_workspace_bytes(size_t rows, size_t vocab, size_t cols, int 
  * joined in order.  Outputs overlap nothing else; ranks may share one weight.
  * rows == 0 is a successful no-op; cols == 0 means logits of 0.
  * `workspace`: at least ar_cross_entropy_workspace_bytes(...) bytes of device
- * memory, 16-byte aligned.  vocab of 1 to 2^31 - 1.  More than a launch can
- * count is refused; up to 2^25 rows, 2^36 rows x cols and 2^36 vocab x cols,
- * each of all ranks together, always fit. */
+ * memory, 16-byte aligned.  vocab of 1 to 2^31 - 1, cols up to 2^20, and up to
+ * 2^28 rows (of 32 ranks together, each rank's counted in whole 256); more is
+ * refused. */
 ar_result_t ar_cross_entropy(const void* const* x, const void* const* weight, const void* const* targets,
                              float* const* loss, float* const* lse, size_t rows, size_t vocab, size_t cols,
                              size_t x_stride, size_t weight_stride, ar_index_t index_type, long long ignore_index,
@@ -770,7 +770,9 @@ ar_result_t ar_cross_entropy(const void* const* x, const void* const* weight, co
  * take no part whatever x holds there: their dx is 0.  A target outside
  * [0, vocab) that is not ignored makes its row of dx, and dweight, NaN.
  * dx[r] may be x[r] with the same stride; outputs overlap nothing else.
- * The workspace as above, with the backward pass's size. */
+ * The workspace as above, with the backward pass's size.  More than a launch
+ * can count is refused; up to 2^25 rows, 2^36 rows x cols and 2^36 vocab x cols,
+ * each of all ranks together, always fit. */
 ar_result_t ar_cross_entropy_backward(const float* const* dloss, const void* const* x, const void* const* weight,
                                       const void* const* targets, const float* const* lse, void* const* dx,
                                       void* const* dweight, size_t rows, size_t vocab, size_t cols, size_t x_stride,

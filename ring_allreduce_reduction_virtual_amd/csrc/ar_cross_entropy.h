@@ -84,6 +84,13 @@ inline double tile_rate(CrossTile t, bool wide) {
 inline uint64_t tiles_in(uint64_t m, uint64_t n, CrossTile t) {
     return (m + tile_m(t) - 1) / tile_m(t) * ((n + tile_n(t) - 1) / tile_n(t));
 }
+constexpr uint64_t tile_threads(CrossTile t) { return t == CrossTile::kLarge || t == CrossTile::kMedium ? 512 : 256; }
+// A launch's threads are counted with 32 bits: the workgroups that it has, whole
+// eights of them (one for each XCD), and whether `batch` products of m x n fit.
+constexpr uint64_t most_blocks(CrossTile t) { return 0xffffffffull / tile_threads(t) / 8 * 8; }
+inline bool fits_launch(CrossTile t, uint64_t m, uint64_t n, uint64_t batch) {
+    return tiles_in(m, n, t) * batch <= most_blocks(t);
+}
 constexpr uint64_t kUnits = 256;   // compute units
 // Microseconds of `batch` products of m x n x depth: what the compute unit with
 // the most tiles takes, at the large tile's 5.3 (float32: 0.56) TFLOP/s each.
@@ -101,6 +108,13 @@ inline CrossTile pick_tile(uint64_t m, uint64_t n, uint64_t batch, bool wide) {
 }
 inline CrossTile forward_tile(uint64_t rows, uint64_t vocab, uint64_t es, int nranks) {
     return pick_tile(vocab, rows, nranks, es == 4);
+}
+// Columns of the vocabulary, whole tiles, that one forward launch has room for:
+// at least one tile while the ranks of a launch have no more than kMostRows rows
+// (2^31 / tile_n(tile) workgroups at most).
+constexpr uint64_t kMostRows = 1ull << 28;
+inline uint64_t launch_vocab(CrossTile t, uint64_t rows, int nranks) {
+    return most_blocks(t) / (tiles_in(1, rows, t) * nranks) * tile_m(t);
 }
 
 // A rank's row of a launch, in the order of the rows that take part.

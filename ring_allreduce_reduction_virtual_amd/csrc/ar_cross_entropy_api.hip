@@ -14,21 +14,25 @@ using namespace arimpl;
 namespace {
 
 constexpr uint64_t kMaxTokens = (1ull << 31) - 1, kMaxVocab = (1ull << 31) - 1, kMaxWidth = 1ull << 20;
-// Large tiles of one launch, whose threads are counted with 32 bits; few rows or
-// columns get up to eight small ones of 256 threads instead of each.
-constexpr uint64_t kMaxTiles = 1ull << 20;
-uint64_t large_tiles(uint64_t m, uint64_t n, uint64_t batch) { return tiles_in(m, n, CrossTile::kLarge) * batch; }
+// Rows of a launch's ranks, those of each rounded up to whole tiles.
+bool rows_fit(uint64_t rows, int nranks) {
+    return tiles_in(1, rows, CrossTile::kLarge) * nranks * tile_n(CrossTile::kLarge) <= kMostRows;
+}
 
-ar_result_t check_sizes(size_t rows, size_t vocab, size_t cols, ar_dtype_t dtype, int nranks) {
+ar_result_t check_sizes(size_t rows, size_t vocab, size_t cols, ar_dtype_t dtype, int nranks, bool backward) {
     const ar_result_t rc = check_types(dtype, dtype, "same", nranks);
     if (rc != AR_SUCCESS) return rc;
     if (vocab == 0) return fail_with(AR_ERR_INVALID_ARGUMENT, "a vocabulary of 0");
-    bool fits = rows <= kMaxTokens && vocab <= kMaxVocab && cols <= kMaxWidth;
-    if (fits) {   // the backward pass's launches; the forward pass's are cut to fit
-        const int n = std::min(nranks, kCrossRanks);
+    const int n = std::min(nranks, kCrossRanks);
+    bool fits = rows <= kMaxTokens && vocab <= kMaxVocab && cols <= kMaxWidth && rows_fit(rows, n);
+    if (fits && backward) {   // its launches; the forward pass's are cut to fit
         const uint64_t es = float_size(dtype), piece = piece_of(rows, vocab, es, n);
-        fits = large_tiles(piece, rows, n) <= kMaxTiles && large_tiles(piece, cols, n) <= kMaxTiles &&
-               large_tiles(cols, rows, n * dx_shape(rows, cols, piece, es, n).splits) <= kMaxTiles;
+        const bool wide = es == 4;
+        const DxShape dx = dx_shape(rows, cols, piece, es, n);
+        fits = fits_launch(pick_tile(piece, rows, n, wide), piece, rows, n) &&
+               fits_launch(dx.tile, cols, rows, static_cast<uint64_t>(n) * dx.splits) &&
+               fits_launch(pick_tile(cols, piece, n, wide), cols, piece, n) &&
+               fits_launch(pick_tile(cols, vocab % piece, n, wide), cols, vocab % piece, n);
     }
     if (!fits)
         return fail_with(AR_ERR_INVALID_ARGUMENT, "%llu rows of %llu columns against a vocabulary of %llu are too large",
@@ -125,7 +129,7 @@ extern "C" {
 size_t ar_cross_entropy_workspace_bytes(size_t rows, size_t vocab, size_t cols, ar_dtype_t dtype, int nranks,
                                         int backward) {
     set_error_detail("");
-    if (check_sizes(rows, vocab, cols, dtype, nranks) != AR_SUCCESS) return static_cast<size_t>(-1);
+    if (check_sizes(rows, vocab, cols, dtype, nranks, backward != 0) != AR_SUCCESS) return static_cast<size_t>(-1);
     return Layout(rows, vocab, cols, dtype, nranks, backward != 0).all;
 }
 
@@ -135,7 +139,7 @@ ar_result_t ar_cross_entropy(const void* const* x, const void* const* weight, co
                              ar_dtype_t dtype, int nranks, void* workspace, size_t workspace_bytes,
                              hipStream_t stream) {
     return guarded([&]() -> ar_result_t {
-        ar_result_t rc = check_sizes(rows, vocab, cols, dtype, nranks);
+        ar_result_t rc = check_sizes(rows, vocab, cols, dtype, nranks, false);
         if (rc != AR_SUCCESS || (rc = check_index(index_type)) != AR_SUCCESS ||
             (rc = check_stride(x_stride, rows, cols, "x_stride")) != AR_SUCCESS ||
             (rc = check_stride(weight_stride, vocab, cols, "weight_stride")) != AR_SUCCESS)
@@ -187,9 +191,9 @@ ar_result_t ar_cross_entropy(const void* const* x, const void* const* weight, co
             }
             // a weight that needs no copy is one piece, as far as one launch goes
             const bool as_is = weight_aligned || words;
-            const uint64_t most = kMaxTiles / large_tiles(1, rows, n) * kVocabTile;
+            const uint64_t most = launch_vocab(at.tile, rows, n);
             for (uint64_t first = 0; first < vocab;) {
-                const uint64_t count = std::min<uint64_t>(vocab - first, as_is ? most : at.piece);
+                const uint64_t count = std::min<uint64_t>(vocab - first, as_is ? most : std::min(most, at.piece));
                 rc = set_piece(a, at, ws, weight + g, n, first, count, weight_stride, as_is, dtype, stream);
                 if (rc == AR_SUCCESS)
                     rc = hip_result(launch_cross_stats(a, n, at.tile, dtype, stream), "cross_entropy launch");
@@ -209,7 +213,7 @@ ar_result_t ar_cross_entropy_backward(const float* const* dloss, const void* con
                                       ar_index_t index_type, long long ignore_index, ar_dtype_t dtype, double scale,
                                       int nranks, void* workspace, size_t workspace_bytes, hipStream_t stream) {
     return guarded([&]() -> ar_result_t {
-        ar_result_t rc = check_sizes(rows, vocab, cols, dtype, nranks);
+        ar_result_t rc = check_sizes(rows, vocab, cols, dtype, nranks, true);
         if (rc != AR_SUCCESS || (rc = check_index(index_type)) != AR_SUCCESS ||
             (rc = check_stride(x_stride, rows, cols, "x_stride")) != AR_SUCCESS ||
             (rc = check_stride(weight_stride, vocab, cols, "weight_stride")) != AR_SUCCESS ||

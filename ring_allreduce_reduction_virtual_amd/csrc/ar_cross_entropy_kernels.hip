@@ -425,16 +425,16 @@ __global__ void __launch_bounds__(256) k_cross_finish(CrossArgs a) {
 
 constexpr uint64_t kMostBlocks = 1u << 16;
 
-// A launch's threads are counted with 32 bits (the host has checked sizes for
-// large tiles, which these sizes get).
-bool fits_launch(uint64_t blocks, int threads) { return blocks * threads <= 0xffffffffull; }
-
 uint32_t tiles_of(uint64_t n, int tile) { return static_cast<uint32_t>((n + tile - 1) / tile); }
 
 template <class Tile>
 constexpr bool is_tile(CrossTile t) {
-    return static_cast<uint64_t>(Tile::EM) == tile_m(t) && static_cast<uint64_t>(Tile::EN) == tile_n(t);
+    return static_cast<uint64_t>(Tile::EM) == tile_m(t) && static_cast<uint64_t>(Tile::EN) == tile_n(t) &&
+           static_cast<uint64_t>(Tile::kThreads) == tile_threads(t);
 }
+// Workgroups of one launch, which the host keeps to.
+template <class Tile>
+constexpr uint64_t kMostTiles = 0xffffffffull / Tile::kThreads;
 static_assert(kMostStride == kMostOperandStride && kCrossRanks <= 64, "the host's operands");
 static_assert(is_tile<LargeTile>(CrossTile::kLarge) && is_tile<MediumTile>(CrossTile::kMedium) &&
                   is_tile<SmallTile>(CrossTile::kSmall) && is_tile<TinyTile<AR_FLOAT32>>(CrossTile::kTiny),
@@ -460,7 +460,7 @@ template <int DT, class Tile>
 hipError_t start_stats(const CrossArgs& a, int nranks, hipStream_t s) {
     const uint32_t tiles_m = tiles_of(a.count, Tile::EM), tiles_n = tiles_of(a.rows, Tile::EN);
     const uint64_t blocks = tile_blocks(static_cast<uint64_t>(tiles_m) * tiles_n * nranks);
-    if (!fits_launch(blocks, Tile::kThreads)) return hipErrorInvalidValue;
+    if (blocks > kMostTiles<Tile>) return hipErrorInvalidValue;
     return by_rows<DT, Tile>(a, [&](auto whole) {
         hipLaunchKernelGGL((k_cross_stats<DT, Tile, whole.value>), dim3(static_cast<unsigned>(blocks)),
                            dim3(Tile::kThreads), 0, s, a, tiles_m, tiles_n, static_cast<uint32_t>(nranks));
@@ -482,7 +482,7 @@ template <int DT, class Tile>
 hipError_t start_dz(const CrossArgs& a, int nranks, hipStream_t s) {
     const uint32_t tiles_m = tiles_of(a.piece, Tile::EM), tiles_n = tiles_of(a.rows, Tile::EN);
     const uint64_t blocks = tile_blocks(static_cast<uint64_t>(tiles_m) * tiles_n * nranks);
-    if (!fits_launch(blocks, Tile::kThreads)) return hipErrorInvalidValue;
+    if (blocks > kMostTiles<Tile>) return hipErrorInvalidValue;
     return by_rows<DT, Tile>(a, [&](auto whole) {
         hipLaunchKernelGGL((k_cross_dz<DT, Tile, whole.value>), dim3(static_cast<unsigned>(blocks)),
                            dim3(Tile::kThreads), 0, s, a, padded_cols(a.cols, elem_size<DT>()), tiles_m,
@@ -494,7 +494,7 @@ template <int DT, class Tile>
 hipError_t start_dx(const CrossArgs& a, int nranks, bool add, hipStream_t s) {
     const uint32_t tiles_m = tiles_of(a.cols, Tile::EM), tiles_n = tiles_of(a.rows, Tile::EN);
     const uint64_t blocks = tile_blocks(static_cast<uint64_t>(tiles_m) * tiles_n * nranks * a.splits);
-    if (!fits_launch(blocks, Tile::kThreads)) return hipErrorInvalidValue;
+    if (blocks > kMostTiles<Tile>) return hipErrorInvalidValue;
     return by_rows<DT, Tile>(a, [&](auto whole) {
         hipLaunchKernelGGL((k_cross_dx<DT, Tile, whole.value>), dim3(static_cast<unsigned>(blocks)),
                            dim3(Tile::kThreads), 0, s, a, add ? 1 : 0, tiles_m, static_cast<uint32_t>(nranks));
@@ -505,7 +505,7 @@ template <int DT, class Tile>
 hipError_t start_dweight(const CrossArgs& a, int nranks, hipStream_t s) {
     const uint32_t tiles_m = tiles_of(a.cols, Tile::EM), tiles_n = tiles_of(a.count, Tile::EN);
     const uint64_t blocks = tile_blocks(static_cast<uint64_t>(tiles_m) * tiles_n * nranks);
-    if (!fits_launch(blocks, Tile::kThreads)) return hipErrorInvalidValue;
+    if (blocks > kMostTiles<Tile>) return hipErrorInvalidValue;
     hipLaunchKernelGGL((k_cross_dweight<DT, Tile>), dim3(static_cast<unsigned>(blocks)), dim3(Tile::kThreads), 0, s, a,
                        padded_cols(a.cols, elem_size<DT>()), tiles_m, tiles_n, static_cast<uint32_t>(nranks));
     return hipGetLastError();

@@ -250,3 +250,30 @@ def test_cross_entropy_launches_fit(lib):
         assert lib.ar_cross_entropy_workspace_bytes(1 << 28, 64, 8, BF16, 1, backward) not in (0, NONE)
         assert lib.ar_cross_entropy_workspace_bytes((1 << 28) + 1, 64, 8, BF16, 1, backward) == NONE
         assert lib.ar_cross_entropy_workspace_bytes(1 << 29, 64, 8, BF16, 1, backward) == NONE
+
+
+def test_cross_entropy_sizes_that_always_fit(lib):
+    """2^25 rows, 2^36 rows x columns and 2^36 vocabulary x columns of all ranks together, the largest that each
+    shape has room for, in every tile's odd sizes: neither pass refuses any.  The forward pass's own limit is 2^28 rows,
+    whatever the columns are (its launches are cut)."""
+    import random
+
+    rng = random.Random(0)
+    cases = [(32, 1, 4_000_000, 513), (32, 129, 8_000_000, 4), (1, 129, 240_000_000, 4), (1, 1, (1 << 27) - 5, 513),
+             (1, 1 << 25, 100, 2048), (32, 1 << 20, 1, 1), (1, 1 << 25, (1 << 31) - 1, 1), (128, 1, 513, 1 << 20)]
+    edges = [1, 2, 31, 33, 64, 65, 129, 160, 161, 192, 193, 257, 320, 385, 513, 640, 769, 1025]
+    for _ in range(4000):
+        n = rng.choice((1, 2, 5, 31, 32, 33, 128))
+        some = lambda most: min(most, rng.choice((rng.choice(edges), int(2 ** rng.uniform(0, 31)), most)))   # noqa: E731
+        cols = some(min(1 << 20, (1 << 36) // n))
+        rows = some(min((1 << 25) // n, (1 << 36) // (n * cols)))
+        vocab = some(min((1 << 31) - 1, (1 << 36) // (n * cols)))
+        cases.append((n, rows, vocab, cols))
+    for n, rows, vocab, cols in cases:
+        for dt in (F32, BF16, F16):
+            for backward in (0, 1):
+                got = lib.ar_cross_entropy_workspace_bytes(rows, vocab, cols, dt, n, backward)
+                assert got != NONE, (n, rows, vocab, cols, dt, backward)
+    for dt in (F32, BF16):
+        for n, rows in ((1, 1 << 28), (32, 1 << 23)):
+            assert lib.ar_cross_entropy_workspace_bytes(rows, (1 << 31) - 1, 16, dt, n, 0) != NONE

@@ -545,3 +545,24 @@ def test_most_rows(ar):
         mine = k == at
         assert ((lse[mine] - want[at]).abs() <= 2 * (2 * EXP + 8 * U32)).all()
         assert ((loss[mine] - (want[at] - (at % 2) * at / 4)).abs() <= 2 * (2 * EXP + 8 * U32)).all()
+
+
+def test_more_tiles_than_a_launch_counts(ar):
+    """129 rows of float32 against 240,000,000 words: 18,750,000 tiles of 64 x 32, which take two launches.
+
+    All logits are 0 but the last word's 20: the sums of ones are whole multiples of a tile's 64, below 2^24 of them, and
+    exact; what the exponentials and the join of 16 sums add is below 30 U32 of the sum, the logarithm and the last sums
+    10 U32 of 20.
+    """
+    torch = _torch()
+    rows, vocab = 129, 240_000_000
+    x = torch.zeros(rows, 4, device="cuda")
+    x[:, 0] = torch.arange(rows, device="cuda") % 2
+    w = torch.zeros(vocab, 4, device="cuda")
+    w[-1, 0] = 20.0
+    t = torch.full((rows,), vocab - 1, device="cuda")
+    (loss,), (lse,) = ar.ar_cross_entropy([x], [w], [t])
+    for odd in (0, 1):
+        want = math.log(math.exp(20.0 * odd) + vocab - 1)
+        off = 30 * U32 + 10 * U32 * 20
+        assert (np.abs(f64(lse)[odd::2] - want) <= off).all() and (np.abs(f64(loss)[odd::2] - (want - 20 * odd)) <= off).all()
