@@ -747,8 +747,8 @@ size_t ar_embedding_workspace_bytes(size_t rows, size_t vocab, size_t cols, int 
  * cores (float32 ones too), maxima and sums of exponentials kept per piece and
  * joined in order.  Outputs overlap nothing else; ranks may share one weight.
  * rows == 0 is a successful no-op; cols == 0 means logits of 0.
- * `workspace`: at least ar_cross_entropy_workspace_bytes(...) bytes of device
- * memory, 16-byte aligned.  vocab of 1 to 2^31 - 1, cols up to 2^20, and up to
+ * `workspace`: at least ar_cross_entropy_workspace_bytes(...) bytes (or fewer,
+ * see there) of device memory, 16-byte aligned.  vocab of 1 to 2^31 - 1, cols up to 2^20, and up to
  * 2^28 rows (of 32 ranks together, each rank's counted in whole 256); more is
  * refused. */
 ar_result_t ar_cross_entropy(const void* const* x, const void* const* weight, const void* const* targets,
@@ -779,9 +779,20 @@ ar_result_t ar_cross_entropy_backward(const float* const* dloss, const void* con
                                       size_t weight_stride, size_t dx_stride, size_t dweight_stride,
                                       ar_index_t index_type, long long ignore_index, ar_dtype_t dtype, double scale,
                                       int nranks, void* workspace, size_t workspace_bytes, hipStream_t stream);
-/* backward: not 0 for the backward pass.  (size_t)-1 for invalid arguments. */
+/* backward: not 0 for the backward pass.  (size_t)-1 for invalid arguments.
+ * The first size is enough for any operands, with room for copies of those that
+ * the matrix products cannot read where they lie.  The second is what a call
+ * needs whose weights (in the forward pass, and x) all start on 16 bytes and
+ * have rows of whole 16 bytes, a multiple of 16 and at most 8 MiB apart: no
+ * copies.  The forward pass then keeps at most 8 bytes per row and 64 words of
+ * the vocabulary, and 4 per row; the backward pass x's rows, dx's float32 sums
+ * (up to 64 times, where few rows need the sum over the vocabulary cut) and a
+ * piece of dz, at most 512 MiB or 2,048 words of each row.  All of this is of 32
+ * ranks at a time. */
 size_t ar_cross_entropy_workspace_bytes(size_t rows, size_t vocab, size_t cols, ar_dtype_t dtype, int nranks,
                                         int backward);
+size_t ar_cross_entropy_aligned_workspace_bytes(size_t rows, size_t vocab, size_t cols, ar_dtype_t dtype, int nranks,
+                                                int backward);
 
 /* Activations in 8 bits.  A block is AR_ACTIVATION_BLOCK consecutive elements
  * of a row (the row's last one may be short).  It has a scale byte e, worth

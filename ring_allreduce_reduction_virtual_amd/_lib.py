@@ -41,6 +41,7 @@ EXPORTS = (
     "ar_layer_norm", "ar_layer_norm_backward", "ar_layer_norm_workspace_bytes",
     "ar_embedding", "ar_embedding_backward", "ar_embedding_workspace_bytes",
     "ar_cross_entropy", "ar_cross_entropy_backward", "ar_cross_entropy_workspace_bytes",
+    "ar_cross_entropy_aligned_workspace_bytes",
     "ar_pack_activations", "ar_unpack_activations", "ar_layer_norm_backward_packed",
 )
 # the training-step operators' enums and constants
@@ -131,6 +132,7 @@ def _declare(lib):
         "ar_cross_entropy_backward": (_int, [_vpp] * 7 + [_sz] * 7 + [_int, ctypes.c_longlong, _int, ctypes.c_double,
                                                                       _int, _vp, _sz, _vp]),
         "ar_cross_entropy_workspace_bytes": (_sz, [_sz, _sz, _sz, _int, _int, _int]),
+        "ar_cross_entropy_aligned_workspace_bytes": (_sz, [_sz, _sz, _sz, _int, _int, _int]),
         "ar_pack_activations": (_int, [_vpp] * 3 + [_sz] * 3 + [_int, _int, _vp]),
         "ar_unpack_activations": (_int, [_vpp] * 3 + [_sz] * 3 + [_int, _int, _vp]),
         "ar_layer_norm_backward_packed": (_int, [_vpp] * 9 + [_sz] * 4 + [_int, _int, _int, _vp, _sz, _vp]),

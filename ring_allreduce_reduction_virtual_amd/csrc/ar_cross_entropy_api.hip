@@ -41,7 +41,8 @@ ar_result_t check_sizes(size_t rows, size_t vocab, size_t cols, ar_dtype_t dtype
     return AR_SUCCESS;
 }
 
-// The parts of the workspace, in bytes from its start.
+// The parts of the workspace, in bytes from its start.  `aligned`: no operand
+// needs a copy.
 struct Layout {
     uint64_t piece = 0, padded = 0, all = 0;
     uint64_t x = 0, weight = 0;                                                    // aligned copies, or live rows
@@ -56,11 +57,11 @@ struct Layout {
         all += (bytes + 255) / 256 * 256;
         return at;
     }
-    Layout(uint64_t rows, uint64_t vocab, uint64_t cols, ar_dtype_t dtype, int nranks, bool backward) {
+    Layout(uint64_t rows, uint64_t vocab, uint64_t cols, ar_dtype_t dtype, int nranks, bool backward, bool aligned) {
         const uint64_t n = static_cast<uint64_t>(std::min(nranks, kCrossRanks)), es = float_size(dtype);
         piece = piece_of(rows, vocab, es, static_cast<int>(n));
         padded = padded_cols(cols, es);
-        const bool copies = !in_words(rows, es, backward);
+        const bool copies = !aligned && !in_words(rows, es, backward);
         if (backward || copies) x = take(n * rows * padded * es);
         if (copies) weight = take(n * std::min(piece, vocab) * padded * es);
         if (backward) {
@@ -130,7 +131,15 @@ size_t ar_cross_entropy_workspace_bytes(size_t rows, size_t vocab, size_t cols, 
                                         int backward) {
     set_error_detail("");
     if (check_sizes(rows, vocab, cols, dtype, nranks, backward != 0) != AR_SUCCESS) return static_cast<size_t>(-1);
-    return Layout(rows, vocab, cols, dtype, nranks, backward != 0).all;
+    return Layout(rows, vocab, cols, dtype, nranks, backward != 0, false).all;
+}
+
+size_t ar_cross_entropy_aligned_workspace_bytes(size_t rows, size_t vocab, size_t cols, ar_dtype_t dtype, int nranks,
+                                                int backward) {
+    set_error_detail("");
+    if (check_sizes(rows, vocab, cols, dtype, nranks, backward != 0) != AR_SUCCESS) return static_cast<size_t>(-1);
+    const bool can_be = cols * float_size(dtype) % kOperandBytes == 0;
+    return Layout(rows, vocab, cols, dtype, nranks, backward != 0, can_be).all;
 }
 
 ar_result_t ar_cross_entropy(const void* const* x, const void* const* weight, const void* const* targets,
@@ -158,7 +167,8 @@ ar_result_t ar_cross_entropy(const void* const* x, const void* const* weight, co
                 (rc = add_range(v, lse[r], rows * 4, 4, true, "lse", r)) != AR_SUCCESS)
                 return rc;
         }
-        const Layout at(rows, vocab, cols, dtype, nranks, false);
+        const bool all_aligned = aligned(x, nranks, x_stride, cols, es) && aligned(weight, nranks, weight_stride, cols, es);
+        const Layout at(rows, vocab, cols, dtype, nranks, false, all_aligned);
         if ((rc = add_scratch(v, workspace, workspace_bytes, at.all, 16)) != AR_SUCCESS) return rc;
         if ((rc = check_ranges(v)) != AR_SUCCESS) return rc;
         char* const ws = static_cast<char*>(workspace);
@@ -244,7 +254,7 @@ ar_result_t ar_cross_entropy_backward(const float* const* dloss, const void* con
                  (rc = add_rows(v, dweight[r], vocab, cols, dweight_stride, es, true, "dweight", r)) != AR_SUCCESS))
                 return rc;
         }
-        const Layout at(rows, vocab, cols, dtype, nranks, true);
+        const Layout at(rows, vocab, cols, dtype, nranks, true, aligned(weight, nranks, weight_stride, cols, es));
         if ((rc = add_scratch(v, workspace, workspace_bytes, at.all, 16)) != AR_SUCCESS) return rc;
         if ((rc = check_ranges(v)) != AR_SUCCESS) return rc;
         if (cols == 0 || (dx == nullptr && dweight == nullptr) || (rows == 0 && dweight == nullptr)) return AR_SUCCESS;

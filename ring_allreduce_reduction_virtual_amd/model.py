@@ -136,12 +136,20 @@ def ar_embedding_backward(dys, tokens, vocab=None, dtables=None, scale: float = 
 # --------------------------------------------------------------------------
 
 def ar_cross_entropy_workspace_bytes(rows: int, vocab: int, cols: int, dtype: str, nranks: int,
-                                     backward: bool = False) -> int:
-    v = _lib.lib().ar_cross_entropy_workspace_bytes(rows, vocab, cols, _lib.DTYPES[dtype], nranks, 1 if backward else 0)
+                                     backward: bool = False, aligned: bool = False) -> int:
+    """Enough for any operands; with `aligned`, for those whose rows lie on 16 bytes (include/ar.h), which need no copies."""
+    name = "ar_cross_entropy_aligned_workspace_bytes" if aligned else "ar_cross_entropy_workspace_bytes"
+    v = getattr(_lib.lib(), name)(rows, vocab, cols, _lib.DTYPES[dtype], nranks, 1 if backward else 0)
     if v == ctypes.c_size_t(-1).value:
         raise ValueError("invalid arguments for ar_cross_entropy_workspace_bytes: "
                          + _lib.lib().ar_get_last_error_detail().decode())
     return v
+
+
+def _aligned(addresses, n, stride, cols, es):
+    """Whether the ranks' operands need no copy: rows on 16 bytes, of whole 16 bytes and at most 8 MiB apart."""
+    return ((stride * es | cols * es) % 16 == 0 and stride * es <= 1 << 23
+            and all((addresses[r] or 0) % 16 == 0 for r in range(n)))
 
 
 def _flat_floats(tensors, n, dev, index, rows, what):
@@ -187,8 +195,10 @@ def ar_cross_entropy(xs, weights, targets, losses=None, lses=None, ignore_index:
         made = [None, None] if all(g is not None for g in given) else _new_parts((n, rows), torch.float32, dev, stream)
         losses, lp = made if losses is None else (losses, _flat_floats(losses, n, dev, index, rows, "losses"))
         lses, sp = made if lses is None else (lses, _flat_floats(lses, n, dev, index, rows, "lses"))
+    if workspace is None:
+        aligned = all(_aligned(p, n, s, shape[2], x0.element_size()) for p, s in zip(inputs, strides))
+        workspace = _scratch(ar_cross_entropy_workspace_bytes(*shape, name, n, False, aligned), None, dev, stream)
     with _on_device(dev):
-        workspace = _scratch(ar_cross_entropy_workspace_bytes(*shape, name, n), workspace, dev, stream)
         wp, wb = _ws(workspace, dev)
         rc = _lib.lib().ar_cross_entropy(*inputs, lp, sp, *shape, *strides, index_type, ignore_index,
                                          _lib.DTYPES[name], n, wp, wb, _stream_handle(stream, dev.index))
@@ -219,8 +229,10 @@ def ar_cross_entropy_backward(dlosses, xs, weights, targets, lses, dxs=None, dwe
         dxs, gx, x_stride = _out_rows(dxs, (rows, cols), n, dt, dev, index, "dxs", stream)
     if dweights is not None or weight_grads:
         dweights, gw, w_stride = _out_rows(dweights, (vocab, cols), n, dt, dev, index, "dweights", stream)
+    if workspace is None:
+        aligned = _aligned(inputs[1], n, strides[1], cols, x0.element_size())
+        workspace = _scratch(ar_cross_entropy_workspace_bytes(*shape, name, n, True, aligned), None, dev, stream)
     with _on_device(dev):
-        workspace = _scratch(ar_cross_entropy_workspace_bytes(*shape, name, n, True), workspace, dev, stream)
         wp, wb = _ws(workspace, dev)
         rc = _lib.lib().ar_cross_entropy_backward(dp, *inputs, sp, gx, gw, *shape, *strides, x_stride, w_stride,
                                                   index_type, ignore_index, _lib.DTYPES[name], scale, n, wp, wb,

@@ -277,3 +277,46 @@ def test_cross_entropy_sizes_that_always_fit(lib):
     for dt in (F32, BF16):
         for n, rows in ((1, 1 << 28), (32, 1 << 23)):
             assert lib.ar_cross_entropy_workspace_bytes(rows, (1 << 31) - 1, 16, dt, n, 0) != NONE
+
+
+def needed(lib):
+    """What the last error said that the call needs."""
+    said = re.search(r"needs a workspace of (\d+) bytes", detail(lib))
+    assert said, detail(lib)
+    return int(said.group(1))
+
+
+@pytest.mark.parametrize("dt", [F32, BF16])
+@pytest.mark.parametrize("rows,vocab,cols", [(1, 1, 8), (16, 65536, 4096), (129, 5003, 520), (4096, 65536, 4096),
+                                             (4096, 131072, 8192), (131072, 50257, 768), (3, 1 << 22, 64)])
+@pytest.mark.parametrize("n", [1, 8, 33])
+def test_cross_entropy_workspace_without_copies(lib, dt, rows, vocab, cols, n):
+    """Operands on 16 bytes need room for no copy: forward for 8 bytes per row and 64 words (4 per row beside), backward
+    for x's rows, dz's piece and dx's sums; and a call asks for just that."""
+    es, ranks = 4 if dt == F32 else 2, min(n, 32)
+    forward = lib.ar_cross_entropy_aligned_workspace_bytes(rows, vocab, cols, dt, n, 0)
+    back = lib.ar_cross_entropy_aligned_workspace_bytes(rows, vocab, cols, dt, n, 1)
+    assert 0 < forward <= ranks * rows * (-(-vocab // 64) * 8 + 4) + 512
+    piece = max(512 << 20, ranks * rows * 2048 * es)
+    dz = min(piece, ranks * rows * vocab * es) + ranks * rows * 256 * es
+    splits = 64 if rows <= 256 else 8
+    assert 0 < back <= dz + ranks * rows * (cols * es + splits * cols * 4 + 64) + 2048
+    spans = [BASE + k * (GAP << 4) for k in range(8 * n)]                # 1 TiB apart
+    ptr = lambda k: spans[k * n:(k + 1) * n]                             # noqa: E731
+    ws = BASE - (GAP << 4)
+    for x, w, aligned, aligned_back in ((0, 0, True, True), (es, 0, False, True), (0, es, False, False)):
+        xs, wst = cols + (8 if x == 0 else 1), cols
+        at = dict(x=[p + x for p in ptr(0)], w=[p + w for p in ptr(1)], t=ptr(2), lse=ptr(3), rows=rows, vocab=vocab,
+                  cols=cols, xs=xs, wst=wst, dt=dt, n=n, ws=ws, have=15)
+        assert cross(lib, loss=ptr(4), **at) == INVALID
+        need = needed(lib)
+        any_operands = lib.ar_cross_entropy_workspace_bytes(rows, vocab, cols, dt, n, 0)
+        assert forward <= any_operands and (need == forward if aligned else forward <= need <= any_operands)
+        assert cross_back(lib, dl=ptr(5), dx=ptr(6), dw=ptr(7), dxs=cols, dws=cols, **at) == INVALID
+        need = needed(lib)
+        any_operands = lib.ar_cross_entropy_workspace_bytes(rows, vocab, cols, dt, n, 1)
+        assert back <= any_operands and (need == back if aligned_back else 0 < need <= any_operands)
+    # rows that are no whole 16 bytes need copies wherever they lie
+    assert (lib.ar_cross_entropy_aligned_workspace_bytes(rows, vocab, cols + 1, dt, n, 0)
+            == lib.ar_cross_entropy_workspace_bytes(rows, vocab, cols + 1, dt, n, 0))
+    assert lib.ar_cross_entropy_aligned_workspace_bytes(rows, 0, cols, dt, n, 1) == NONE

@@ -566,3 +566,32 @@ def test_more_tiles_than_a_launch_counts(ar):
         want = math.log(math.exp(20.0 * odd) + vocab - 1)
         off = 30 * U32 + 10 * U32 * 20
         assert (np.abs(f64(lse)[odd::2] - want) <= off).all() and (np.abs(f64(loss)[odd::2] - (want - 20 * odd)) <= off).all()
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_few_rows_take_little_memory(ar, dtype):
+    """16 rows against 131 to 262 MB of weight that lies on 16 bytes: no copy of it is made room for."""
+    torch = _torch()
+    rng = np.random.default_rng(16)
+    xs, weights = rows_of(rng, 1, 16, 1024, dtype, 8), rows_of(rng, 1, 64000, 1024, dtype, 8)
+    targets = targets_of(rng, 1, 16, 64000)
+    losses, lses = ar.ar_cross_entropy(xs, weights, targets)
+    dws = [torch.empty_like(weights[0])]
+    most = {}
+    for name, call in (("forward", lambda: ar.ar_cross_entropy(xs, weights, targets)),
+                       ("backward", lambda: ar.ar_cross_entropy_backward(None, xs, weights, targets, lses, dweights=dws))):
+        call()
+        torch.cuda.synchronize()
+        torch.cuda.reset_peak_memory_stats()
+        before = torch.cuda.memory_allocated()
+        call()
+        most[name] = torch.cuda.max_memory_allocated() - before
+    logits = 16 * 64000 * 4
+    # forward: 8 bytes per row and 64 words; backward: dz, 64 splits of dx's sums and the rest, which is x's size
+    assert most["forward"] <= logits / 16 and most["backward"] <= 2 * logits + 64 * 16 * 1024 * 4
+    # a workspace of the size for any operands serves as well
+    for aligned in (False, True):
+        ws = torch.empty(ar.ar_cross_entropy_workspace_bytes(16, 64000, 1024, dtype, 1, False, aligned), dtype=torch.uint8,
+                         device="cuda")
+        again = ar.ar_cross_entropy(xs, weights, targets, workspace=ws)
+        assert torch.equal(again[0][0], losses[0]) and torch.equal(again[1][0], lses[0])
