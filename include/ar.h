@@ -781,14 +781,15 @@ ar_result_t ar_cross_entropy_backward(const float* const* dloss, const void* con
                                       int nranks, void* workspace, size_t workspace_bytes, hipStream_t stream);
 /* backward: not 0 for the backward pass.  (size_t)-1 for invalid arguments.
  * The first size is enough for any operands, with room for copies of those that
- * the matrix products cannot read where they lie.  The second is what a call
- * needs whose weights (in the forward pass, and x) all start on 16 bytes and
- * have rows of whole 16 bytes, a multiple of 16 and at most 8 MiB apart: no
- * copies.  The forward pass then keeps at most 8 bytes per row and 64 words of
- * the vocabulary, and 4 per row; the backward pass x's rows, dx's float32 sums
- * (up to 64 times, where few rows need the sum over the vocabulary cut) and a
- * piece of dz, at most 512 MiB or 2,048 words of each row.  All of this is of 32
- * ranks at a time. */
+ * the matrix products cannot read where they lie: x, and a piece of the weights
+ * (128 MiB or what gives each compute unit a tile; backward 256 MiB, that or
+ * 2,048 words of each).  The second is what a call needs whose weights (in the
+ * forward pass, and x) all start on 16 bytes and have rows of whole 16 bytes, a
+ * multiple of 16 and at most 8 MiB apart: no copies.  The forward pass then keeps
+ * at most 8 bytes per row and 64 words of the vocabulary, and 4 per row; the
+ * backward pass x's rows, dx's float32 sums (up to 64 times, where few rows need
+ * the sum over the vocabulary cut) and a piece of dz, at most 512 MiB or 2,048
+ * words of each row.  All of this is of 32 ranks at a time. */
 size_t ar_cross_entropy_workspace_bytes(size_t rows, size_t vocab, size_t cols, ar_dtype_t dtype, int nranks,
                                         int backward);
 size_t ar_cross_entropy_aligned_workspace_bytes(size_t rows, size_t vocab, size_t cols, ar_dtype_t dtype, int nranks,

@@ -38,22 +38,7 @@ constexpr bool in_words(uint64_t rows, uint64_t es, bool backward) {
     return es == 4 && rows <= (backward ? kWordRowsBackward : kWordRows);
 }
 
-// The backward pass works the vocabulary off in pieces of whole tiles, so that
-// what it keeps of dz is bounded whatever the vocabulary is: kPieceBytes in all,
-// or kLeastPiece columns.  Every piece more reads and writes dx's float32 sums
-// once more.  ms with 128 / 256 / 512 / 1,024 MiB, bf16: 2 x 4,096 rows of 4,096
-// against 65,536 10.5 / 10.45 / 10.45 / 10.4, 8 x 2,048 rows of 768 against
-// 50,257 4.41 / 4.34 / 4.27 / 4.05, 4 x 4,096 of 2,048 against 32,768 5.78 /
-// 5.63 / 5.56 / 5.56.
-constexpr uint64_t kVocabTile = 256;
-constexpr uint64_t kPieceBytes = 512ull << 20, kLeastPiece = 2048;
-inline uint64_t piece_of(uint64_t rows, uint64_t vocab, uint64_t es, int nranks) {
-    const uint64_t tiles = (vocab + kVocabTile - 1) / kVocabTile;
-    const uint64_t row_bytes = std::max<uint64_t>(1, rows) * nranks * es;
-    const uint64_t most = std::min(std::max(kLeastPiece, kPieceBytes / row_bytes), kMostOperandStride / es) / kVocabTile;
-    const uint64_t pieces = (tiles + most - 1) / most;
-    return (tiles + pieces - 1) / pieces * kVocabTile;
-}
+constexpr uint64_t kVocabTile = 256;   // of the vocabulary's pieces: whole ones of any tile
 
 // Tiles of the products, m x n: the large one keeps the matrix cores busiest,
 // the smaller ones give few rows or columns more workgroups.
@@ -115,6 +100,48 @@ inline CrossTile forward_tile(uint64_t rows, uint64_t vocab, uint64_t es, int nr
 constexpr uint64_t kMostRows = 1ull << 28;
 inline uint64_t launch_vocab(CrossTile t, uint64_t rows, int nranks) {
     return most_blocks(t) / (tiles_in(1, rows, t) * nranks) * tile_m(t);
+}
+
+// The backward pass works the vocabulary off in pieces of whole tiles, so that
+// what it keeps of dz is bounded whatever the vocabulary is: kPieceBytes in all,
+// or kLeastPiece columns.  Every piece more reads and writes dx's float32 sums
+// once more.  ms with 128 / 256 / 512 / 1,024 MiB, bf16: 2 x 4,096 rows of 4,096
+// against 65,536 10.5 / 10.45 / 10.45 / 10.4, 8 x 2,048 rows of 768 against
+// 50,257 4.41 / 4.34 / 4.27 / 4.05, 4 x 4,096 of 2,048 against 32,768 5.78 /
+// 5.63 / 5.56 / 5.56.
+constexpr uint64_t kPieceBytes = 512ull << 20, kLeastPiece = 2048;
+// A weight that is copied is worked off in pieces in both passes: of kCopyBytes
+// (the backward pass: kCopyBytesBackward) of all ranks, or as many rows as give
+// each compute unit a tile (and the backward pass kLeastPiece).  us with 64 / 128 /
+// 256 / 512 MiB, bf16, forward and backward: 16 rows of 4,095 against 65,536 340 /
+// 293 / 311 / 333 and 790 / 735 / 698 / 755, 2 x 1,024 of 4,095 against 65,536
+// 1,670 / 1,210 / 1,280 / 1,270 and 4,200 / 3,580 / 3,570 / 3,530, 2 x 4,096 of
+// 4,095 against 65,536 3,590 / 3,560 / 3,610 / 3,590 and 11,640 / 11,170 / 11,080 /
+// 11,090: what is copied comes back from the last-level cache.
+constexpr uint64_t kCopyBytes = 128ull << 20, kCopyBytesBackward = 256ull << 20;
+inline uint64_t even_pieces(uint64_t vocab, uint64_t most) {   // whole tiles
+    const uint64_t tiles = (vocab + kVocabTile - 1) / kVocabTile, each = std::max<uint64_t>(1, most / kVocabTile);
+    const uint64_t pieces = (tiles + each - 1) / each;
+    return (tiles + pieces - 1) / pieces * kVocabTile;
+}
+// Rows of the weight that give each compute unit a tile.
+inline uint64_t one_turn(uint64_t rows, uint64_t vocab, uint64_t es, int nranks) {
+    const CrossTile t = pick_tile(vocab, rows, nranks, es == 4);
+    const uint64_t beside = std::max<uint64_t>(1, tiles_in(1, rows, t) * nranks);
+    return ((kUnits + beside - 1) / beside * tile_m(t) + kVocabTile - 1) / kVocabTile * kVocabTile;
+}
+// copy_bytes: of a copied row of the weight; 0: read where it lies.
+inline uint64_t forward_piece(uint64_t rows, uint64_t vocab, uint64_t es, uint64_t copy_bytes, int nranks) {
+    if (copy_bytes == 0) return even_pieces(vocab, vocab + kVocabTile);
+    return even_pieces(vocab, std::max(one_turn(rows, vocab, es, nranks), kCopyBytes / (copy_bytes * nranks)));
+}
+inline uint64_t piece_of(uint64_t rows, uint64_t vocab, uint64_t es, uint64_t copy_bytes, int nranks) {
+    const uint64_t row_bytes = std::max<uint64_t>(1, rows) * nranks * es;
+    uint64_t most = std::min(std::max(kLeastPiece, kPieceBytes / row_bytes), kMostOperandStride / es);
+    if (copy_bytes != 0)
+        most = std::min(most, std::max({kLeastPiece, one_turn(rows, vocab, es, nranks),
+                                        kCopyBytesBackward / (copy_bytes * nranks)}));
+    return even_pieces(vocab, most);
 }
 
 // A rank's row of a launch, in the order of the rows that take part.

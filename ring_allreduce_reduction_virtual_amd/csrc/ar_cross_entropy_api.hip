@@ -25,14 +25,17 @@ ar_result_t check_sizes(size_t rows, size_t vocab, size_t cols, ar_dtype_t dtype
     if (vocab == 0) return fail_with(AR_ERR_INVALID_ARGUMENT, "a vocabulary of 0");
     const int n = std::min(nranks, kCrossRanks);
     bool fits = rows <= kMaxTokens && vocab <= kMaxVocab && cols <= kMaxWidth && rows_fit(rows, n);
-    if (fits && backward) {   // its launches; the forward pass's are cut to fit
-        const uint64_t es = float_size(dtype), piece = piece_of(rows, vocab, es, n);
+    if (fits && backward) {   // its launches, with the weight as it lies and copied; the forward pass's are cut to fit
+        const uint64_t es = float_size(dtype);
         const bool wide = es == 4;
-        const DxShape dx = dx_shape(rows, cols, piece, es, n);
-        fits = fits_launch(pick_tile(piece, rows, n, wide), piece, rows, n) &&
-               fits_launch(dx.tile, cols, rows, static_cast<uint64_t>(n) * dx.splits) &&
-               fits_launch(pick_tile(cols, piece, n, wide), cols, piece, n) &&
-               fits_launch(pick_tile(cols, vocab % piece, n, wide), cols, vocab % piece, n);
+        for (const uint64_t copy_bytes : {uint64_t{0}, padded_cols(cols, es) * es}) {
+            const uint64_t piece = piece_of(rows, vocab, es, copy_bytes, n);
+            const DxShape dx = dx_shape(rows, cols, piece, es, n);
+            fits = fits && fits_launch(pick_tile(piece, rows, n, wide), piece, rows, n) &&
+                   fits_launch(dx.tile, cols, rows, static_cast<uint64_t>(n) * dx.splits) &&
+                   fits_launch(pick_tile(cols, piece, n, wide), cols, piece, n) &&
+                   fits_launch(pick_tile(cols, vocab % piece, n, wide), cols, vocab % piece, n);
+        }
     }
     if (!fits)
         return fail_with(AR_ERR_INVALID_ARGUMENT, "%llu rows of %llu columns against a vocabulary of %llu are too large",
@@ -59,9 +62,11 @@ struct Layout {
     }
     Layout(uint64_t rows, uint64_t vocab, uint64_t cols, ar_dtype_t dtype, int nranks, bool backward, bool aligned) {
         const uint64_t n = static_cast<uint64_t>(std::min(nranks, kCrossRanks)), es = float_size(dtype);
-        piece = piece_of(rows, vocab, es, static_cast<int>(n));
         padded = padded_cols(cols, es);
         const bool copies = !aligned && !in_words(rows, es, backward);
+        const uint64_t copy_bytes = copies ? padded * es : 0;
+        piece = backward ? piece_of(rows, vocab, es, copy_bytes, static_cast<int>(n))
+                         : forward_piece(rows, vocab, es, copy_bytes, static_cast<int>(n));
         if (backward || copies) x = take(n * rows * padded * es);
         if (copies) weight = take(n * std::min(piece, vocab) * padded * es);
         if (backward) {
@@ -131,15 +136,18 @@ size_t ar_cross_entropy_workspace_bytes(size_t rows, size_t vocab, size_t cols, 
                                         int backward) {
     set_error_detail("");
     if (check_sizes(rows, vocab, cols, dtype, nranks, backward != 0) != AR_SUCCESS) return static_cast<size_t>(-1);
-    return Layout(rows, vocab, cols, dtype, nranks, backward != 0, false).all;
+    // smaller pieces can need less than none to copy
+    return std::max(Layout(rows, vocab, cols, dtype, nranks, backward != 0, false).all,
+                    Layout(rows, vocab, cols, dtype, nranks, backward != 0, true).all);
 }
 
 size_t ar_cross_entropy_aligned_workspace_bytes(size_t rows, size_t vocab, size_t cols, ar_dtype_t dtype, int nranks,
                                                 int backward) {
     set_error_detail("");
     if (check_sizes(rows, vocab, cols, dtype, nranks, backward != 0) != AR_SUCCESS) return static_cast<size_t>(-1);
-    const bool can_be = cols * float_size(dtype) % kOperandBytes == 0;
-    return Layout(rows, vocab, cols, dtype, nranks, backward != 0, can_be).all;
+    if (cols * float_size(dtype) % kOperandBytes != 0)   // they cannot be
+        return ar_cross_entropy_workspace_bytes(rows, vocab, cols, dtype, nranks, backward);
+    return Layout(rows, vocab, cols, dtype, nranks, backward != 0, true).all;
 }
 
 ar_result_t ar_cross_entropy(const void* const* x, const void* const* weight, const void* const* targets,

@@ -320,3 +320,20 @@ def test_cross_entropy_workspace_without_copies(lib, dt, rows, vocab, cols, n):
     assert (lib.ar_cross_entropy_aligned_workspace_bytes(rows, vocab, cols + 1, dt, n, 0)
             == lib.ar_cross_entropy_workspace_bytes(rows, vocab, cols + 1, dt, n, 0))
     assert lib.ar_cross_entropy_aligned_workspace_bytes(rows, 0, cols, dt, n, 1) == NONE
+
+
+@pytest.mark.parametrize("dt", [F32, BF16])
+@pytest.mark.parametrize("n,rows,vocab,cols", [(1, 80, 131072, 4095), (8, 80, 131072, 8191), (32, 100, 131072, 8191),
+                                               (2, 4096, 65536, 4095), (1, 4096, 1 << 22, 2047), (33, 70, 1 << 20, 1023)])
+def test_cross_entropy_copies_are_bounded(lib, dt, n, rows, vocab, cols):
+    """Of a weight that is copied a piece is held at a time: 128 MiB of all ranks (backward 256, or 2,048 rows of each),
+    or what gives 256 compute units a tile of at most 256 rows; x is copied whole."""
+    es, ranks = 4 if dt == F32 else 2, min(n, 32)
+    row = -(-cols * es // 16) * 16
+    turn = 256 * (256 + ranks) * row
+    forward = lib.ar_cross_entropy_workspace_bytes(rows, vocab, cols, dt, n, 0)
+    back = lib.ar_cross_entropy_workspace_bytes(rows, vocab, cols, dt, n, 1)
+    assert forward <= ranks * rows * (row + -(-vocab // 64) * 8 + 4) + max(128 << 20, turn) + ranks * 256 * row + 4096
+    dz = min(max(512 << 20, ranks * rows * 2048 * es), ranks * rows * (vocab + 256) * es) + ranks * rows * 256 * es
+    weight = max(256 << 20, turn, ranks * 2048 * row) + ranks * 256 * row
+    assert back <= dz + weight + ranks * rows * (row + 64 * (cols + 4) * 4 + 64) + 4096
