@@ -717,8 +717,10 @@ ar_result_t ar_embedding(const void* const* tokens, const void* const* table, vo
 
 /* Its gradient: row v of dtable[r] (table_dtype, dtable_stride apart) receives
  * scale * the sum of the rows of dy[r] whose token is v, added in float32 in an
- * order that depends on the tokens alone (they are sorted by token, then by
- * place), and rounded once.  Rows that no token names become 0.  With
+ * order that depends on the tokens, rows and nranks alone (places are sorted by
+ * token and added in groups, whose size goes by rows * nranks), and rounded
+ * once: the same bits in every run, and on every rank of a call that has the
+ * same tokens and dy.  Rows that no token names become 0.  With
  * `accumulate` the sum is added to what the row holds (before the rounding),
  * and rows that no token names are not touched: a table that is also the
  * head's weight gets both gradients in one buffer.  Tokens outside [0, vocab)

@@ -38,7 +38,8 @@ constexpr int kDigits = 1 << kDigitBits;
 
 // Places of the sorted order that one group of threads adds up (see the
 // kernel): few, so that few tokens fill the GPU, or more, which leave fewer
-// partial sums.
+// partial sums.  The choice goes by all ranks' places, so that the grouping of a
+// token's sum does too.
 constexpr uint64_t kFewPlaces = 16384;
 inline uint64_t sum_chunk(uint64_t rows, int nranks) { return rows * nranks <= kFewPlaces ? 8 : 32; }
 

@@ -368,3 +368,16 @@ def test_one_token_of_a_million_places(ar, rows):
     off = (32 + 256 + 256 + rows / 32 / 65536 + 4) * U32 * want
     assert ((got[3].double() - want).abs() <= off).all(), ((got[3].double() - want) / want / U32).tolist()
     assert (got[[0, 1, 2, 4]] == 0).all()
+
+
+@pytest.mark.parametrize("n", [4, 5])
+def test_bits_on_every_rank(ar, n):
+    """4,096 places on each of 4 ranks, the most that are added in groups of 8, and of 5 (groups of 32): ranks with the
+    same tokens and dy have the same bits, in every run; both groupings stay within the sum's roundings."""
+    torch = _torch()
+    rng = np.random.default_rng(7)
+    tokens = tokens_of([(rng.random(4096) ** 3 * 60).astype(int)]) * n
+    dys = rows_of(rng, 1, 4096, 40, "f32") * n
+    outs = check_backward(ar, dys, tokens, 60, "f32", "f32", 1.5)
+    again = ar.ar_embedding_backward(dys, tokens, 60, scale=1.5)
+    assert all(torch.equal(o, outs[0]) for o in outs + again)
