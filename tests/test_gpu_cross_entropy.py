@@ -595,3 +595,107 @@ def test_few_rows_take_little_memory(ar, dtype):
                          device="cuda")
         again = ar.ar_cross_entropy(xs, weights, targets, workspace=ws)
         assert torch.equal(again[0][0], losses[0]) and torch.equal(again[1][0], lses[0])
+
+
+def random_case(n, rows, cols, vocab, dtype, seed):
+    """check()'s inputs, made on the GPU: (xs, weights, targets, dlosses)."""
+    torch = _torch()
+    gen = torch.Generator(device="cuda").manual_seed(seed)
+    dt = torch_dtype(dtype)
+    xs = [torch.randn(rows, cols, device="cuda", generator=gen).to(dt) for _ in range(n)]
+    weights = [(torch.randn(vocab, cols, device="cuda", generator=gen) * (1.5 / math.sqrt(cols))).to(dt) for _ in range(n)]
+    targets = []
+    for _ in range(n):
+        t = torch.randint(0, vocab, (rows,), device="cuda", generator=gen)
+        targets.append(torch.where(torch.rand(rows, device="cuda", generator=gen) < 0.2, IGNORE, t))
+    return xs, weights, targets, [torch.rand(rows, device="cuda", generator=gen) / rows for _ in range(n)]
+
+
+def check_large(ar, n, rows, cols, vocab, dtype):
+    """Both passes against float64 on the GPU, row by row.
+
+    lse and loss: check_forward()'s bound.  Gradients: the 2-norm of a row's error, relative to the row's.  What goes
+    into it is independent from term to term and adds up as its root of squares: of 16-bit dz a rounding (UNIT at most)
+    and one of the result; for float32 p's error, of some sqrt(cols) roundings of logits of a few units and 4 of
+    arguments up to 16 (16 sqrt(cols) U32 hold both), and a sum's roundings, sqrt(depth) U32 of partial sums no larger
+    than the result.  All rows together 2 times that, and a row (its largest of some thousand) 4 times: a step of the
+    sum left out, 32 to 128 of its terms, is sqrt(32 / depth), 3% and more.
+    """
+    torch = _torch()
+    xs, weights, targets, dlosses = random_case(n, rows, cols, vocab, dtype, rows + cols + vocab)
+    losses, lses = ar.ar_cross_entropy(xs, weights, targets, ignore_index=IGNORE)
+    dxs, dws = ar.ar_cross_entropy_backward(dlosses, xs, weights, targets, lses, ignore_index=IGNORE)
+    for x, w, t, g, loss, lse, dx, dw in zip(xs, weights, targets, dlosses, losses, lses, dxs, dws):
+        x, w, kept = x.double(), w.double(), t != IGNORE
+        z = x @ w.t()
+        want = z.logsumexp(1)
+        spread = (z - z.amax(1, keepdim=True)).abs()
+        off = (cols + 1) * U32 * (x.abs() @ w.abs().t())
+        at = t.clamp(min=0)[:, None]
+        lse_off = ((torch.exp(z - want[:, None]) * (off + 4 * (spread + off) * U32)).sum(1) * 1.01 + EXP
+                   + (vocab / 128 + 300) * U32 + 8 * U32 * (want.abs() + z.abs().amax(1) + 1))
+        assert ((lse - want).abs() <= lse_off).all()
+        want_loss = want - z.gather(1, at)[:, 0]
+        loss_off = lse_off + off.gather(1, at)[:, 0] + 2 * U32 * want_loss.abs()
+        assert ((loss - want_loss).abs() <= loss_off)[kept].all() and (loss[~kept] == 0).all()
+        del off, spread
+        dz = torch.exp(z.sub_(lse.double()[:, None]))
+        dz[kept, t[kept]] -= 1
+        dz *= (g.double() * kept)[:, None]
+        assert (dx[~kept] == 0).all()
+        for got, want, depth, other in ((dx, dz @ w, vocab, w), (dw, dz.t() @ x, rows, x)):
+            # below the normal numbers a rounding is no longer relative: the result's moves each of a row's `cols` elements
+            # by at most TINY, their 2-norm by sqrt(cols) TINY (weights g near 0 make such rows of binary16); dz's moves each
+            # of its elements by TINY times the largest |g| / 2^13 (binary16), and the row by that times the other
+            # factor's 2-norm
+            tiny = math.sqrt(cols) * TINY[dtype]
+            if dtype == "f16":
+                tiny = tiny + float(g[kept].max()) * 2.0 ** -13 * TINY["f16"] * float(other.norm())
+            bound = 2 * UNIT[dtype] if dtype != "f32" else (math.sqrt(depth) + 16 * math.sqrt(cols)) * U32
+            away, size = (got.double() - want).norm(dim=1), want.norm(dim=1)
+            assert away.norm() <= 2 * bound * size.norm() + math.sqrt(len(got)) * tiny, float(away.norm() / size.norm() / bound)
+            # a word that is no row's target has small terms only, whose rounding in a binary16 of 2^13 for the largest |g|
+            # may be a subnormal's: what is far below the others counts with them
+            size = size.clamp(min=1e-3 * float(size.max()))
+            assert (away <= 4 * bound * size + tiny)[kept if got is dx else slice(None)].all(), float((away / size).max() / bound)
+
+
+@pytest.mark.parametrize("n,rows,cols,vocab", [(3, 520, 100, 8200), (3, 2060, 100, 5000), (1, 3000, 100, 5000),
+                                               (2, 150, 1500, 5000), (2, 2000, 390, 33000)])
+def test_every_tile_in_float32(ar, n, rows, cols, vocab):
+    """Sizes that the larger three tiles are picked for in each of the four products, all of several steps of the sum: the
+    largest for the loss and dz in the third, for dweight in the fourth, for dx in the last."""
+    check_large(ar, n, rows, cols, vocab, "f32")
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("n,rows,cols,vocab", [(1, 260, 100, 8200), (3, 520, 130, 5000), (2, 150, 130, 16400),
+                                               (2, 4100, 1000, 300), (1, 1500, 520, 33000), (1, 4096, 260, 16400)])
+def test_every_tile_in_16_bits(ar, dtype, n, rows, cols, vocab):
+    """The same: the largest for the loss and dz in the second and the last two, for dweight in the third and fifth, for dx
+    in the fourth and last."""
+    check_large(ar, n, rows, cols, vocab, dtype)
+
+
+@pytest.mark.parametrize("large", ["weights", "rows"])
+def test_small_gradients_keep_their_bits_in_binary16(ar, large):
+    """g of 1e-7 against the float64 oracle, dx where the weights are large and dweight where x is, so that the results are
+    normal binary16 numbers: the softmax's part of dz, 1e-7 of some 1/2,000 each, is below all of binary16 unless it is
+    held relative to g.  Every third row has the target that its logits favour, so that its gradient is made of small
+    terms only."""
+    torch = _torch()
+    rng = np.random.default_rng(17)
+    up = 2000.0 if large == "weights" else 1 / 2000.0
+    xs, weights = rows_of(rng, 1, 150, 64, "f16", 0, 1.2 / up), rows_of(rng, 1, 2000, 64, "f16", 0, 0.2 * up)
+    targets = targets_of(rng, 1, 150, 2000)
+    best = (xs[0].double() @ weights[0].double().t()).argmax(1)
+    targets[0][::3] = best[::3]
+    _, lses = check_forward(ar, xs, weights, targets)
+    g = [torch.full((150,), 1e-7, device="cuda")]
+    (dx,), (dw,) = check_backward(ar, xs, weights, targets, lses, g, "f16")
+    x, w, t = f64(xs[0]), f64(weights[0]), targets[0].cpu().numpy()
+    want_dx, want_dw, _ = oracle.cross_entropy_backward(f64(g[0]), x, w, t, f64(lses[0]), IGNORE)
+    got, want = (f64(dx), want_dx) if large == "weights" else (f64(dw), want_dw)
+    # a rounding of dz and one of the result, the subnormals' step for the result's small elements
+    size = np.sqrt(np.maximum((want ** 2).sum(1), want.shape[1] * (2.0 ** 13 * TINY["f16"]) ** 2))
+    assert (np.sqrt(((got - want) ** 2).sum(1)) <= 2 * UNIT["f16"] * size).all()
