@@ -28,10 +28,10 @@ ar_result_t check_sizes(size_t rows, size_t vocab, size_t cols, ar_dtype_t dtype
     if (fits && backward) {   // its launches, with the weight as it lies and copied; the forward pass's are cut to fit
         const uint64_t es = float_size(dtype);
         const bool wide = es == 4;
-        for (const uint64_t copy_bytes : {uint64_t{0}, padded_cols(cols, es) * es}) {
-            const uint64_t piece = piece_of(rows, vocab, es, copy_bytes, n);
+        for (uint64_t piece = piece_of(rows, vocab, es, 0, n), checked = 0; fits && piece != checked;
+             checked = piece, piece = piece_of(rows, vocab, es, padded_cols(cols, es) * es, n)) {
             const DxShape dx = dx_shape(rows, cols, piece, es, n);
-            fits = fits && fits_launch(pick_tile(piece, rows, n, wide), piece, rows, n) &&
+            fits = fits_launch(pick_tile(piece, rows, n, wide), piece, rows, n) &&
                    fits_launch(dx.tile, cols, rows, static_cast<uint64_t>(n) * dx.splits) &&
                    fits_launch(pick_tile(cols, piece, n, wide), cols, piece, n) &&
                    fits_launch(pick_tile(cols, vocab % piece, n, wide), cols, vocab % piece, n);

@@ -148,8 +148,12 @@ def ar_cross_entropy_workspace_bytes(rows: int, vocab: int, cols: int, dtype: st
 
 def _aligned(addresses, n, stride, cols, es):
     """Whether the ranks' operands need no copy: rows on 16 bytes, of whole 16 bytes and at most 8 MiB apart."""
-    return ((stride * es | cols * es) % 16 == 0 and stride * es <= 1 << 23
-            and all((addresses[r] or 0) % 16 == 0 for r in range(n)))
+    if (stride * es | cols * es) & 15 or stride * es > 1 << 23:
+        return False
+    for a in addresses[:n]:
+        if a and a & 15:
+            return False
+    return True
 
 
 def _flat_floats(tensors, n, dev, index, rows, what):
@@ -196,7 +200,8 @@ def ar_cross_entropy(xs, weights, targets, losses=None, lses=None, ignore_index:
         losses, lp = made if losses is None else (losses, _flat_floats(losses, n, dev, index, rows, "losses"))
         lses, sp = made if lses is None else (lses, _flat_floats(lses, n, dev, index, rows, "lses"))
     if workspace is None:
-        aligned = all(_aligned(p, n, s, shape[2], x0.element_size()) for p, s in zip(inputs, strides))
+        es = x0.element_size()
+        aligned = (_aligned(inputs[0], n, strides[0], shape[2], es) and _aligned(inputs[1], n, strides[1], shape[2], es))
         workspace = _scratch(ar_cross_entropy_workspace_bytes(*shape, name, n, False, aligned), None, dev, stream)
     with _on_device(dev):
         wp, wb = _ws(workspace, dev)
