@@ -33,6 +33,7 @@ from .binding import (  # noqa: F401
 from .model import (  # noqa: F401
     PackedRows,
     ar_cross_entropy,
+    ar_cross_entropy_aligned_workspace_bytes,
     ar_cross_entropy_backward,
     ar_cross_entropy_workspace_bytes,
     ar_embedding,
@@ -75,5 +76,6 @@ __all__ = [
     "ar_layer_norm", "ar_layer_norm_backward", "ar_layer_norm_workspace_bytes",
     "ar_embedding", "ar_embedding_backward", "ar_embedding_workspace_bytes",
     "ar_cross_entropy", "ar_cross_entropy_backward", "ar_cross_entropy_workspace_bytes",
+    "ar_cross_entropy_aligned_workspace_bytes",
     "PackedRows", "ar_pack_activations", "ar_unpack_activations", "ar_layer_norm_backward_packed",
 ]

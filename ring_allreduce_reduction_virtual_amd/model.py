@@ -135,15 +135,28 @@ def ar_embedding_backward(dys, tokens, vocab=None, dtables=None, scale: float = 
 # cross entropy
 # --------------------------------------------------------------------------
 
-def ar_cross_entropy_workspace_bytes(rows: int, vocab: int, cols: int, dtype: str, nranks: int,
-                                     backward: bool = False, aligned: bool = False) -> int:
-    """Enough for any operands; with `aligned`, for those whose rows lie on 16 bytes (include/ar.h), which need no copies."""
-    name = "ar_cross_entropy_aligned_workspace_bytes" if aligned else "ar_cross_entropy_workspace_bytes"
-    v = getattr(_lib.lib(), name)(rows, vocab, cols, _lib.DTYPES[dtype], nranks, 1 if backward else 0)
+def _cross_entropy_bytes(call, rows, vocab, cols, dtype, nranks, backward):
+    v = getattr(_lib.lib(), call)(rows, vocab, cols, _lib.DTYPES[dtype], nranks, 1 if backward else 0)
     if v == ctypes.c_size_t(-1).value:
-        raise ValueError("invalid arguments for ar_cross_entropy_workspace_bytes: "
-                         + _lib.lib().ar_get_last_error_detail().decode())
+        raise ValueError(f"invalid arguments for {call}: " + _lib.lib().ar_get_last_error_detail().decode())
     return v
+
+
+def ar_cross_entropy_workspace_bytes(rows: int, vocab: int, cols: int, dtype: str, nranks: int,
+                                     backward: bool = False) -> int:
+    """Enough for any operands."""
+    return _cross_entropy_bytes("ar_cross_entropy_workspace_bytes", rows, vocab, cols, dtype, nranks, backward)
+
+
+def ar_cross_entropy_aligned_workspace_bytes(rows: int, vocab: int, cols: int, dtype: str, nranks: int,
+                                             backward: bool = False) -> int:
+    """What operands need whose rows lie on 16 bytes (include/ar.h), so that none is copied."""
+    return _cross_entropy_bytes("ar_cross_entropy_aligned_workspace_bytes", rows, vocab, cols, dtype, nranks, backward)
+
+
+def _cross_entropy_scratch(shape, name, n, backward, aligned, dev, stream):
+    need = ar_cross_entropy_aligned_workspace_bytes if aligned else ar_cross_entropy_workspace_bytes
+    return _scratch(need(*shape, name, n, backward), None, dev, stream)
 
 
 def _aligned(addresses, n, stride, cols, es):
@@ -202,7 +215,7 @@ def ar_cross_entropy(xs, weights, targets, losses=None, lses=None, ignore_index:
     if workspace is None:
         es = x0.element_size()
         aligned = (_aligned(inputs[0], n, strides[0], shape[2], es) and _aligned(inputs[1], n, strides[1], shape[2], es))
-        workspace = _scratch(ar_cross_entropy_workspace_bytes(*shape, name, n, False, aligned), None, dev, stream)
+        workspace = _cross_entropy_scratch(shape, name, n, False, aligned, dev, stream)
     with _on_device(dev):
         wp, wb = _ws(workspace, dev)
         rc = _lib.lib().ar_cross_entropy(*inputs, lp, sp, *shape, *strides, index_type, ignore_index,
@@ -236,7 +249,7 @@ def ar_cross_entropy_backward(dlosses, xs, weights, targets, lses, dxs=None, dwe
         dweights, gw, w_stride = _out_rows(dweights, (vocab, cols), n, dt, dev, index, "dweights", stream)
     if workspace is None:
         aligned = _aligned(inputs[1], n, strides[1], cols, x0.element_size())
-        workspace = _scratch(ar_cross_entropy_workspace_bytes(*shape, name, n, True, aligned), None, dev, stream)
+        workspace = _cross_entropy_scratch(shape, name, n, True, aligned, dev, stream)
     with _on_device(dev):
         wp, wb = _ws(workspace, dev)
         rc = _lib.lib().ar_cross_entropy_backward(dp, *inputs, sp, gx, gw, *shape, *strides, x_stride, w_stride,

@@ -590,9 +590,8 @@ def test_few_rows_take_little_memory(ar, dtype):
     # forward: 8 bytes per row and 64 words; backward: dz, 64 splits of dx's sums and the rest, which is x's size
     assert most["forward"] <= logits / 16 and most["backward"] <= 2 * logits + 64 * 16 * 1024 * 4
     # a workspace of the size for any operands serves as well
-    for aligned in (False, True):
-        ws = torch.empty(ar.ar_cross_entropy_workspace_bytes(16, 64000, 1024, dtype, 1, False, aligned), dtype=torch.uint8,
-                         device="cuda")
+    for need in (ar.ar_cross_entropy_workspace_bytes, ar.ar_cross_entropy_aligned_workspace_bytes):
+        ws = torch.empty(need(16, 64000, 1024, dtype, 1), dtype=torch.uint8, device="cuda")
         again = ar.ar_cross_entropy(xs, weights, targets, workspace=ws)
         assert torch.equal(again[0][0], losses[0]) and torch.equal(again[1][0], lses[0])
 
