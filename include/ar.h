@@ -744,13 +744,13 @@ size_t ar_embedding_workspace_bytes(size_t rows, size_t vocab, size_t cols, int 
  * difference, not from the rounded lse: beside large logits a small one stays.
  * A target equal to ignore_index gives loss 0; any other outside [0, vocab)
  * gives NaN.  A NaN or +infinity among a row's logits makes its lse and loss
- * NaN.  The vocabulary is worked off in
- * pieces: products of 16-bit elements are summed in float32 by the matrix
- * cores (float32 ones too), maxima and sums of exponentials kept per piece and
- * joined in order.  Outputs overlap nothing else; ranks may share one weight.
- * rows == 0 is a successful no-op; cols == 0 means logits of 0.
- * `workspace`: at least ar_cross_entropy_workspace_bytes(...) bytes (or fewer,
- * see there) of device memory, 16-byte aligned.  vocab of 1 to 2^31 - 1, cols up to 2^20, and up to
+ * NaN.  The vocabulary is worked off in pieces: products of 16-bit elements are
+ * summed in float32 by the matrix cores (float32 ones too), maxima and sums of
+ * exponentials kept per piece and joined in order.  Outputs overlap nothing
+ * else; ranks may share one weight.  rows == 0 is a successful no-op; cols == 0
+ * means logits of 0.  `workspace`: at least
+ * ar_cross_entropy_workspace_bytes(...) bytes (or fewer, see there) of device
+ * memory, 16-byte aligned.  vocab of 1 to 2^31 - 1, cols up to 2^20, and up to
  * 2^28 rows (of 32 ranks together, each rank's counted in whole 256); more is
  * refused. */
 ar_result_t ar_cross_entropy(const void* const* x, const void* const* weight, const void* const* targets,

@@ -95,9 +95,11 @@ inline CrossTile forward_tile(uint64_t rows, uint64_t vocab, uint64_t es, int nr
     return pick_tile(vocab, rows, nranks, es == 4);
 }
 // Columns of the vocabulary, whole tiles, that one forward launch has room for:
-// at least one tile while the ranks of a launch have no more than kMostRows rows
-// (2^31 / tile_n(tile) workgroups at most).
+// at least one tile while the ranks of a launch have no more than kMostRows rows.
 constexpr uint64_t kMostRows = 1ull << 28;
+static_assert(kMostRows / tile_n(CrossTile::kTiny) <= most_blocks(CrossTile::kTiny) &&
+                  kMostRows / tile_n(CrossTile::kMedium) <= most_blocks(CrossTile::kMedium),
+              "a tile for every row: fewest rows a workgroup of 256 threads, and of 512");
 inline uint64_t launch_vocab(CrossTile t, uint64_t rows, int nranks) {
     return most_blocks(t) / (tiles_in(1, rows, t) * nranks) * tile_m(t);
 }

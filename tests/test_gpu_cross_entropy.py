@@ -698,3 +698,40 @@ def test_small_gradients_keep_their_bits_in_binary16(ar, large):
     # a rounding of dz and one of the result, the subnormals' step for the result's small elements
     size = np.sqrt(np.maximum((want ** 2).sum(1), want.shape[1] * (2.0 ** 13 * TINY["f16"]) ** 2))
     assert (np.sqrt(((got - want) ** 2).sum(1)) <= 2 * UNIT["f16"] * size).all()
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
+def test_copies_in_pieces(ar, dtype):
+    """Rows that do not lie on 16 bytes, of a weight whose copy takes several pieces in both passes, the last one short."""
+    check_large(ar, 1, 300, 1023, 160001, dtype)
+
+
+def test_copied_forward_has_the_same_bits(ar):
+    """The pieces of a copied weight leave every tile as it is: the bits of the same values on 16 bytes."""
+    torch = _torch()
+    (x,), (w,), (t,), _ = random_case(1, 300, 1016, 100000, "bf16", 18)
+    flat = torch.empty(w.numel() + 1, dtype=w.dtype, device="cuda")
+    off = flat[1:].view(w.shape)
+    off.copy_(w)
+    for a, b in zip(ar.ar_cross_entropy([x], [w], [t]), ar.ar_cross_entropy([x], [off], [t])):
+        assert torch.equal(a[0], b[0])
+
+
+@pytest.mark.parametrize("odd", [0, 33])
+def test_one_rank_of_many_off_16_bytes(ar, odd):
+    """35 ranks, two launches: only the launch of the rank whose weight and x do not start on 16 bytes copies, and all
+    have the same bits as without it."""
+    torch = _torch()
+    rng = np.random.default_rng(19)
+    n = 35
+    xs, weights = rows_of(rng, n, 33, 24, "bf16"), rows_of(rng, n, 700, 24, "bf16")
+    targets = targets_of(rng, n, 33, 700)
+    losses, lses = ar.ar_cross_entropy(xs, weights, targets)
+    dxs, dws = ar.ar_cross_entropy_backward(None, xs, weights, targets, lses)
+    for group in (xs, weights):
+        flat = torch.empty(group[odd].numel() + 1, dtype=torch.bfloat16, device="cuda")
+        group[odd] = flat[1:].view(group[odd].shape).copy_(group[odd])
+    again = ar.ar_cross_entropy(xs, weights, targets)
+    back = ar.ar_cross_entropy_backward(None, xs, weights, targets, lses)
+    for a, b in zip((losses, lses, dxs, dws), again + back):
+        assert all(torch.equal(p, q) for p, q in zip(a, b))
